@@ -422,3 +422,17 @@ def make_desc(name, elem_bits, rows, cols, split, tp, shard_offset, recv_offset,
     d.recv_layout, d.recv_group, d.recv_slot = recv_layout, recv_group, recv_slot
     d.recv_offset = recv_offset
     return d
+
+
+# The operators around a refit need torch, which the calls above import only
+# when they use it: they are looked up in .ops at their first use.
+_OPS = ("Nvfp4", "nvfp4_quantize", "nvfp4_matmul", "nvfp4_linear", "policy_loss", "token_logprobs")
+
+
+def __getattr__(name):
+    if name in _OPS:
+        from . import ops
+        for n in _OPS:
+            globals()[n] = getattr(ops, n)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
