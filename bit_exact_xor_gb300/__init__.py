@@ -426,7 +426,8 @@ def make_desc(name, elem_bits, rows, cols, split, tp, shard_offset, recv_offset,
 
 # The operators around a refit need torch, which the calls above import only
 # when they use it: they are looked up in .ops at their first use.
-_OPS = ("Nvfp4", "nvfp4_quantize", "nvfp4_matmul", "nvfp4_linear", "policy_loss", "token_logprobs")
+_OPS = ("Nvfp4", "nvfp4_quantize", "nvfp4_matmul", "nvfp4_linear", "policy_loss", "token_logprobs",
+        "ops_status")
 
 
 def __getattr__(name):

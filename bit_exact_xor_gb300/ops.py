@@ -19,7 +19,8 @@ SCALE_GIVEN, SCALE_TENSOR, SCALE_ROW = 0, 1, 2
 MAX_EXPERTS = 1024
 DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
-OP_EXPORTS = ["dcr_nvfp4_quantize", "dcr_nvfp4_matmul", "dcr_policy_loss", "dcr_token_logprobs"]
+OP_EXPORTS = ["dcr_nvfp4_quantize", "dcr_nvfp4_matmul", "dcr_policy_loss", "dcr_token_logprobs",
+              "dcr_ops_status"]
 
 
 class Nvfp4(NamedTuple):
@@ -54,6 +55,7 @@ def _lib():
         L.dcr_nvfp4_matmul.argtypes = [P(_Nvfp4), P(_Nvfp4), U64, U64, U64, VP, U32, VP, U32, U64, VP]
         L.dcr_policy_loss.argtypes = [VP, U32, U64, U64, U64, VP, VP, VP, VP, VP, P(PolicyOpts), VP, VP, VP, VP, U64, VP]
         L.dcr_token_logprobs.argtypes = [VP, U32, U64, U64, U64, VP, ctypes.c_float, VP, VP]
+        L.dcr_ops_status.argtypes = [VP]
         _ops = L
     return _ops
 
@@ -248,3 +250,9 @@ def token_logprobs(logits, tokens, temperature=1.0, out=None):
     check(_lib().dcr_token_logprobs(logits.data_ptr(), DTYPES[logits.dtype], rows, vocab, stride, pt, temperature,
                                     out.data_ptr(), _stream()))
     return out
+
+
+def ops_status(stream=None):
+    """dcr_ops_status: waits for the stream and raises DcrError (TIMEOUT) if an
+    operator gave up a wait on the device since the last call."""
+    check(_lib().dcr_ops_status(_stream() if stream is None else getattr(stream, "cuda_stream", stream)))

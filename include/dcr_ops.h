@@ -102,6 +102,12 @@ int dcr_policy_loss(const void* logits, uint32_t dtype, uint64_t rows, uint64_t 
 int dcr_token_logprobs(const void* logits, uint32_t dtype, uint64_t rows, uint64_t vocab, uint64_t row_stride,
                        const int64_t* tokens, float temperature, float* logp, void* stream);
 
+/* Waits for `stream` and reports whether any operator on the current device
+ * gave up a wait since the last report: every wait inside a kernel is
+ * bounded (two seconds), after which the kernel ends with its output
+ * incomplete.  DCR_OK, DCR_ERR_TIMEOUT or DCR_ERR_CUDA. */
+int dcr_ops_status(void* stream);
+
 #ifdef __cplusplus
 }
 #endif
