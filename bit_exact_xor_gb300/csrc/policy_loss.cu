@@ -1,5 +1,14 @@
 // Clipped policy loss with a KL term, its gradient by the logits, and the
 // log-probabilities of tokens (include/dcr_ops.h).
+//
+// A row is read once: each thread keeps its share of it in registers, as
+// 16-byte words, between the statistics (maximum m and sum s of
+// exp((x - m) / T), each thread against its own maximum first) and the
+// gradient.  Long rows are shared by the blocks of a cluster, which exchange
+// (m, s) through distributed shared memory once.  What does not fit on the
+// chip that way is read a second time.  Differences to the maximum are taken
+// before the temperature is applied: they are exact or small, and a row of
+// the type's lowest value behaves like any other constant row.
 #include "ops_internal.h"
 
 namespace dcr {
@@ -19,15 +28,143 @@ struct LossArgs {
     float inv_temp, lo, hi, kl;
 };
 
-// The running maximum and sum of exponentials of two stretches of a row,
-// joined.  A stretch without a finite value has maximum -inf and sum 0.
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2)
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ float exp2_fast(float v)
 {
-    float t = fmaxf(m, m2);
-    float a = m == t ? 1.0f : __expf(m - t), b = m2 == t ? 1.0f : __expf(m2 - t);
-    s = s * a + s2 * b;
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// The 16 bytes of a word as its values, and their largest (a NaN is passed
+// over), without a value for each on the way where two share a register.
+template <typename T>
+struct Word;
+template <>
+struct Word<float> {
+    static constexpr int kN = 4;
+    static constexpr uint32_t kLow = 0xFF800000u;   // -inf
+    static __device__ __forceinline__ void values(const uint4& q, float (&v)[4])
+    {
+        v[0] = __uint_as_float(q.x), v[1] = __uint_as_float(q.y), v[2] = __uint_as_float(q.z), v[3] = __uint_as_float(q.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&v)[4])
+    {
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    }
+};
+template <>
+struct Word<__nv_bfloat16> {
+    static constexpr int kN = 8;
+    static constexpr uint32_t kLow = 0xFF80FF80u;
+    static __device__ __forceinline__ void values(const uint4& q, float (&v)[8])
+    {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&v)[8])
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <>
+struct Word<__half> {
+    static constexpr int kN = 8;
+    static constexpr uint32_t kLow = 0xFC00FC00u;
+    static __device__ __forceinline__ void values(const uint4& q, float (&v)[8])
+    {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            v[2 * i] = f.x, v[2 * i + 1] = f.y;
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&v)[8])
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ float word_max(const uint4& q)
+{
+    float v[Word<T>::kN];
+    Word<T>::values(q, v);
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < Word<T>::kN; ++i) m = fmaxf(m, v[i]);
+    return m;
+}
+
+// Sum of exp((x - m) / T) over a word; sc = log2(e) / T.
+template <typename T>
+__device__ __forceinline__ float word_sum(const uint4& q, float m, float sc)
+{
+    float v[Word<T>::kN], s[2] = {0.0f, 0.0f};
+    Word<T>::values(q, v);
+#pragma unroll
+    for (int i = 0; i < Word<T>::kN; ++i) s[i & 1] += exp2_fast((v[i] - m) * sc);
+    return s[0] + s[1];
+}
+
+// Statistics of two stretches of a row, joined.  Maxima that are equal
+// (infinite ones among them) need no factor.
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2, float sc)
+{
+    const float t = fmaxf(m, m2);
+    s = s * (m == t ? 1.0f : exp2_fast((m - t) * sc)) + s2 * (m2 == t ? 1.0f : exp2_fast((m2 - t) * sc));
     m = t;
 }
+
+// A row as 16-byte words, the first of which may begin before it and the last
+// end behind it: `skip` values of the first word belong to what lies before.
+template <typename T>
+struct Row {
+    T* base;          // on a 16-byte boundary, at or below the row's start
+    uint32_t skip, vocab, words;
+    __device__ __forceinline__ Row(const T* p, uint32_t v)
+    {
+        skip = uint32_t((uintptr_t(p) & 15) / sizeof(T));
+        base = const_cast<T*>(p) - skip;
+        vocab = v;
+        words = (skip + v + Word<T>::kN - 1) / Word<T>::kN;
+    }
+    __device__ __forceinline__ bool whole(uint32_t g) const
+    {
+        return (g > 0 || skip == 0) && (g + 1) * Word<T>::kN <= skip + vocab;
+    }
+    // word g, with -inf where it is not the row
+    __device__ __forceinline__ uint4 load(uint32_t g) const
+    {
+        if (g < words && whole(g)) return *reinterpret_cast<const uint4*>(base + uint64_t(g) * Word<T>::kN);
+        union { uint4 q; T t[Word<T>::kN]; } u;
+        u.q = make_uint4(Word<T>::kLow, Word<T>::kLow, Word<T>::kLow, Word<T>::kLow);
+        if (g < words) {
+#pragma unroll
+            for (int i = 0; i < Word<T>::kN; ++i) {
+                const uint32_t at = g * Word<T>::kN + i;
+                if (at >= skip && at - skip < vocab) u.t[i] = base[at];
+            }
+        }
+        return u.q;
+    }
+};
 
 // Loss of a row and its derivative by the log-probability.
 __device__ __forceinline__ void row_loss(const LossArgs& A, uint64_t row, float lp, float& loss, float& slope)
@@ -44,45 +181,137 @@ __device__ __forceinline__ void row_loss(const LossArgs& A, uint64_t row, float 
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) loss_kernel(LossArgs A)
+// TH threads a block, NV words a thread kept, `cluster` blocks a row.
+template <typename T, int TH, int NV>
+__global__ void __launch_bounds__(TH, TH == 256 ? 3 : 8) loss_kernel(LossArgs A, uint32_t cluster)
 {
-    __shared__ float pm[8], ps[8];
-    const uint64_t row = blockIdx.x;
+    constexpr int N = Word<T>::kN;
+    __shared__ float2 part[TH / 32], all[kMaxCluster];
+    const uint32_t rank = cluster > 1 ? blockIdx.x % cluster : 0;
+    const uint64_t row = blockIdx.x / cluster;
+    const uint32_t vocab = uint32_t(A.vocab);
     const T* x = static_cast<const T*>(A.logits) + row * A.row_stride;
     T* g = A.grad ? static_cast<T*>(A.grad) + row * A.grad_stride : nullptr;
-    const int64_t y = A.tokens[row];
+    const uint32_t step = cluster * TH, first = rank * TH + threadIdx.x;   // this thread's words: first + i * step
+
+    const int64_t token = A.tokens[row];
     const float w = A.weights ? A.weights[row] : 1.0f;
-    if (w == 0.0f || y < 0 || uint64_t(y) >= A.vocab) {
-        if (threadIdx.x == 0) {
-            A.logp[row] = 0.0f;
-            if (A.row_loss) A.row_loss[row] = 0.0f;
+    const bool on = w != 0.0f && token >= 0 && token < int64_t(vocab);
+    const uint32_t y = uint32_t(token);
+    float m = -INFINITY, s = 0.0f, sc = A.inv_temp * kLog2e;
+    uint4 q[NV];
+    float xy = 0.0f;
+    const Row<T> in(x, vocab);
+    if (on) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) q[i] = in.load(first + i * step);
+        xy = to_f32(x[y]);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) m = fmaxf(m, word_max<T>(q[i]));
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s += word_sum<T>(q[i], m, sc);
+        // no value above -inf: nothing to add; +inf: exp(inf - inf) is not a number, although the sum is not one only
+        // if a value is not
+        if (m == -INFINITY || m == INFINITY) {
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float v[N];
+                Word<T>::values(q[i], v);
+#pragma unroll
+                for (int j = 0; j < N; ++j) nan |= v[j] != v[j];
+            }
+            s = nan ? NAN : 0.0f;
         }
-        if (g)
-            for (uint64_t i = threadIdx.x; i < A.vocab; i += 256) g[i] = from_f32<T>(0.0f);
-        return;
+        for (uint32_t k = first + NV * step; k < in.words; k += step) {
+            const uint4 e = in.load(k);
+            const float m2 = word_max<T>(e);
+            float s2 = word_sum<T>(e, m2, sc);
+            if (m2 == -INFINITY || m2 == INFINITY) {
+                float v[N];
+                Word<T>::values(e, v);
+                bool nan = false;
+#pragma unroll
+                for (int j = 0; j < N; ++j) nan |= v[j] != v[j];
+                s2 = nan ? NAN : 0.0f;
+            }
+            join(m, s, m2, s2, sc);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) join(m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o), sc);
+        if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = make_float2(m, s);
+        __syncthreads();
+        m = part[0].x, s = part[0].y;
+#pragma unroll
+        for (int i = 1; i < TH / 32; ++i) join(m, s, part[i].x, part[i].y, sc);
+        if (cluster > 1) {
+            if (threadIdx.x < cluster) {
+                const uint32_t at = uint32_t(__cvta_generic_to_shared(&all[rank]));
+                asm volatile(
+                    "{ .reg .b32 a; mapa.shared::cluster.u32 a, %0, %1; st.shared::cluster.v2.f32 [a], {%2, %3}; }" ::"r"(at),
+                    "r"(threadIdx.x), "f"(m), "f"(s)
+                    : "memory");
+            }
+            asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+            m = all[0].x, s = all[0].y;
+            for (uint32_t i = 1; i < cluster; ++i) join(m, s, all[i].x, all[i].y, sc);
+        } else {
+            __syncthreads();   // grad may be logits: everybody has read x[y]
+        }
+        if (m == INFINITY && s == s) s = 1.0f;
     }
-    float m = -INFINITY, s = 0.0f;
-    for (uint64_t i = threadIdx.x; i < A.vocab; i += 256) join(m, s, to_f32(x[i]) * A.inv_temp, 1.0f);
-    for (int o = 16; o; o >>= 1) join(m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
-    if (threadIdx.x % 32 == 0) pm[threadIdx.x / 32] = m, ps[threadIdx.x / 32] = s;
-    __syncthreads();
-    m = pm[0], s = ps[0];
-    for (int i = 1; i < 8; ++i) join(m, s, pm[i], ps[i]);
-    const float lse = m + logf(s);
-    const float lp = to_f32(x[y]) * A.inv_temp - lse;
-    if (threadIdx.x == 0) A.logp[row] = lp;
-    if (!A.old_logp) return;
-    float loss, slope;
-    row_loss(A, row, lp, loss, slope);
-    if (threadIdx.x == 0) A.row_loss[row] = w * loss;
+
+    float c = 0.0f;
+    if (on) {
+        const float lp = ((xy - m) * sc - log2f(s)) * kLn2;
+        float loss = 0.0f, slope = 0.0f;
+        if (A.old_logp) row_loss(A, row, lp, loss, slope);
+        if (rank == 0 && threadIdx.x == 0) {
+            A.logp[row] = lp;
+            if (A.row_loss) A.row_loss[row] = w * loss;
+        }
+        c = w * slope * A.inv_temp;
+    } else if (rank == 0 && threadIdx.x == 0) {
+        A.logp[row] = 0.0f;
+        if (A.row_loss) A.row_loss[row] = 0.0f;
+    }
     if (!g) return;
-    const float c = w * slope * A.inv_temp;
-    __syncthreads();   // grad may be logits: x[y] has been read by all
-    for (uint64_t i = threadIdx.x; i < A.vocab; i += 256) {
-        float p = __expf(to_f32(x[i]) * A.inv_temp - lse);
-        g[i] = from_f32<T>(c * ((int64_t(i) == y ? 1.0f : 0.0f) - p));
-    }
+
+    // grad_j = c ([j = y] - exp((x_j - m) / T) / s): the words as they were read, where the gradient's row lies on the
+    // same offset from a 16-byte boundary
+    const float d = on ? -c / s : 0.0f;
+    const Row<T> out(g, vocab);
+    const bool same = out.skip == in.skip;
+    const uint32_t ypos = in.skip + y;
+    auto put = [&](uint32_t k, const uint4& e) {
+        if (k >= in.words) return;
+        float v[N];
+        if (on) {
+            Word<T>::values(e, v);
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = d * exp2_fast((v[j] - m) * sc);
+            if (ypos / N == k) {
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (ypos % N == j) v[j] += c;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = 0.0f;
+        }
+        if (same && in.whole(k)) {
+            *reinterpret_cast<uint4*>(out.base + uint64_t(k) * N) = Word<T>::pack(v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const uint32_t at = k * N + j;
+                if (at >= in.skip && at - in.skip < vocab) g[at - in.skip] = from_f32<T>(v[j]);
+            }
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i) put(first + i * step, q[i]);
+    for (uint32_t k = first + NV * step; k < in.words; k += step) put(k, on ? in.load(k) : make_uint4(0, 0, 0, 0));
 }
 
 // The rows' losses summed in a fixed order: thread i takes rows i, i + 1024,
@@ -102,10 +331,43 @@ __global__ void __launch_bounds__(1024) sum_kernel(const float* v, uint64_t n, f
     }
 }
 
+template <typename T, int TH, int NV>
+int launch_rows(const LossArgs& A, uint32_t cluster, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(A.rows * cluster));
+    cfg.blockDim = dim3(TH);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, loss_kernel<T, TH, NV>, A, cluster);
+    return e == cudaSuccess ? DCR_OK : cuda_error(e, "policy loss launch");
+}
+
+// Blocks just large enough for the row, up to 32 KiB of it each; then a
+// cluster of them.
+template <typename T>
+int launch_rows(const LossArgs& A, cudaStream_t s)
+{
+    const uint64_t bytes = A.vocab * sizeof(T) + 16;
+    if (bytes <= 2048) return launch_rows<T, 128, 1>(A, 1, s);
+    if (bytes <= 8192) return launch_rows<T, 128, 4>(A, 1, s);
+    uint32_t cluster = 1;
+    while (cluster < kMaxCluster && bytes > 32768ull * cluster) cluster *= 2;
+    return launch_rows<T, 256, 8>(A, cluster, s);
+}
+
 int launch(const LossArgs& A, uint32_t dtype, float* loss, cudaStream_t s)
 {
     if (A.rows == 0 && !loss) return DCR_OK;
-    if (A.rows) with_dtype(dtype, [&](auto t) { loss_kernel<decltype(t)><<<unsigned(A.rows), 256, 0, s>>>(A); });
+    if (A.rows) {
+        const int rc = with_dtype(dtype, [&](auto t) { return launch_rows<decltype(t)>(A, s); });
+        if (rc != DCR_OK) return rc;
+    }
     if (loss) sum_kernel<<<1, 1024, 0, s>>>(A.row_loss, A.rows, loss);
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? DCR_OK : cuda_error(e, "policy loss launch");
@@ -117,8 +379,8 @@ int check(const char* what, const void* logits, uint32_t dtype, uint64_t rows, u
     if (dtype > DCR_F16) return set_error(DCR_ERR_INVALID, "%s: unknown dtype %u", what, dtype);
     if (!(temperature > 0.0f) || temperature > 3.0e38f)
         return set_error(DCR_ERR_INVALID, "%s: temperature must be positive and finite", what);
-    if (vocab == 0 || vocab >= 1ull << 31 || rows >= 1ull << 31 || row_stride >= 1ull << 40)
-        return set_error(DCR_ERR_INVALID, "%s: vocab must be at least 1 and sizes below 2^31", what);
+    if (vocab == 0 || vocab >= 1ull << 31 || rows >= 1ull << 28 || row_stride >= 1ull << 40)
+        return set_error(DCR_ERR_INVALID, "%s: vocab must be at least 1 and below 2^31, rows below 2^28", what);
     if (row_stride < vocab) return set_error(DCR_ERR_INVALID, "%s: row_stride below vocab", what);
     if (rows && (!logits || !tokens || !logp)) return set_error(DCR_ERR_INVALID, "%s: NULL argument", what);
     if (uintptr_t(logits) % dtype_size(dtype) || uintptr_t(tokens) % 8 || uintptr_t(logp) % 4)

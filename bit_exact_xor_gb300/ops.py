@@ -17,6 +17,7 @@ from . import ERR_INVALID, DcrError, check, lib
 F32, BF16, F16, NONE = 0, 1, 2, 3
 SCALE_GIVEN, SCALE_TENSOR, SCALE_ROW = 0, 1, 2
 MAX_EXPERTS = 1024
+QUANT_PARTIALS = 1216
 DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 OP_EXPORTS = ["dcr_nvfp4_quantize", "dcr_nvfp4_matmul", "dcr_policy_loss", "dcr_token_logprobs",
@@ -51,7 +52,7 @@ def _lib():
     if _ops is None:
         L = lib()
         P, VP, U32, U64 = ctypes.POINTER, ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64
-        L.dcr_nvfp4_quantize.argtypes = [VP, U32, U64, U64, U64, U32, VP, VP, VP, VP, U32, VP]
+        L.dcr_nvfp4_quantize.argtypes = [VP, U32, U64, U64, U64, U32, VP, VP, VP, VP, U32, VP, VP]
         L.dcr_nvfp4_matmul.argtypes = [P(_Nvfp4), P(_Nvfp4), U64, U64, U64, VP, U32, VP, U32, U64, VP]
         L.dcr_policy_loss.argtypes = [VP, U32, U64, U64, U64, VP, VP, VP, VP, VP, P(PolicyOpts), VP, VP, VP, VP, U64, VP]
         L.dcr_token_logprobs.argtypes = [VP, U32, U64, U64, U64, VP, ctypes.c_float, VP, VP]
@@ -136,7 +137,14 @@ def nvfp4_quantize(x, scale=None, per_row=False, values=None, out=None):
         mode, sc = SCALE_GIVEN, scale
     else:
         mode = SCALE_ROW if per_row else SCALE_TENSOR
-        sc = _out(sc, (rows if per_row else 1,), torch.float32, "scale", dev)
+        if sc is not None:
+            _flat(sc, rows if per_row else 1, torch.float32, "scale", dev)
+        elif per_row:
+            sc = torch.empty(rows, dtype=torch.float32, device=dev)
+    work = None
+    if mode == SCALE_TENSOR:
+        work = torch.empty(QUANT_PARTIALS + 1, dtype=torch.float32, device=dev)
+        sc = work[QUANT_PARTIALS:] if sc is None else sc
     vt = NONE
     if values is not None:
         if isinstance(values, torch.dtype):
@@ -146,7 +154,8 @@ def nvfp4_quantize(x, scale=None, per_row=False, values=None, out=None):
         _flat(values, rows * cols, values.dtype, "values", dev)
     check(_lib().dcr_nvfp4_quantize(x.data_ptr(), DTYPES[x.dtype], rows, cols, stride, mode, sc.data_ptr(),
                                     codes.data_ptr(), scales.data_ptr(),
-                                    values.data_ptr() if values is not None else None, vt, _stream()))
+                                    values.data_ptr() if values is not None else None, vt,
+                                    work.data_ptr() if work is not None else None, _stream()))
     return Nvfp4(codes, scales, sc), values
 
 

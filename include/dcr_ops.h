@@ -58,10 +58,12 @@ typedef struct {
  * DCR_NONE without) receives what the codes stand for, rounded once to its
  * type: the weights that a quantisation-aware forward pass computes with.
  * The gradient of a quantisation-aware pass goes straight through: no value
- * saturates, except under a GIVEN scale. */
+ * saturates, except under a GIVEN scale.  workspace (TENSOR only, device, at
+ * least DCR_QUANT_PARTIALS floats) holds partial maxima during the call. */
+#define DCR_QUANT_PARTIALS 1216u
 int dcr_nvfp4_quantize(const void* x, uint32_t dtype, uint64_t rows, uint64_t cols, uint64_t row_stride,
                        uint32_t scale_mode, float* scale, void* codes, void* scales, void* values,
-                       uint32_t values_dtype, void* stream);
+                       uint32_t values_dtype, void* workspace, void* stream);
 
 /* y [m, n] (dtype, rows y_stride elements apart) = x w^T, x [m, k] and w
  * [n, k] both NVFP4, k a multiple of 32.  The sums are held in 32 bits and

@@ -15,14 +15,14 @@ from bit_exact_xor_gb300 import ops  # noqa: E402
 P = 4096   # a well-aligned address that no refused call reads
 
 
-def _quant(x=P, dtype=0, rows=2, cols=32, stride=32, mode=1, scale=P, codes=P, scales=P, values=None, vt=3):
-    return ops._lib().dcr_nvfp4_quantize(x, dtype, rows, cols, stride, mode, scale, codes, scales, values, vt, None)
+def _quant(x=P, dtype=0, rows=2, cols=32, stride=32, mode=1, scale=P, codes=P, scales=P, values=None, vt=3, work=P):
+    return ops._lib().dcr_nvfp4_quantize(x, dtype, rows, cols, stride, mode, scale, codes, scales, values, vt, work, None)
 
 
 @pytest.mark.parametrize("kw,why", [
     (dict(dtype=3), "unknown dtype"), (dict(mode=3), "scale mode"), (dict(cols=24), "multiple of 16"),
     (dict(stride=16), "row_stride"), (dict(values=P), "values"), (dict(vt=1), "values"), (dict(x=None), "NULL"),
-    (dict(scale=None), "NULL"), (dict(codes=None), "NULL"), (dict(scales=None), "NULL"), (dict(codes=P + 8), "misaligned"),
+    (dict(scale=None), "NULL"), (dict(work=None), "NULL"), (dict(work=P + 2), "misaligned"), (dict(codes=None), "NULL"), (dict(scales=None), "NULL"), (dict(codes=P + 8), "misaligned"),
     (dict(values=P + 2, vt=1), "misaligned"), (dict(x=P + 2), "misaligned"), (dict(scale=P + 1), "misaligned"),
     (dict(rows=1 << 32), "too large"), (dict(cols=1 << 32, stride=1 << 32), "too large"),
 ])
@@ -82,7 +82,7 @@ def _loss(logits=P, dtype=1, rows=4, vocab=10, stride=10, tokens=P, old=P, ref=P
     (dict(opts=(float("inf"), 0.2, 0.2, 0.0)), "temperature"), (dict(opts=(1.0, -0.1, 0.2, 0.0)), "clip_low"),
     (dict(opts=(1.0, 0.1, float("nan"), 0.0)), "clip_high"), (dict(opts=(1.0, 0.1, 0.2, -1.0)), "kl_coef"),
     (dict(grad=P, gstride=12), "same stride"), (dict(grad=P + 1), "misaligned"), (dict(logits=P + 1), "misaligned"),
-    (dict(tokens=P + 4), "misaligned"), (dict(old=P + 2), "misaligned"), (dict(rows=1 << 31), "sizes"),
+    (dict(tokens=P + 4), "misaligned"), (dict(old=P + 2), "misaligned"), (dict(rows=1 << 28), "rows below"),
 ])
 def test_policy_loss(kw, why):
     assert _loss(**kw) == dcr.ERR_INVALID
@@ -113,6 +113,7 @@ def test_header_constants_and_exports():
     src = re.sub(r"/\*.*?\*/", "", open(os.path.join(os.path.dirname(ops.__file__), "..", "include", "dcr_ops.h")).read(), flags=re.S)
     vals = {k: int(v) for k, v in re.findall(r"\bDCR_(\w+)\s*=\s*(\d+)", src)}
     assert vals and all(getattr(ops, k) == v for k, v in vals.items())
+    assert int(re.search(r"DCR_QUANT_PARTIALS (\d+)u", src).group(1)) == ops.QUANT_PARTIALS
     assert int(re.search(r"DCR_MAX_EXPERTS (\d+)u", src).group(1)) == ops.MAX_EXPERTS
     declared = set(re.findall(r"^int (dcr_\w+)\(", src, flags=re.M))
     assert declared == set(ops.OP_EXPORTS)
