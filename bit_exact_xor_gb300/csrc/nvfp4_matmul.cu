@@ -292,6 +292,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
     }
     __syncthreads();
     fence_after();
+    grid_wait();   // what is read from here on may come from the kernel before
     const uint32_t tmem = C.tmem_base;
     const uint32_t rank = split > 1 ? cluster_rank() : 0;
     const uint32_t steps = (A.k + kStep - 1) / kStep;
@@ -565,7 +566,7 @@ uint32_t scale_align(const void* p, uint32_t k)
 }
 
 template <int BN, bool XP, typename T>
-int launch(MatmulArgs A, const dcr_nvfp4& x, const dcr_nvfp4& w, uint32_t split, cudaStream_t s)
+int launch(MatmulArgs A, const dcr_nvfp4& x, const dcr_nvfp4& w, uint32_t split, bool dependent, cudaStream_t s)
 {
     using S = Shape<BN>;
     const dcr_nvfp4 &p = XP ? x : w, &q = XP ? w : x;
@@ -589,18 +590,8 @@ int launch(MatmulArgs A, const dcr_nvfp4& x, const dcr_nvfp4& w, uint32_t split,
     const int smem = S::kSmem + int(sizeof(Control<S::kStages>) + 4 * groups);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return cuda_error(e, "NVFP4 product attributes");
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(grid));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = size_t(smem);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, mp, mq, A, split);
+    const LaunchAttrs at(grid, kThreads, size_t(smem), split, dependent, s);
+    e = cudaLaunchKernelEx(&at.cfg, kernel, mp, mq, A, split);
     return e == cudaSuccess ? DCR_OK : cuda_error(e, "NVFP4 product launch");
 }
 
@@ -608,21 +599,59 @@ int launch(MatmulArgs A, const dcr_nvfp4& x, const dcr_nvfp4& w, uint32_t split,
 // there are enough tokens that 128-token by 256-weight tiles fill the SMs.
 // Few tiles are split over K among the blocks of a cluster.
 template <typename T>
-int choose(const MatmulArgs& A, const dcr_nvfp4& x, const dcr_nvfp4& w, cudaStream_t s)
+int choose(const MatmulArgs& A, const dcr_nvfp4& x, const dcr_nvfp4& w, bool dependent, cudaStream_t s)
 {
     const uint64_t groups = A.experts ? A.experts : 1, sms = uint64_t(sm_count());
     const uint64_t each = (A.m + groups - 1) / groups;
     const uint64_t wide = ((each + 127) / 128) * ((A.n + 255) / 256) * groups;
-    if (each > 64 && wide >= sms / 2) return launch<256, true, T>(A, x, w, 1, s);
+    if (each > 64 && wide >= sms / 2) return launch<256, true, T>(A, x, w, 1, dependent, s);
     const uint64_t bn = each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : 128;
     const uint64_t tiles = ((each + bn - 1) / bn) * ((A.n + 127) / 128) * groups;
     const uint32_t steps = (A.k + kStep - 1) / kStep;
     uint32_t split = 1;
     while (split < 8 && tiles * split * 2 <= sms * 2 && steps >= split * 4) split *= 2;
-    if (bn == 16) return launch<16, false, T>(A, x, w, split, s);
-    if (bn == 32) return launch<32, false, T>(A, x, w, split, s);
-    if (bn == 64) return launch<64, false, T>(A, x, w, split, s);
-    return launch<128, false, T>(A, x, w, split, s);
+    if (bn == 16) return launch<16, false, T>(A, x, w, split, dependent, s);
+    if (bn == 32) return launch<32, false, T>(A, x, w, split, dependent, s);
+    if (bn == 64) return launch<64, false, T>(A, x, w, split, dependent, s);
+    return launch<128, false, T>(A, x, w, split, dependent, s);
+}
+
+}  // namespace
+
+int matmul_launch(const dcr_nvfp4& x, const dcr_nvfp4& w, uint64_t m, uint64_t n, uint64_t k, const int32_t* offsets,
+                  uint32_t experts, void* y, uint32_t dtype, uint64_t y_stride, bool dependent, cudaStream_t s)
+{
+    MatmulArgs A{};
+    A.x_scale = x.scale, A.w_scale = w.scale;
+    A.x_scale_rows = x.scale_count > 1, A.w_scale_each = w.scale_count > 1;
+    A.m = uint32_t(m), A.n = uint32_t(n), A.k = uint32_t(k), A.experts = experts;
+    A.offsets = offsets, A.y = y, A.y_stride = y_stride;
+    A.y_vec = uintptr_t(y) % 32 == 0 && y_stride * dtype_size(dtype) % 32 == 0;
+    return with_dtype(dtype, [&](auto t) { return choose<decltype(t)>(A, x, w, dependent, s); });
+}
+
+namespace {
+
+// What dcr_nvfp4_matmul and dcr_nvfp4_linear refuse alike; 1 if there is nothing to do.
+int check(const char* what, const dcr_nvfp4& w, uint64_t m, uint64_t n, uint64_t k, const int32_t* offsets,
+          uint32_t experts, const void* y, uint32_t dtype, uint64_t y_stride)
+{
+    if (dtype > DCR_F16) return set_error(DCR_ERR_INVALID, "%s: unknown dtype %u", what, dtype);
+    if (k == 0 || k % 32) return set_error(DCR_ERR_INVALID, "%s: k must be a positive multiple of 32", what);
+    if (experts > DCR_MAX_EXPERTS) return set_error(DCR_ERR_INVALID, "%s: more than %u experts", what, DCR_MAX_EXPERTS);
+    if ((experts > 0) != (offsets != nullptr))
+        return set_error(DCR_ERR_INVALID, "%s: experts and offsets do not go together", what);
+    const uint64_t wrows = n * (experts ? experts : 1);
+    if (m >= 1ull << 31 || n >= 1ull << 31 || k >= 1ull << 31 || wrows >= 1ull << 31 || y_stride >= 1ull << 40)
+        return set_error(DCR_ERR_INVALID, "%s: matrix too large", what);
+    if (y_stride < n) return set_error(DCR_ERR_INVALID, "%s: y_stride below n", what);
+    if (w.scale_count != 1 && (experts == 0 || w.scale_count != experts))
+        return set_error(DCR_ERR_INVALID, "%s: w needs one scale or one per expert", what);
+    if (m == 0 || n == 0) return 1;
+    if (!w.codes || !w.scales || !w.scale || !y) return set_error(DCR_ERR_INVALID, "%s: NULL argument", what);
+    if (uintptr_t(w.codes) % 16 || uintptr_t(y) % dtype_size(dtype) || uintptr_t(w.scale) % 4 || uintptr_t(offsets) % 4)
+        return set_error(DCR_ERR_INVALID, "%s: misaligned buffer", what);
+    return DCR_OK;
 }
 
 }  // namespace
@@ -635,32 +664,34 @@ extern "C" int dcr_nvfp4_matmul(const dcr_nvfp4* x, const dcr_nvfp4* w, uint64_t
                                 void* stream)
 {
     if (!x || !w) return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: NULL argument");
-    if (dtype > DCR_F16) return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: unknown dtype %u", dtype);
-    if (k == 0 || k % 32) return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: k must be a positive multiple of 32");
-    if (experts > DCR_MAX_EXPERTS) return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: more than %u experts", DCR_MAX_EXPERTS);
-    if ((experts > 0) != (offsets != nullptr))
-        return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: experts and offsets do not go together");
-    const uint64_t wrows = n * (experts ? experts : 1);
-    if (m >= 1ull << 31 || n >= 1ull << 31 || k >= 1ull << 31 || wrows >= 1ull << 31 || y_stride >= 1ull << 40)
-        return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: matrix too large");
-    if (y_stride < n) return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: y_stride below n");
     if (x->scale_count != 1 && x->scale_count != m)
         return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: x needs one scale or one per row");
-    if (w->scale_count != 1 && (experts == 0 || w->scale_count != experts))
-        return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: w needs one scale or one per expert");
-    if (m == 0 || n == 0) return DCR_OK;
-    if (!x->codes || !x->scales || !x->scale || !w->codes || !w->scales || !w->scale || !y)
-        return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: NULL argument");
-    if (uintptr_t(x->codes) % 16 || uintptr_t(w->codes) % 16 || uintptr_t(y) % dtype_size(dtype) ||
-        uintptr_t(x->scale) % 4 || uintptr_t(w->scale) % 4 || uintptr_t(offsets) % 4)
+    if (int rc = dcr::check("dcr_nvfp4_matmul", *w, m, n, k, offsets, experts, y, dtype, y_stride)) return rc > 0 ? DCR_OK : rc;
+    if (!x->codes || !x->scales || !x->scale) return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: NULL argument");
+    if (uintptr_t(x->codes) % 16 || uintptr_t(x->scale) % 4)
         return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: misaligned buffer");
-    MatmulArgs A{};
-    A.x_scale = x->scale, A.w_scale = w->scale;
-    A.x_scale_rows = x->scale_count > 1, A.w_scale_each = w->scale_count > 1;
-    A.m = uint32_t(m), A.n = uint32_t(n), A.k = uint32_t(k), A.experts = experts;
-    A.offsets = offsets, A.y = y, A.y_stride = y_stride;
-    A.y_vec = uintptr_t(y) % 32 == 0 && y_stride * dtype_size(dtype) % 32 == 0;
-    return with_dtype(dtype, [&](auto t) { return choose<decltype(t)>(A, *x, *w, static_cast<cudaStream_t>(stream)); });
+    return matmul_launch(*x, *w, m, n, k, offsets, experts, y, dtype, y_stride, false, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int dcr_nvfp4_linear(const void* x, uint32_t x_dtype, uint64_t x_stride, const dcr_nvfp4* w, uint64_t m,
+                                uint64_t n, uint64_t k, const int32_t* offsets, uint32_t experts, void* y, uint32_t dtype,
+                                uint64_t y_stride, void* workspace, void* stream)
+{
+    if (!w) return set_error(DCR_ERR_INVALID, "dcr_nvfp4_linear: NULL argument");
+    if (x_dtype > DCR_F16) return set_error(DCR_ERR_INVALID, "dcr_nvfp4_linear: unknown dtype %u", x_dtype);
+    if (int rc = dcr::check("dcr_nvfp4_linear", *w, m, n, k, offsets, experts, y, dtype, y_stride)) return rc > 0 ? DCR_OK : rc;
+    if (!x || !workspace) return set_error(DCR_ERR_INVALID, "dcr_nvfp4_linear: NULL argument");
+    if (x_stride < k || x_stride >= 1ull << 40) return set_error(DCR_ERR_INVALID, "dcr_nvfp4_linear: bad x_stride");
+    if (uintptr_t(x) % dtype_size(x_dtype) || uintptr_t(workspace) % 16)
+        return set_error(DCR_ERR_INVALID, "dcr_nvfp4_linear: misaligned buffer");
+    // k is a multiple of 32: the scales start on a 16-byte boundary, the rows' scales on one of 4
+    uint8_t* codes = static_cast<uint8_t*>(workspace);
+    uint8_t* scales = codes + m * (k / 2);
+    float* scale = reinterpret_cast<float*>(scales + (m * (k / 16) + 3) / 4 * 4);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (int rc = quantize_launch(x, x_dtype, m, k, x_stride, DCR_SCALE_ROW, scale, codes, scales, nullptr, DCR_NONE, nullptr, s))
+        return rc;
+    return matmul_launch(dcr_nvfp4{codes, scales, scale, m}, *w, m, n, k, offsets, experts, y, dtype, y_stride, true, s);
 }
 
 extern "C" int dcr_ops_status(void* stream)

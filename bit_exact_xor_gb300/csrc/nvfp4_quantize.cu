@@ -232,6 +232,7 @@ template <typename T, bool VEC, bool FLAT>
 __global__ void __launch_bounds__(kThreads) amax_kernel(QuantArgs A, float* partial)
 {
     const uint8_t *lo = static_cast<const uint8_t*>(A.x), *hi = matrix_end<T>(A);
+    launch_dependents();
     float a = 0.0f;
     const uint64_t step = uint64_t(gridDim.x) * kThreads;
     for (uint64_t b = uint64_t(blockIdx.x) * kThreads + threadIdx.x; b < A.blocks; b += kUnroll * step) {
@@ -256,6 +257,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(QuantArgs A)
     const uint8_t *lo = static_cast<const uint8_t*>(A.x), *hi = matrix_end<T>(A);
     float t;
     if (MODE == DCR_SCALE_TENSOR) {
+        grid_wait();
         t = 0.0f;
         for (uint32_t i = threadIdx.x; i < A.n_partial; i += kThreads) t = fmaxf(t, A.partial[i]);
         t = scale_or_one(block_max<kThreads>(t));
@@ -290,6 +292,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantArgs A)
 {
     const uint8_t *lo = static_cast<const uint8_t*>(A.x), *hi = matrix_end<T>(A);
     const uint32_t lane = threadIdx.x % TPR;
+    launch_dependents();
     for (uint64_t row = uint64_t(blockIdx.x) * (kThreads / TPR) + threadIdx.x / TPR; row < A.rows;
          row += uint64_t(gridDim.x) * (kThreads / TPR)) {
         const T* x = static_cast<const T*>(A.x) + row * A.row_stride;
@@ -346,7 +349,8 @@ void launch(const QuantArgs& A, uint32_t mode, float* partial, cudaStream_t s)
                 B.partial = partial;
                 B.n_partial = grid;
                 amax_kernel<T, ve.value, fl.value><<<grid, kThreads, 0, s>>>(A, partial);
-                quantize_kernel<T, V, DCR_SCALE_TENSOR, VALUES, ve.value, fl.value><<<grid, kThreads, 0, s>>>(B);
+                const LaunchAttrs at(grid, kThreads, 0, 1, true, s);
+                cudaLaunchKernelEx(&at.cfg, quantize_kernel<T, V, DCR_SCALE_TENSOR, VALUES, ve.value, fl.value>, B);
             } else {
                 quantize_kernel<T, V, DCR_SCALE_GIVEN, VALUES, ve.value, fl.value><<<grid, kThreads, 0, s>>>(A);
             }
@@ -355,6 +359,22 @@ void launch(const QuantArgs& A, uint32_t mode, float* partial, cudaStream_t s)
 }
 
 }  // namespace
+
+int quantize_launch(const void* x, uint32_t dtype, uint64_t rows, uint64_t cols, uint64_t row_stride, uint32_t scale_mode,
+                    float* scale, void* codes, void* scales, void* values, uint32_t values_dtype, void* workspace,
+                    cudaStream_t s)
+{
+    QuantArgs A{x, scale, nullptr, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), values, rows, row_stride,
+                rows * (cols / 16), uint32_t(cols / 16), 0};
+    float* partial = static_cast<float*>(workspace);
+    with_dtype(dtype, [&](auto t) {
+        if (!values) return launch<decltype(t), float, false>(A, scale_mode, partial, s);
+        with_dtype(values_dtype, [&](auto v) { launch<decltype(t), decltype(v), true>(A, scale_mode, partial, s); });
+    });
+    cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? DCR_OK : cuda_error(e, "NVFP4 quantise launch");
+}
+
 }  // namespace dcr
 
 using namespace dcr;
@@ -376,14 +396,6 @@ extern "C" int dcr_nvfp4_quantize(const void* x, uint32_t dtype, uint64_t rows, 
         return set_error(DCR_ERR_INVALID, "dcr_nvfp4_quantize: NULL argument");
     if (uintptr_t(codes) % 16 || uintptr_t(values) % 16 || uintptr_t(scale) % 4 || uintptr_t(workspace) % 4 || uintptr_t(x) % dtype_size(dtype))
         return set_error(DCR_ERR_INVALID, "dcr_nvfp4_quantize: misaligned buffer");
-    QuantArgs A{x, scale, nullptr, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), values, rows, row_stride,
-                rows * (cols / 16), uint32_t(cols / 16), 0};
-    float* partial = static_cast<float*>(workspace);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    with_dtype(dtype, [&](auto t) {
-        if (!values) return launch<decltype(t), float, false>(A, scale_mode, partial, s);
-        with_dtype(values_dtype, [&](auto v) { launch<decltype(t), decltype(v), true>(A, scale_mode, partial, s); });
-    });
-    cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? DCR_OK : cuda_error(e, "NVFP4 quantise launch");
+    return quantize_launch(x, dtype, rows, cols, row_stride, scale_mode, scale, codes, scales, values, values_dtype,
+                           workspace, static_cast<cudaStream_t>(stream));
 }

@@ -28,7 +28,7 @@ struct LossArgs {
     float inv_temp, lo, hi, kl;
 };
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ float exp2_fast(float v)
@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 3 : 8) loss_kernel(LossArgs A,
 {
     constexpr int N = Word<T>::kN;
     __shared__ float2 part[TH / 32], all[kMaxCluster];
+    launch_dependents();
     const uint32_t rank = cluster > 1 ? blockIdx.x % cluster : 0;
     const uint64_t row = blockIdx.x / cluster;
     const uint32_t vocab = uint32_t(A.vocab);
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 3 : 8) loss_kernel(LossArgs A,
 
     float c = 0.0f;
     if (on) {
-        const float lp = ((xy - m) * sc - log2f(s)) * kLn2;
+        const float lp = (xy - m) * A.inv_temp - logf(s);
         float loss = 0.0f, slope = 0.0f;
         if (A.old_logp) row_loss(A, row, lp, loss, slope);
         if (rank == 0 && threadIdx.x == 0) {
@@ -319,6 +320,7 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 3 : 8) loss_kernel(LossArgs A,
 __global__ void __launch_bounds__(1024) sum_kernel(const float* v, uint64_t n, float* out)
 {
     __shared__ double part[32];
+    grid_wait();
     double s = 0.0;
     for (uint64_t i = threadIdx.x; i < n; i += 1024) s += v[i];
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
@@ -334,17 +336,8 @@ __global__ void __launch_bounds__(1024) sum_kernel(const float* v, uint64_t n, f
 template <typename T, int TH, int NV>
 int launch_rows(const LossArgs& A, uint32_t cluster, cudaStream_t s)
 {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(A.rows * cluster));
-    cfg.blockDim = dim3(TH);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = cluster;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, loss_kernel<T, TH, NV>, A, cluster);
+    const LaunchAttrs at(A.rows * cluster, TH, 0, cluster, false, s);
+    const cudaError_t e = cudaLaunchKernelEx(&at.cfg, loss_kernel<T, TH, NV>, A, cluster);
     return e == cudaSuccess ? DCR_OK : cuda_error(e, "policy loss launch");
 }
 
@@ -368,8 +361,9 @@ int launch(const LossArgs& A, uint32_t dtype, float* loss, cudaStream_t s)
         const int rc = with_dtype(dtype, [&](auto t) { return launch_rows<decltype(t)>(A, s); });
         if (rc != DCR_OK) return rc;
     }
-    if (loss) sum_kernel<<<1, 1024, 0, s>>>(A.row_loss, A.rows, loss);
-    cudaError_t e = cudaGetLastError();
+    if (!loss) return DCR_OK;
+    const LaunchAttrs at(1, 1024, 0, 1, A.rows != 0, s);
+    const cudaError_t e = cudaLaunchKernelEx(&at.cfg, sum_kernel, static_cast<const float*>(A.row_loss), A.rows, loss);
     return e == cudaSuccess ? DCR_OK : cuda_error(e, "policy loss launch");
 }
 

@@ -79,6 +79,16 @@ int dcr_nvfp4_matmul(const dcr_nvfp4* x, const dcr_nvfp4* w, uint64_t m, uint64_
                      const int32_t* offsets, uint32_t experts, void* y, uint32_t dtype, uint64_t y_stride,
                      void* stream);
 
+/* y = x w^T for activations x [m, k] (x_dtype, rows x_stride elements apart):
+ * x is quantised with a scale per row, so that a row's result does not depend
+ * on the rows beside it, then multiplied as in dcr_nvfp4_matmul.  workspace
+ * (device, 16-byte aligned, DCR_LINEAR_WORKSPACE bytes) holds the quantised
+ * activations during the call. */
+#define DCR_LINEAR_WORKSPACE(m, k) ((m) * ((k) / 2 + (k) / 16 + 4) + 4)
+int dcr_nvfp4_linear(const void* x, uint32_t x_dtype, uint64_t x_stride, const dcr_nvfp4* w, uint64_t m, uint64_t n,
+                     uint64_t k, const int32_t* offsets, uint32_t experts, void* y, uint32_t dtype,
+                     uint64_t y_stride, void* workspace, void* stream);
+
 /* Clipped policy loss with a KL term, from logits [rows, vocab] (dtype, rows
  * row_stride elements apart), with the gradient by the logits.  Per row, with
  * token y, old log-probability o, reference q, advantage A and weight w:

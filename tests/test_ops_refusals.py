@@ -1,7 +1,6 @@
 """Arguments that the operators refuse, at the C entries and in the binding,
 before anything is launched (so on a machine without a GPU)."""
 import ctypes
-import glob
 import os
 import re
 
@@ -66,6 +65,23 @@ def test_matmul_null_and_nothing():
     assert _matmul(n=0, w=_mat(None, None, P, 1), y=None, stride=0) == dcr.OK
 
 
+def _linear(x=P, xdt=1, xs=64, w=None, m=4, n=8, k=64, offsets=None, experts=0, y=P, dtype=1, stride=8, work=P):
+    w = w or _mat()
+    return ops._lib().dcr_nvfp4_linear(x, xdt, xs, ctypes.byref(w), m, n, k, offsets, experts, y, dtype, stride, work, None)
+
+
+@pytest.mark.parametrize("kw,why", [
+    (dict(xdt=3), "unknown dtype"), (dict(dtype=4), "unknown dtype"), (dict(k=48), "multiple of 32"), (dict(xs=63), "x_stride"),
+    (dict(x=None), "NULL"), (dict(work=None), "NULL"), (dict(w=_mat(codes=None)), "NULL"), (dict(work=P + 8), "misaligned"),
+    (dict(x=P + 1), "misaligned"), (dict(w=_mat(codes=P + 8)), "misaligned"), (dict(experts=1), "offsets"),
+    (dict(stride=7), "y_stride"), (dict(w=_mat(count=2)), "w needs"), (dict(n=1 << 31, stride=1 << 31), "too large"),
+])
+def test_linear(kw, why):
+    assert _linear(**kw) == dcr.ERR_INVALID
+    assert why in dcr.last_error(), dcr.last_error()
+    assert _linear(m=0, x=None, y=None, work=None) == dcr.OK
+
+
 def _loss(logits=P, dtype=1, rows=4, vocab=10, stride=10, tokens=P, old=P, ref=P, adv=P, w=P, opts=(1.0, 0.2, 0.2, 0.1),
           loss=P, row_loss=P, logp=P, grad=2 * P, gstride=10):
     o = ctypes.byref(ops.PolicyOpts(*opts)) if opts else None
@@ -115,6 +131,6 @@ def test_header_constants_and_exports():
     assert vals and all(getattr(ops, k) == v for k, v in vals.items())
     assert int(re.search(r"DCR_QUANT_PARTIALS (\d+)u", src).group(1)) == ops.QUANT_PARTIALS
     assert int(re.search(r"DCR_MAX_EXPERTS (\d+)u", src).group(1)) == ops.MAX_EXPERTS
+    assert "#define DCR_LINEAR_WORKSPACE(m, k) ((m) * ((k) / 2 + (k) / 16 + 4) + 4)" in src
     declared = set(re.findall(r"^int (dcr_\w+)\(", src, flags=re.M))
     assert declared == set(ops.OP_EXPORTS)
-    assert glob.glob(os.path.join(os.path.dirname(ops.__file__), "csrc", "policy_loss.cu"))
