@@ -68,7 +68,7 @@ __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity)
 {
     uint32_t ok;
     asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
         : "=r"(ok) : "r"(saddr(b)), "r"(parity) : "memory");
     return ok != 0;
 }
@@ -82,7 +82,7 @@ __device__ __forceinline__ uint64_t now_ns()
 
 // Every wait is bounded: after two seconds, or once another warp of the block
 // has given up, it returns false and the block winds down.
-__device__ __noinline__ bool mbar_wait_long(uint64_t* b, uint32_t parity, volatile int* dead)
+__device__ __forceinline__ bool mbar_wait_long(uint64_t* b, uint32_t parity, volatile int* dead)
 {
     const uint64_t t0 = now_ns();
     while (!*dead) {
@@ -196,6 +196,34 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* row, uint32_t k16, u
     return u.v;
 }
 
+// The scales of this lane's rows (one of each NV, or null) for steps k0 to
+// k1, handed to `put` step by step.  Two steps' loads go out together, four
+// ahead of their use: they share a 32-byte sector.
+template <int NV, typename F>
+__device__ __forceinline__ void stream_scales(const uint8_t* const (&row)[NV], const uint32_t (&align)[NV], uint32_t n16,
+                                              uint32_t k0, uint32_t k1, F put)
+{
+    uint4 buf[2][2][NV];
+    auto load = [&](uint4 (&b)[2][NV], uint32_t k) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                b[i][v] = k + i < k1 && row[v] ? load_scales(row[v], 16 * (k + i), n16, align[v]) : make_uint4(0, 0, 0, 0);
+    };
+    load(buf[0], k0);
+    load(buf[1], k0 + 2);
+    for (uint32_t k = k0; k < k1; k += 4) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (k + 2 * h + i < k1 && !put(buf[h][i])) return;
+            load(buf[h], k + 2 * h + 4);
+        }
+    }
+}
+
 // Lane l of a quad holds four words of one row; afterwards it holds word l of
 // the quad's four rows.
 __device__ __forceinline__ uint4 transpose4(uint4 v, uint32_t lane)
@@ -213,14 +241,71 @@ __device__ __forceinline__ uint4 transpose4(uint4 v, uint32_t lane)
     return v;
 }
 
+__device__ __forceinline__ void put_patches(uint8_t* at, uint32_t c, uint32_t r, uint4 v, uint32_t lane)
+{
+    *reinterpret_cast<uint4*>(at + c * kPatch + 16 * r) = transpose4(v, lane);
+}
+
+// Rows of x that belong to expert e: offsets cut to [0, m], none where they decrease.
+__device__ __forceinline__ void expert_rows(const MatmulArgs& A, uint32_t e, uint32_t& lo, uint32_t& hi)
+{
+    lo = 0, hi = A.m;
+    if (A.offsets) {
+        lo = uint32_t(min(max(A.offsets[e], 0), int(A.m)));
+        hi = max(lo, uint32_t(min(max(A.offsets[e + 1], 0), int(A.m))));
+    }
+}
+
+// By one warp: token tiles of `tile` rows before each expert, and all of them.
+__device__ __forceinline__ void count_tiles(const MatmulArgs& A, uint32_t tile, uint32_t* pref, uint32_t lane)
+{
+    const uint32_t groups = A.experts ? A.experts : 1;
+    uint32_t sum = 0;
+    for (uint32_t e0 = 0; e0 < groups; e0 += 32) {
+        uint32_t lo = 0, hi = 0;
+        if (e0 + lane < groups) expert_rows(A, e0 + lane, lo, hi);
+        const uint32_t c = (hi - lo + tile - 1) / tile;
+        uint32_t inc = c;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const uint32_t up = __shfl_up_sync(~0u, inc, o);
+            if (lane >= o) inc += up;
+        }
+        if (e0 + lane < groups) pref[e0 + lane] = sum + inc - c;
+        sum += __shfl_sync(~0u, inc, 31);
+    }
+    if (lane == 0) pref[groups] = sum;
+}
+
+// Tile t: its expert, its rows of x from x0 (to x1 at most), its first row of
+// the expert's matrix.  nw tiles of tile_w weight rows to each token tile.
+struct Tile {
+    uint32_t e, x0, x1, w0;
+};
+__device__ __forceinline__ Tile tile_of(const MatmulArgs& A, const uint32_t* pref, uint32_t t, uint32_t nw, uint32_t tile_x,
+                                        uint32_t tile_w)
+{
+    const uint32_t tt = t / nw;
+    uint32_t lo = 0, hi = A.experts ? A.experts - 1 : 0;
+    while (lo < hi) {
+        const uint32_t mid = (lo + hi + 1) / 2;
+        if (pref[mid] <= tt) lo = mid;
+        else hi = mid - 1;
+    }
+    uint32_t a, b;
+    expert_rows(A, lo, a, b);
+    return Tile{lo, a + (tt - pref[lo]) * tile_x, b, (t % nw) * tile_w};
+}
+
+// ---- few tokens: the weights are P ---------------------------------------------------------------------------------
+
 template <int BN>
 struct Shape {
-    static constexpr int kHalves = BN > 128 ? 2 : 1;              // 128-row halves of Q
     static constexpr int kTileBytes = (kP + BN) * kStepBytes;
-    static constexpr int kScaleBytes = (1 + kHalves) * 4 * kPatch;
+    static constexpr int kScaleBytes = 2 * 4 * kPatch;
     static constexpr int kStageBytes = kTileBytes + kScaleBytes;
     static constexpr int kStages = BN == 128 || BN == 64 ? 3 : 4;
-    static constexpr int kScaleCols = 16 * (1 + kHalves);         // tensor-memory columns of one stage's scales
+    static constexpr int kScaleCols = 32;                         // tensor-memory columns of one stage's scales
     static constexpr int kCols = BN + kStages * kScaleCols;
     static constexpr int kAlloc = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
     static constexpr int kSmem = kStages * kStageBytes;
@@ -236,7 +321,7 @@ struct Control {
     uint32_t pref[1];   // token tiles before each expert, and all of them: one entry an expert, and one
 };
 
-template <int BN, bool XP, typename T>
+template <int BN, typename T>
 __global__ void __launch_bounds__(kThreads, Shape<BN>::kBlocks)
 matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, MatmulArgs A, uint32_t split)
 {
@@ -251,8 +336,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     uint8_t* patches = smem + NS * S::kTileBytes;
 
-    const uint32_t tile_x = XP ? kP : BN, tile_w = XP ? BN : kP;
-    const uint32_t nw = (A.n + tile_w - 1) / tile_w;
+    const uint32_t nw = (A.n + kP - 1) / kP;
     const uint32_t groups = A.experts ? A.experts : 1;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) mbar_init(&full[i], 1), mbar_init(&scaled[i], 4), mbar_init(&empty[i], 1);
@@ -261,56 +345,20 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
         dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    auto bounds = [&](uint32_t e, uint32_t& lo, uint32_t& hi) {
-        lo = 0, hi = A.m;
-        if (A.offsets) {
-            lo = uint32_t(min(max(A.offsets[e], 0), int(A.m)));
-            hi = uint32_t(min(max(A.offsets[e + 1], 0), int(A.m)));
-            hi = max(lo, hi);
-        }
-    };
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&C.tmem_base)), "r"(S::kAlloc) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         fence_before();
     }
-    if (warp == 3) {
-        uint32_t sum = 0;
-        for (uint32_t e0 = 0; e0 < groups; e0 += 32) {
-            uint32_t lo = 0, hi = 0;
-            if (e0 + lane < groups) bounds(e0 + lane, lo, hi);
-            uint32_t c = (hi - lo + tile_x - 1) / tile_x, inc = c;
-#pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                uint32_t up = __shfl_up_sync(~0u, inc, o);
-                if (lane >= o) inc += up;
-            }
-            if (e0 + lane < groups) pref[e0 + lane] = sum + inc - c;
-            sum += __shfl_sync(~0u, inc, 31);
-        }
-        if (lane == 0) pref[groups] = sum;
-    }
+    if (warp == 3) count_tiles(A, BN, pref, lane);
+    grid_wait();   // what is read from here on may come from the kernel before
     __syncthreads();
     fence_after();
-    grid_wait();   // what is read from here on may come from the kernel before
     const uint32_t tmem = C.tmem_base;
     const uint32_t rank = split > 1 ? cluster_rank() : 0;
     const uint32_t steps = (A.k + kStep - 1) / kStep;
     const uint32_t k0 = uint64_t(steps) * rank / split, k1 = uint64_t(steps) * (rank + 1) / split;
 
-    struct Tile { uint32_t e, x0, x1, w0; };   // expert, its rows of x from x0 (to x1 at most), first row of its matrix
-    auto tile_of = [&](uint32_t t) {
-        const uint32_t tt = t / nw;
-        uint32_t lo = 0, hi = groups - 1;
-        while (lo < hi) {
-            uint32_t mid = (lo + hi + 1) / 2;
-            if (pref[mid] <= tt) lo = mid;
-            else hi = mid - 1;
-        }
-        uint32_t a, b;
-        bounds(lo, a, b);
-        return Tile{lo, a + (tt - pref[lo]) * tile_x, b, (t % nw) * tile_w};
-    };
     const uint32_t first = blockIdx.x / split, stride = gridDim.x / split;
     // a split tile's sums are joined once a cluster; the grid has a cluster for every tile that ordered offsets make
     const uint32_t tiles = split > 1 ? min(pref[groups] * nw, stride) : pref[groups] * nw;
@@ -320,15 +368,15 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
         bool ok = true;
         if (lane == 0) {
             for (uint32_t t = first; t < tiles && ok; t += stride) {
-                const Tile c = tile_of(t);
+                const Tile c = tile_of(A, pref, t, nw, BN, kP);
                 const int xr = int(c.x0), wr = int(c.e * A.n + c.w0);
                 for (uint32_t k = k0; k < k1; ++k, ++it) {
                     const uint32_t s = it % NS;
                     if (it >= NS && !(ok = mbar_wait(&empty[s], (it / NS - 1) & 1, &dead))) break;
                     uint8_t* at = smem + s * S::kTileBytes;
                     mbar_expect(&full[s], S::kTileBytes);
-                    tma_load(at, &map_p, &full[s], int(k * kStepBytes), XP ? xr : wr);
-                    tma_load(at + kP * kStepBytes, &map_q, &full[s], int(k * kStepBytes), XP ? wr : xr);
+                    tma_load(at, &map_p, &full[s], int(k * kStepBytes), wr);
+                    tma_load(at + kP * kStepBytes, &map_q, &full[s], int(k * kStepBytes), xr);
                 }
             }
             // nothing may be in flight into this block's memory when it ends
@@ -353,13 +401,11 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         copy_patch(tp + 4 * j, desc_patch(sc + j * kPatch));
-#pragma unroll
-                        for (int h = 0; h < S::kHalves; ++h)
-                            copy_patch(tq + 4 * (j * S::kHalves + h), desc_patch(sc + (4 + 4 * h + j) * kPatch));
+                        copy_patch(tq + 4 * j, desc_patch(sc + (4 + j) * kPatch));
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        mma(tmem, desc_tile(p + 32 * j), desc_tile(q + 32 * j), idesc, tp + 4 * j, tq + 4 * j * S::kHalves,
+                        mma(tmem, desc_tile(p + 32 * j), desc_tile(q + 32 * j), idesc, tp + 4 * j, tq + 4 * j,
                             k > k0 || j > 0);
                     mma_commit(&empty[s]);
                 }
@@ -370,97 +416,41 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
             if (done) mbar_wait(&acc_full, (done - 1) & 1, &never);
         }
     } else if (warp >= 4 && warp < 8) {
-        // scales, PD steps ahead in registers
-        constexpr int PD = 4, NV = 1 + S::kHalves;
-        const uint32_t w = warp - 4;
-        const uint32_t r = w * 8 + lane / 4, c = lane % 4;   // this lane's row 32 c + r of each 128
-        const uint32_t n16 = A.k / 16;
+        const uint32_t r = (warp - 4) * 8 + lane / 4, c = lane % 4, i = 32 * c + r;   // this lane's row of each 128
+        const uint32_t n16 = A.k / 16, align[2] = {A.p_align, A.q_align};
         uint32_t it = 0;
         bool ok = true;
         for (uint32_t t = first; t < tiles && ok; t += stride) {
-            const Tile tl = tile_of(t);
-            const uint8_t* row[NV];
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const uint32_t i = 32 * c + r + (v == 2 ? 128 : 0);
-                const bool isx = (v == 0) == XP;
-                const bool in = v == 0 || i < BN;
-                row[v] = nullptr;
-                if (isx) {
-                    if (in && tl.x0 + i < tl.x1) row[v] = (v == 0 ? A.p_scales : A.q_scales) + uint64_t(tl.x0 + i) * n16;
-                } else {
-                    if (in && tl.w0 + i < A.n)
-                        row[v] = (v == 0 ? A.p_scales : A.q_scales) + (uint64_t(tl.e) * A.n + tl.w0 + i) * n16;
-                }
-            }
-            auto load = [&](int v, uint32_t k) {
-                if (k >= k1 || !row[v]) return make_uint4(0, 0, 0, 0);
-                return load_scales(row[v], 16 * k, n16, v == 0 ? A.p_align : A.q_align);
-            };
-            uint4 buf[PD][NV];
-#pragma unroll
-            for (int d = 0; d < PD; ++d)
-#pragma unroll
-                for (int v = 0; v < NV; ++v) buf[d][v] = load(v, k0 + d);
-            for (uint32_t kb = k0; kb < k1 && ok; kb += PD) {
-#pragma unroll
-                for (int d = 0; d < PD; ++d) {
-                    if (kb + d < k1 && ok) {
-                        const uint32_t s = it % NS;
-                        if (it >= NS) ok = mbar_wait(&empty[s], (it / NS - 1) & 1, &dead);
-                        ok = __all_sync(~0u, ok);
-                        if (ok) {
-                            uint8_t* at = patches + s * S::kScaleBytes;
-#pragma unroll
-                            for (int v = 0; v < NV; ++v) {
-                                *reinterpret_cast<uint4*>(at + (4 * v + c) * kPatch + 16 * r) = transpose4(buf[d][v], lane);
-                                buf[d][v] = load(v, kb + d + PD);
-                            }
-                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&scaled[s]);
-                            ++it;
-                        }
-                    }
-                }
-            }
+            const Tile tl = tile_of(A, pref, t, nw, BN, kP);
+            const uint8_t* const row[2] = {
+                tl.w0 + i < A.n ? A.p_scales + (uint64_t(tl.e) * A.n + tl.w0 + i) * n16 : nullptr,
+                i < BN && tl.x0 + i < tl.x1 ? A.q_scales + uint64_t(tl.x0 + i) * n16 : nullptr};
+            stream_scales<2>(row, align, n16, k0, k1, [&](const uint4 (&v)[2]) {
+                const uint32_t s = it % NS;
+                if (it >= NS) ok = mbar_wait(&empty[s], (it / NS - 1) & 1, &dead);
+                ok = __all_sync(~0u, ok);
+                if (!ok) return false;
+                uint8_t* at = patches + s * S::kScaleBytes;
+                put_patches(at, c, r, v[0], lane);
+                put_patches(at + 4 * kPatch, c, r, v[1], lane);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&scaled[s]);
+                ++it;
+                return true;
+            });
         }
     } else if (warp >= 8) {
         const uint32_t w = warp - 8;
         uint32_t n = 0;
         for (uint32_t t = first; t < tiles; t += stride, ++n) {
-            const Tile c = tile_of(t);
+            const Tile c = tile_of(A, pref, t, nw, BN, kP);
             if (!__all_sync(~0u, mbar_wait(&acc_full, n & 1, &dead))) break;
             fence_after();
             const uint32_t row = 32 * w + lane;
             const float tw = A.w_scale[A.w_scale_each ? c.e : 0];
             T* y = static_cast<T*>(A.y);
-            if (XP) {
-                const uint32_t m = c.x0 + row;
-                const bool in = m < c.x1;
-                const float sc = in ? A.x_scale[A.x_scale_rows ? m : 0] * tw : 0.0f;
-                T* out = y + uint64_t(in ? m : 0) * A.y_stride + c.w0;
-#pragma unroll 1
-                for (int j = 0; j < BN; j += 16) {
-                    uint32_t v[16];
-                    tmem_load16(v, tmem + (w << 21) + j);
-                    tmem_load_wait();
-                    if (in) {
-                        if (A.y_vec && c.w0 + j + 16 <= A.n) {
-                            alignas(32) T o[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = from_f32<T>(__uint_as_float(v[i]) * sc);
-                            const uint4* o4 = reinterpret_cast<const uint4*>(o);
-#pragma unroll
-                            for (int i = 0; i < int(sizeof(o) / 16); ++i) reinterpret_cast<uint4*>(out + j)[i] = o4[i];
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (c.w0 + j + i < A.n) out[j + i] = from_f32<T>(__uint_as_float(v[i]) * sc);
-                        }
-                    }
-                }
-            } else if (split == 1) {
+            if (split == 1) {
                 const uint32_t nn = c.w0 + row;
 #pragma unroll 1
                 for (int j = 0; j < BN; j += 16) {
@@ -498,8 +488,8 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
         // the cluster's blocks hold the same tile's sums over their parts of K: each adds up, in rank order, the
         // columns (tokens) that fall to it
         cluster_sync();
-        if (first < tiles && !XP) {
-            const Tile c = tile_of(first);
+        if (first < tiles) {
+            const Tile c = tile_of(A, pref, first, nw, BN, kP);
             const float tw = A.w_scale[A.w_scale_each ? c.e : 0];
             const uint32_t there = min(c.x1 - c.x0, uint32_t(BN));
             for (uint32_t i = rank * kThreads + threadIdx.x; i < there * kP; i += split * kThreads) {
@@ -517,6 +507,263 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
     if (warp == 2) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kAlloc));
+    }
+}
+
+// ---- many tokens: two SMs on a tile of 256 tokens by 256 weight rows -------------------------------------------------
+//
+// Block 0 of a cluster of two (the leader) issues the instructions for both:
+// each block holds the codes of its own 128 tokens and of half of the weight
+// rows, the scales of its tokens and of all weight rows, and its tokens' half
+// of the sums.  A tile so takes 2/3 of the bytes from the L2 that two tiles of
+// 128 by 256 take, and that is what bounds it.  The eight output warps take
+// all sums of a tile into registers before they write any, so that the next
+// tile's products begin at once.
+
+struct Pair {
+    static constexpr int kStages = 5;
+    static constexpr int kThreads = 512;
+    static constexpr int kTileBytes = 2 * kP * kStepBytes;          // a block's: 128 tokens, 128 weight rows
+    static constexpr int kScaleBytes = 3 * 4 * kPatch;              // 128 tokens, 256 weight rows
+    static constexpr int kScaleCols = 48;
+    static constexpr int kSmem = kStages * (kTileBytes + kScaleBytes);
+    static_assert(256 + kStages * kScaleCols <= 512, "tensor memory");
+};
+
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t addr)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// Into this block's memory, counted on the leader's barrier.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+        ::"r"(saddr(dst)), "l"(map), "r"(bar), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void copy_patch_pair(uint32_t tmem, uint64_t desc)
+{
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t add)
+{
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %6, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p; }"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(add) : "memory");
+}
+// Arrives on the barrier at this offset in both blocks.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(saddr(bar)), "h"(uint16_t(3)) : "memory");
+}
+
+__device__ __forceinline__ void tmem_load32(uint32_t* v, uint32_t addr)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]),
+          "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]),
+          "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr));
+}
+
+// 32 bytes to a 32-byte boundary: a whole sector.
+__device__ __forceinline__ void store32(void* p, const uint32_t* w)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float, float, float) { return 0; }
+
+template <typename T>
+__global__ void __launch_bounds__(Pair::kThreads, 1)
+matmul_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, MatmulArgs A)
+{
+    constexpr int NS = Pair::kStages;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Control<NS>& C = *reinterpret_cast<Control<NS>*>(smem + Pair::kSmem);
+    uint64_t *full = C.full, *scaled = C.scaled, *empty = C.empty, &acc_full = C.acc_full, &acc_empty = C.acc_empty;
+    uint32_t* pref = C.pref;
+    volatile int& dead = C.dead;
+
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, rank = cluster_rank();
+    uint8_t* patches = smem + NS * Pair::kTileBytes;
+    const uint32_t nw = (A.n + 255) / 256;
+    const uint32_t groups = A.experts ? A.experts : 1;
+    if (threadIdx.x == 0) {
+        // full, scaled and acc_empty are used in the leader alone
+        for (int i = 0; i < NS; ++i) mbar_init(&full[i], 1), mbar_init(&scaled[i], 8), mbar_init(&empty[i], 1);
+        mbar_init(&acc_full, 1);
+        mbar_init(&acc_empty, 16);
+        C.dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&C.tmem_base)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        fence_before();
+    }
+    grid_wait();
+    if (warp == 3) count_tiles(A, 256, pref, lane);
+    __syncwarp();
+    __syncthreads();
+    cluster_sync();
+    fence_after();
+    const uint32_t tmem = C.tmem_base;
+    const uint32_t steps = (A.k + kStep - 1) / kStep;
+    const uint32_t tiles = pref[groups] * nw;
+    const uint32_t first = blockIdx.x / 2, stride = gridDim.x / 2;
+
+    // registers of the launch: 4 warpgroups x 128; the two of the output take 168 each, the others 88
+    if (warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 0) {
+        uint32_t it = 0;
+        bool ok = true;
+        if (lane == 0) {
+            for (uint32_t t = first; t < tiles && ok; t += stride) {
+                const Tile c = tile_of(A, pref, t, nw, 256, 256);
+                const int xr = int(c.x0 + rank * kP), wr = int(c.e * A.n + c.w0 + rank * kP);
+                for (uint32_t k = 0; k < steps; ++k, ++it) {
+                    const uint32_t s = it % NS;
+                    if (it >= NS && !(ok = mbar_wait(&empty[s], (it / NS - 1) & 1, &dead))) break;
+                    uint8_t* at = smem + s * Pair::kTileBytes;
+                    const uint32_t bar = at_rank(saddr(&full[s]), 0);
+                    if (rank == 0) mbar_expect(&full[s], 2 * Pair::kTileBytes);
+                    tma_load_pair(at, &map_x, bar, int(k * kStepBytes), xr);
+                    tma_load_pair(at + kP * kStepBytes, &map_w, bar, int(k * kStepBytes), wr);
+                }
+            }
+            // nothing may be in flight into either block's memory when they end: the leader sees both blocks' loads
+            volatile int never = 0;
+            if (rank == 0)
+                for (uint32_t i = it > NS ? it - NS : 0; i < it; ++i) mbar_wait(&full[i % NS], (i / NS) & 1, &never);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = (1u << 7) | (1u << 10) | (uint32_t(256 / 8) << 17) | (16u << 24);
+            uint32_t it = 0, done = 0;
+            bool ok = true;
+            for (uint32_t t = first; t < tiles && ok; t += stride) {
+                if (done > 0 && !(ok = mbar_wait(&acc_empty, (done - 1) & 1, &dead))) break;
+                fence_after();
+                for (uint32_t k = 0; k < steps; ++k, ++it) {
+                    const uint32_t s = it % NS;
+                    if (!(ok = mbar_wait(&full[s], (it / NS) & 1, &dead) && mbar_wait(&scaled[s], (it / NS) & 1, &dead))) break;
+                    fence_after();
+                    const uint32_t p = saddr(smem + s * Pair::kTileBytes), q = p + kP * kStepBytes;
+                    const uint32_t sc = saddr(patches + s * Pair::kScaleBytes);
+                    const uint32_t tp = tmem + 256 + s * Pair::kScaleCols, tq = tp + 16;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        copy_patch_pair(tp + 4 * j, desc_patch(sc + j * kPatch));
+                        copy_patch_pair(tq + 8 * j, desc_patch(sc + (4 + j) * kPatch));
+                        copy_patch_pair(tq + 8 * j + 4, desc_patch(sc + (8 + j) * kPatch));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_pair(tmem, desc_tile(p + 32 * j), desc_tile(q + 32 * j), idesc, tp + 4 * j, tq + 8 * j, k > 0 || j > 0);
+                    mma_commit_pair(&empty[s]);
+                }
+                mma_commit_pair(&acc_full);
+                ++done;
+            }
+            volatile int never = 0;
+            if (done) mbar_wait(&acc_full, (done - 1) & 1, &never);
+        }
+    } else if (warp >= 4) {
+        const uint32_t r = (warp - 4) * 8 + lane / 4, c = lane % 4, i = 32 * c + r;
+        const uint32_t n16 = A.k / 16, align[3] = {A.p_align, A.q_align, A.q_align};
+        uint32_t it = 0;
+        bool ok = true;
+        for (uint32_t t = first; t < tiles && ok; t += stride) {
+            const Tile tl = tile_of(A, pref, t, nw, 256, 256);
+            const uint32_t xi = tl.x0 + rank * kP + i, wi = tl.w0 + i;
+            const uint8_t* const w = A.q_scales + (uint64_t(tl.e) * A.n + wi) * n16;
+            const uint8_t* const row[3] = {xi < tl.x1 ? A.p_scales + uint64_t(xi) * n16 : nullptr, wi < A.n ? w : nullptr,
+                                           wi + kP < A.n ? w + uint64_t(kP) * n16 : nullptr};
+            stream_scales<3>(row, align, n16, 0, steps, [&](const uint4 (&v)[3]) {
+                const uint32_t s = it % NS;
+                if (it >= NS) ok = mbar_wait(&empty[s], (it / NS - 1) & 1, &dead);
+                ok = __all_sync(~0u, ok);
+                if (!ok) return false;
+                uint8_t* at = patches + s * Pair::kScaleBytes;
+#pragma unroll
+                for (int h = 0; h < 3; ++h) put_patches(at + 4 * h * kPatch, c, r, v[h], lane);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) arrive_cluster(at_rank(saddr(&scaled[s]), 0));
+                ++it;
+                return true;
+            });
+        }
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        const uint32_t quarter = warp % 4, half = (warp - 8) / 4;
+        uint32_t n = 0;
+        for (uint32_t t = first; t < tiles; t += stride, ++n) {
+            const Tile c = tile_of(A, pref, t, nw, 256, 256);
+            if (!__all_sync(~0u, mbar_wait(&acc_full, n & 1, &dead))) break;
+            fence_after();
+            uint32_t v[128];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) tmem_load32(v + 32 * j, tmem + (quarter << 21) + 128 * half + 32 * j);
+            tmem_load_wait();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(at_rank(saddr(&acc_empty), 0));
+            const uint32_t m = c.x0 + rank * kP + 32 * quarter + lane, n0 = c.w0 + 128 * half;
+            if (m < c.x1 && n0 < A.n) {
+                const float sc = A.x_scale[A.x_scale_rows ? m : 0] * A.w_scale[A.w_scale_each ? c.e : 0];
+                T* out = static_cast<T*>(A.y) + uint64_t(m) * A.y_stride + n0;
+                constexpr int N = 32 / sizeof(T);   // values of a sector
+#pragma unroll
+                for (int j = 0; j < 128; j += N) {
+                    if (A.y_vec && n0 + j + N <= A.n) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            w[q] = sizeof(T) == 4 ? __float_as_uint(__uint_as_float(v[j + q]) * sc)
+                                                  : pack2(__uint_as_float(v[j + 2 * q % N]) * sc,
+                                                          __uint_as_float(v[j + (2 * q + 1) % N]) * sc, T());
+                        store32(out + j, w);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < N; ++q)
+                            if (n0 + j + q < A.n) out[j + q] = from_f32<T>(__uint_as_float(v[j + q]) * sc);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 2) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
     }
 }
 
@@ -565,55 +812,89 @@ uint32_t scale_align(const void* p, uint32_t k)
     return a % 16 == 0 ? 16 : a % 8 == 0 ? 8 : a % 4 == 0 ? 4 : 1;
 }
 
-template <int BN, bool XP, typename T>
+// Shared memory of a kernel whose tile counts take an entry an expert, allowed.
+template <typename K>
+cudaError_t allow_smem(K kernel, int smem)
+{
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
+template <int BN, typename T>
 int launch(MatmulArgs A, const dcr_nvfp4& x, const dcr_nvfp4& w, uint32_t split, bool dependent, cudaStream_t s)
 {
     using S = Shape<BN>;
-    const dcr_nvfp4 &p = XP ? x : w, &q = XP ? w : x;
     const uint64_t groups = A.experts ? A.experts : 1, wrows = groups * A.n;
     CUtensorMap mp, mq;
-    if (!tile_map(&mp, p.codes, XP ? A.m : wrows, A.k, kP) || !tile_map(&mq, q.codes, XP ? wrows : A.m, A.k, BN))
+    if (!tile_map(&mp, w.codes, wrows, A.k, kP) || !tile_map(&mq, x.codes, A.m, A.k, BN))
         return set_error(DCR_ERR_CUDA, "dcr_nvfp4_matmul: tensor map");
-    A.p_scales = static_cast<const uint8_t*>(p.scales);
-    A.q_scales = static_cast<const uint8_t*>(q.scales);
-    A.p_align = scale_align(p.scales, A.k);
-    A.q_align = scale_align(q.scales, A.k);
-    const uint32_t tx = XP ? kP : BN, tw = XP ? BN : kP;
+    A.p_scales = static_cast<const uint8_t*>(w.scales);
+    A.q_scales = static_cast<const uint8_t*>(x.scales);
+    A.p_align = scale_align(w.scales, A.k);
+    A.q_align = scale_align(x.scales, A.k);
     // an expert's rows end in a tile of their own: at most one more tile an expert that has any
-    uint64_t xt = (A.m + tx - 1) / tx;
-    if (A.experts) xt = A.m / tx + (A.m < groups ? A.m : groups);
-    const uint64_t tiles = xt * ((A.n + tw - 1) / tw);
+    uint64_t xt = (A.m + BN - 1) / BN;
+    if (A.experts) xt = A.m / BN + (A.m < groups ? A.m : groups);
+    const uint64_t tiles = xt * ((A.n + kP - 1) / kP);
     uint64_t grid = uint64_t(sm_count()) * S::kBlocks;
     if (tiles < grid || split > 1) grid = tiles * split;
     if (grid == 0 || grid >= 1ull << 31) return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: matrix too large");
-    auto kernel = matmul_kernel<BN, XP, T>;
+    auto kernel = matmul_kernel<BN, T>;
     const int smem = S::kSmem + int(sizeof(Control<S::kStages>) + 4 * groups);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return cuda_error(e, "NVFP4 product attributes");
     const LaunchAttrs at(grid, kThreads, size_t(smem), split, dependent, s);
     e = cudaLaunchKernelEx(&at.cfg, kernel, mp, mq, A, split);
     return e == cudaSuccess ? DCR_OK : cuda_error(e, "NVFP4 product launch");
 }
 
+template <typename T>
+int launch_pair(MatmulArgs A, const dcr_nvfp4& x, const dcr_nvfp4& w, bool dependent, cudaStream_t s)
+{
+    const uint64_t groups = A.experts ? A.experts : 1, wrows = groups * A.n;
+    CUtensorMap mx, mw;
+    if (!tile_map(&mx, x.codes, A.m, A.k, kP) || !tile_map(&mw, w.codes, wrows, A.k, kP))
+        return set_error(DCR_ERR_CUDA, "dcr_nvfp4_matmul: tensor map");
+    A.p_scales = static_cast<const uint8_t*>(x.scales);
+    A.q_scales = static_cast<const uint8_t*>(w.scales);
+    A.p_align = scale_align(x.scales, A.k);
+    A.q_align = scale_align(w.scales, A.k);
+    auto kernel = matmul_pair_kernel<T>;
+    const int smem = Pair::kSmem + int(sizeof(Control<Pair::kStages>) + 4 * groups);
+    cudaError_t e = allow_smem(kernel, smem);
+    if (e != cudaSuccess) return cuda_error(e, "NVFP4 product attributes");
+    // as many clusters as fit at once (GPCs with an odd number of SMs leave one out)
+    static const int resident = [&] {
+        const LaunchAttrs at(2, Pair::kThreads, size_t(smem), 2, false, nullptr);
+        int n = 0;
+        return cudaOccupancyMaxActiveClusters(&n, kernel, &at.cfg) == cudaSuccess && n > 0 ? n : 1;
+    }();
+    uint64_t xt = (A.m + 255) / 256;
+    if (A.experts) xt = A.m / 256 + (A.m < groups ? A.m : groups);
+    const uint64_t tiles = xt * ((A.n + 255) / 256);
+    const LaunchAttrs at(2 * (tiles < uint64_t(resident) ? tiles : resident), Pair::kThreads, size_t(smem), 2, dependent, s);
+    e = cudaLaunchKernelEx(&at.cfg, kernel, mx, mw, A);
+    return e == cudaSuccess ? DCR_OK : cuda_error(e, "NVFP4 product launch");
+}
+
 // Which kernel: the weights are P, with Q as narrow as the tokens allow, until
-// there are enough tokens that 128-token by 256-weight tiles fill the SMs.
-// Few tiles are split over K among the blocks of a cluster.
+// there are enough tokens that tiles of 256 by 256 give every pair of SMs
+// something to do.  Few tiles are split over K among the blocks of a cluster.
 template <typename T>
 int choose(const MatmulArgs& A, const dcr_nvfp4& x, const dcr_nvfp4& w, bool dependent, cudaStream_t s)
 {
     const uint64_t groups = A.experts ? A.experts : 1, sms = uint64_t(sm_count());
     const uint64_t each = (A.m + groups - 1) / groups;
-    const uint64_t wide = ((each + 127) / 128) * ((A.n + 255) / 256) * groups;
-    if (each > 64 && wide >= sms / 2) return launch<256, true, T>(A, x, w, 1, dependent, s);
+    const uint64_t wide = ((each + 255) / 256) * ((A.n + 255) / 256) * groups;
+    if (each > 64 && wide >= sms / 4) return launch_pair<T>(A, x, w, dependent, s);
     const uint64_t bn = each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : 128;
     const uint64_t tiles = ((each + bn - 1) / bn) * ((A.n + 127) / 128) * groups;
     const uint32_t steps = (A.k + kStep - 1) / kStep;
     uint32_t split = 1;
     while (split < 8 && tiles * split * 2 <= sms * 2 && steps >= split * 4) split *= 2;
-    if (bn == 16) return launch<16, false, T>(A, x, w, split, dependent, s);
-    if (bn == 32) return launch<32, false, T>(A, x, w, split, dependent, s);
-    if (bn == 64) return launch<64, false, T>(A, x, w, split, dependent, s);
-    return launch<128, false, T>(A, x, w, split, dependent, s);
+    if (bn == 16) return launch<16, T>(A, x, w, split, dependent, s);
+    if (bn == 32) return launch<32, T>(A, x, w, split, dependent, s);
+    if (bn == 64) return launch<64, T>(A, x, w, split, dependent, s);
+    return launch<128, T>(A, x, w, split, dependent, s);
 }
 
 }  // namespace

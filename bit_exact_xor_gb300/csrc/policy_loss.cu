@@ -6,9 +6,9 @@
 // exp((x - m) / T), each thread against its own maximum first) and the
 // gradient.  Long rows are shared by the blocks of a cluster, which exchange
 // (m, s) through distributed shared memory once.  What does not fit on the
-// chip that way is read a second time.  Differences to the maximum are taken
-// before the temperature is applied: they are exact or small, and a row of
-// the type's lowest value behaves like any other constant row.
+// chip that way is read a second time.
+#include <type_traits>
+
 #include "ops_internal.h"
 
 namespace dcr {
@@ -38,8 +38,7 @@ __device__ __forceinline__ float exp2_fast(float v)
     return r;
 }
 
-// The 16 bytes of a word as its values, and their largest (a NaN is passed
-// over), without a value for each on the way where two share a register.
+// The 16 bytes of a word as its values.
 template <typename T>
 struct Word;
 template <>
@@ -101,26 +100,58 @@ struct Word<__half> {
     }
 };
 
-template <typename T>
-__device__ __forceinline__ float word_max(const uint4& q)
+// Largest value of a word (a NaN is passed over), two at a time where two
+// share a register.
+__device__ __forceinline__ float word_max(const uint4& q, float)
 {
-    float v[Word<T>::kN];
-    Word<T>::values(q, v);
-    float m = v[0];
-#pragma unroll
-    for (int i = 1; i < Word<T>::kN; ++i) m = fmaxf(m, v[i]);
-    return m;
+    return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)), fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+}
+template <typename T>
+__device__ __forceinline__ float word_max(const uint4& q, T)
+{
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    const T2* h = reinterpret_cast<const T2*>(&q);
+    const T2 a = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(to_f32(a.x), to_f32(a.y));
 }
 
-// Sum of exp((x - m) / T) over a word; sc = log2(e) / T.
-template <typename T>
-__device__ __forceinline__ float word_sum(const uint4& q, float m, float sc)
+// exp((x - m) / T) = 2^(x sc - m sc), sc = log2(e) / T: one multiply-add with
+// the rounded product msc = m sc, whose rounding error is the same factor on
+// every term (the row's sum is corrected for it once).  A maximum so large
+// that msc could overflow (a row of the type's lowest values) takes the
+// difference first.
+struct Exponent {
+    float sc, m, msc;
+    bool plain;
+    __device__ __forceinline__ Exponent(float m_, float sc_) : sc(sc_), m(m_), msc(m_ * sc_), plain(fabsf(m_ * sc_) < 1e30f) {}
+    template <bool PLAIN>
+    __device__ __forceinline__ float of(float x) const
+    {
+        return exp2_fast(PLAIN ? fmaf(x, sc, -msc) : (x - m) * sc);
+    }
+    // log2 of the factor that all terms carry
+    __device__ __forceinline__ float excess() const { return plain ? fmaf(m, sc, -msc) : 0.0f; }
+};
+
+template <typename T, bool PLAIN>
+__device__ __forceinline__ float word_sum(const uint4& q, const Exponent& e)
 {
     float v[Word<T>::kN], s[2] = {0.0f, 0.0f};
     Word<T>::values(q, v);
 #pragma unroll
-    for (int i = 0; i < Word<T>::kN; ++i) s[i & 1] += exp2_fast((v[i] - m) * sc);
+    for (int i = 0; i < Word<T>::kN; ++i) s[i & 1] += e.of<PLAIN>(v[i]);
     return s[0] + s[1];
+}
+
+template <typename T>
+__device__ __forceinline__ bool word_nan(const uint4& q)
+{
+    float v[Word<T>::kN];
+    Word<T>::values(q, v);
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < Word<T>::kN; ++i) nan |= v[i] != v[i];
+    return nan;
 }
 
 // Statistics of two stretches of a row, joined.  Maxima that are equal
@@ -166,6 +197,30 @@ struct Row {
     }
 };
 
+// Sum of exp((x - m) / T) over words whose largest value is m.
+template <typename T, int NV>
+__device__ __forceinline__ float words_sum(const uint4 (&q)[NV], float m, float sc)
+{
+    float s = 0.0f;
+    if (fabsf(m) == INFINITY || m != m) {
+        // nothing above -inf: nothing to add; +inf: exp(inf - inf) is not a number, although the sum is not one only if
+        // a value is not
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) nan |= word_nan<T>(q[i]);
+        return nan ? NAN : 0.0f;
+    }
+    const Exponent e(m, sc);
+    if (e.plain) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s += word_sum<T, true>(q[i], e);
+        return s * exp2f(-e.excess());
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s += word_sum<T, false>(q[i], e);
+    return s;
+}
+
 // Loss of a row and its derivative by the log-probability.
 __device__ __forceinline__ void row_loss(const LossArgs& A, uint64_t row, float lp, float& loss, float& slope)
 {
@@ -208,35 +263,12 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 3 : 8) loss_kernel(LossArgs A,
         for (int i = 0; i < NV; ++i) q[i] = in.load(first + i * step);
         xy = to_f32(x[y]);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) m = fmaxf(m, word_max<T>(q[i]));
-#pragma unroll
-        for (int i = 0; i < NV; ++i) s += word_sum<T>(q[i], m, sc);
-        // no value above -inf: nothing to add; +inf: exp(inf - inf) is not a number, although the sum is not one only
-        // if a value is not
-        if (m == -INFINITY || m == INFINITY) {
-            bool nan = false;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float v[N];
-                Word<T>::values(q[i], v);
-#pragma unroll
-                for (int j = 0; j < N; ++j) nan |= v[j] != v[j];
-            }
-            s = nan ? NAN : 0.0f;
-        }
+        for (int i = 0; i < NV; ++i) m = fmaxf(m, word_max(q[i], T()));
+        s = words_sum<T, NV>(q, m, sc);
         for (uint32_t k = first + NV * step; k < in.words; k += step) {
-            const uint4 e = in.load(k);
-            const float m2 = word_max<T>(e);
-            float s2 = word_sum<T>(e, m2, sc);
-            if (m2 == -INFINITY || m2 == INFINITY) {
-                float v[N];
-                Word<T>::values(e, v);
-                bool nan = false;
-#pragma unroll
-                for (int j = 0; j < N; ++j) nan |= v[j] != v[j];
-                s2 = nan ? NAN : 0.0f;
-            }
-            join(m, s, m2, s2, sc);
+            const uint4 e[1] = {in.load(k)};
+            const float m2 = word_max(e[0], T());
+            join(m, s, m2, words_sum<T, 1>(e, m2, sc), sc);
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) join(m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o), sc);
@@ -278,28 +310,18 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 3 : 8) loss_kernel(LossArgs A,
     }
     if (!g) return;
 
-    // grad_j = c ([j = y] - exp((x_j - m) / T) / s): the words as they were read, where the gradient's row lies on the
-    // same offset from a 16-byte boundary
-    const float d = on ? -c / s : 0.0f;
+    // grad_j = c ([j = y] - exp((x_j - m) / T) / s).  The words go out as they came in where the gradient's row lies on
+    // the same offset from a 16-byte boundary.
+    const Exponent e(m, sc);
+    const float d = on ? -c / s * exp2f(-e.excess()) : 0.0f;
     const Row<T> out(g, vocab);
     const bool same = out.skip == in.skip;
-    const uint32_t ypos = in.skip + y;
-    auto put = [&](uint32_t k, const uint4& e) {
+    auto put = [&](uint32_t k, const uint4& q, auto plain) {
         if (k >= in.words) return;
         float v[N];
-        if (on) {
-            Word<T>::values(e, v);
+        Word<T>::values(q, v);
 #pragma unroll
-            for (int j = 0; j < N; ++j) v[j] = d * exp2_fast((v[j] - m) * sc);
-            if (ypos / N == k) {
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (ypos % N == j) v[j] += c;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < N; ++j) v[j] = 0.0f;
-        }
+        for (int j = 0; j < N; ++j) v[j] = d * e.of<decltype(plain)::value>(v[j]);
         if (same && in.whole(k)) {
             *reinterpret_cast<uint4*>(out.base + uint64_t(k) * N) = Word<T>::pack(v);
         } else {
@@ -310,9 +332,29 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 3 : 8) loss_kernel(LossArgs A,
             }
         }
     };
+    auto put_all = [&](auto plain) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) put(first + i * step, q[i]);
-    for (uint32_t k = first + NV * step; k < in.words; k += step) put(k, on ? in.load(k) : make_uint4(0, 0, 0, 0));
+        for (int i = 0; i < NV; ++i) put(first + i * step, q[i], plain);
+        for (uint32_t k = first + NV * step; k < in.words; k += step) put(k, in.load(k), plain);
+    };
+    if (!on) {
+        for (uint32_t k = rank * TH + threadIdx.x; k < out.words; k += step) {
+            if (out.whole(k)) {
+                *reinterpret_cast<uint4*>(out.base + uint64_t(k) * N) = make_uint4(0, 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const uint32_t at = k * N + j;
+                    if (at >= out.skip && at - out.skip < vocab) out.base[at] = from_f32<T>(0.0f);
+                }
+            }
+        }
+        return;
+    }
+    if (e.plain) put_all(std::true_type());
+    else put_all(std::false_type());
+    // the token's own value, by the thread that wrote its word
+    if ((in.skip + y) / N % step == first % step) g[y] = from_f32<T>(c + d * (e.plain ? e.of<true>(xy) : e.of<false>(xy)));
 }
 
 // The rows' losses summed in a fixed order: thread i takes rows i, i + 1024,

@@ -169,6 +169,32 @@ def test_product_sizes(m, n, k, out):
     _close(dcr.nvfp4_matmul(x, w, dtype=DT[out]), y, mag, k, out)
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("m,n,k", [(65, 9800, 32), (128, 9984, 256), (257, 5000, 96), (300, 5121, 544), (511, 5120, 1312),
+                                   (700, 3333, 2080), (1030, 2048, 288)])
+def test_product_of_many_tokens(m, n, k, out):
+    # enough 256 by 256 tiles for the paired blocks; sizes around the tile's, odd row lengths (no 32-byte stores)
+    x, w = _operand(m, k, m + k, per_row=True), _operand(n, k, n + k, std=0.05)
+    y, mag = _product(x, w)
+    _close(dcr.nvfp4_matmul(x, w, dtype=DT[out]), y, mag, k, out)
+
+
+@pytest.mark.parametrize("counts", [[300, 0, 90, 257, 5], [256, 256, 0, 513], [0, 0, 700], [65] * 12])
+def test_experts_of_many_tokens(counts):
+    n, k, m, e = 2600, 416, sum(counts), len(counts)
+    off = [0]
+    for c in counts:
+        off.append(off[-1] + c)
+    x, w = _operand(m, k, m, per_row=True), _operand(e * n, k, e)
+    w = dcr.Nvfp4(w.codes, w.scales, torch.linspace(0.5, 2.0, e, device="cuda"))
+    y, mag = _product(x, w, off)
+    for out in ("bf16", "f32"):
+        got = dcr.nvfp4_matmul(x, w, offsets=torch.tensor(off, dtype=torch.int32, device="cuda"), dtype=DT[out])
+        _close(got, y, mag, k, out)
+        assert torch.equal(got, dcr.nvfp4_matmul(x, w, offsets=torch.tensor(off, dtype=torch.int32, device="cuda"), dtype=DT[out]))
+    dcr.ops_status()
+
+
 @pytest.mark.parametrize("m", [1, 5, 40, 150, 300])
 def test_product_of_a_long_k(m):
     k = 16384 + 32

@@ -169,6 +169,19 @@ def test_masked_vocabulary(dtype, vocab):
     assert float(dcr.token_logprobs(z, tokens.cuda())[0]) == float("-inf")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("vocab", [30, 5000, 70000])
+def test_constant_rows_of_any_size(dtype, vocab):
+    # the type's lowest and highest value, and others: softmax is uniform whatever the constant
+    for v in (torch.finfo(DT[dtype]).min, torch.finfo(DT[dtype]).max, 0.0, -50.0):
+        z = torch.full((2, vocab), v, dtype=DT[dtype], device="cuda")
+        t = torch.tensor([0, vocab - 1], device="cuda")
+        one = torch.ones(2, device="cuda")
+        _, lp, grad = dcr.policy_loss(z, t, -one, one, one, clip_high=1e9)
+        assert float((lp + math.log(vocab)).abs().max()) <= 1e-5
+        assert bool(torch.isfinite(grad).all())
+
+
 def test_non_finite_logits_show():
     for vocab in (64, 9000, 70000):
         z = torch.zeros(4, vocab, device="cuda")
