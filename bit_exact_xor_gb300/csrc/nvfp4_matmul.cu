@@ -11,9 +11,9 @@
 // come by TMA (128-byte swizzle, one box a step).  The instruction wants the
 // scales in tensor memory, for 64 values of K as a 32-lane by 4-column patch
 // in which lane r, column c holds the four scales of row 32 c + r; the scale
-// warps read each row's 16 scales as one word of 16 bytes, transpose 4 x 4
-// words between the four lanes that hold rows r, 32 + r, 64 + r and 96 + r,
-// and leave the patches in shared memory, from where tcgen05.cp takes them.
+// warps read the rows' scales (16 bytes a row and step), transpose 4 x 4 words
+// between the four lanes that hold rows r, 32 + r, 64 + r and 96 + r, and
+// leave the patches in shared memory, from where tcgen05.cp takes them.
 //
 // Warps: 0 TMA, 1 tensor core, 2 tensor memory, 4-7 scales, 8-11 output.
 #include <cuda.h>
@@ -28,8 +28,8 @@ constexpr int kThreads = 384;
 constexpr int kP = 128;             // rows of P
 constexpr int kStepBytes = 128;     // codes of a row in one step of K
 constexpr int kStep = 256;          // values of K in one step
-constexpr int kPatch = 544;         // a scale patch: 512 bytes, and 32 so that four patches start in different banks
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kPatch = 512;         // a scale patch: 32 lanes x 16 bytes
+constexpr int64_t kWaitCycles = 4000000000ll;   // two seconds at the highest clock
 
 __device__ int g_error;             // a wait ran out (dcr_ops_status reads and clears it)
 
@@ -68,27 +68,20 @@ __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity)
 {
     uint32_t ok;
     asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
         : "=r"(ok) : "r"(saddr(b)), "r"(parity) : "memory");
     return ok != 0;
 }
 
-__device__ __forceinline__ uint64_t now_ns()
-{
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-// Every wait is bounded: after two seconds, or once another warp of the block
+// Every wait is bounded: after about two seconds, or once another warp of the block
 // has given up, it returns false and the block winds down.
 __device__ __forceinline__ bool mbar_wait_long(uint64_t* b, uint32_t parity, volatile int* dead)
 {
-    const uint64_t t0 = now_ns();
+    const int64_t t0 = clock64();   // (the global timer takes microseconds to read)
     while (!*dead) {
         for (int i = 0; i < 64; ++i)
             if (mbar_try(b, parity)) return true;
-        if (now_ns() - t0 > kWaitNs) {
+        if (clock64() - t0 > kWaitCycles) {
             *dead = 1;
             atomicExch(&g_error, 1);
         }
@@ -149,6 +142,18 @@ __device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::l
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// One lane of a converged warp.  The warp that issues the tensor core's
+// instructions runs its loop as a whole and elects a lane only around them,
+// so that their operands are formed in uniform registers: issued from a loop
+// of one lane they took 50 ns each (4096 x 4096 x 14336: 179 us instead of
+// 100 without the scales' loads).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
+}
+
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -196,54 +201,98 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* row, uint32_t k16, u
     return u.v;
 }
 
-// The scales of this lane's rows (one of each NV, or null) for steps k0 to
-// k1, handed to `put` step by step.  Two steps' loads go out together, four
-// ahead of their use: they share a 32-byte sector.
-template <int NV, typename F>
-__device__ __forceinline__ void stream_scales(const uint8_t* const (&row)[NV], const uint32_t (&align)[NV], uint32_t n16,
-                                              uint32_t k0, uint32_t k1, F put)
+// A 4 x 4 matrix whose columns lie in the lanes l, l ^ A, l ^ B, l ^ (A | B),
+// transposed: `at` is this lane's column.
+template <int A, int B, typename V, typename X>
+__device__ __forceinline__ void transpose4(V& v0, V& v1, V& v2, V& v3, uint32_t at, X xchg)
 {
-    uint4 buf[2][2][NV];
-    auto load = [&](uint4 (&b)[2][NV], uint32_t k) {
+    const bool b0 = at & 1, b1 = at & 2;
+    V t;
+    t = xchg(b0 ? v0 : v1, A);
+    (b0 ? v0 : v1) = t;
+    t = xchg(b0 ? v2 : v3, A);
+    (b0 ? v2 : v3) = t;
+    t = xchg(b1 ? v0 : v2, B);
+    (b1 ? v0 : v2) = t;
+    t = xchg(b1 ? v1 : v3, B);
+    (b1 ? v1 : v3) = t;
+}
+__device__ __forceinline__ uint32_t xchg1(uint32_t v, int mask) { return __shfl_xor_sync(~0u, v, mask); }
+__device__ __forceinline__ uint4 xchg4(uint4 v, int mask)
+{
+    return make_uint4(xchg1(v.x, mask), xchg1(v.y, mask), xchg1(v.z, mask), xchg1(v.w, mask));
+}
+
+// The scale warps' work.  Lane l of warp w owns row 32 (l / 8) + 8 w + l % 8
+// of each 128-row operand.  Scales are loaded for four steps at once: the
+// four lanes of a quad read 64 bytes of one row together, for each of their
+// four rows in turn (8 rows of 64 bytes an instruction instead of 32 rows of
+// 16, which bound the tensor core), and hand them to their owners by
+// shuffles.  Two such groups are in registers, the next tile's among them.
+//   rows(t, v, base, left): tile t's first row of this lane's quad of operand v, and how many rows there are from it on
+//   put(v): one step's scales of this lane's rows; false ends it
+template <int NV, typename R, typename F>
+__device__ __forceinline__ void stream_scales(uint32_t lane, const uint32_t (&align)[NV], uint32_t n16, uint32_t k0, uint32_t k1,
+                                              uint32_t first, uint32_t tiles, uint32_t stride, R rows, F put)
+{
+    if (first >= tiles) return;
+    const uint8_t* base[NV];
+    int32_t left[NV];
+    uint32_t lt = first, lk = k0;
+    auto set_rows = [&] {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) rows(lt, v, base[v], left[v]);
+    };
+    set_rows();
+    auto load = [&](uint4 (&b)[NV][4]) {
+        const uint32_t k = lk + lane % 4;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                b[i][v] = k + i < k1 && row[v] ? load_scales(row[v], 16 * (k + i), n16, align[v]) : make_uint4(0, 0, 0, 0);
-    };
-    load(buf[0], k0);
-    load(buf[1], k0 + 2);
-    for (uint32_t k = k0; k < k1; k += 4) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (k + 2 * h + i < k1 && !put(buf[h][i])) return;
-            load(buf[h], k + 2 * h + 4);
+            for (int q = 0; q < 4; ++q)
+                b[v][q] = lt < tiles && k < k1 && q < left[v] ? load_scales(base[v] + uint64_t(q) * n16, 16 * k, n16, align[v])
+                                                              : make_uint4(0, 0, 0, 0);
+        lk += 4;
+        if (lk >= k1) {
+            lk = k0;
+            lt += stride;
+            if (lt < tiles) set_rows();
         }
+    };
+    const uint32_t groups = ((tiles - first + stride - 1) / stride) * ((k1 - k0 + 3) / 4);
+    uint32_t k = k0;
+    auto use = [&](uint4 (&b)[NV][4]) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) transpose4<1, 2>(b[v][0], b[v][1], b[v][2], b[v][3], lane, xchg4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (k + i >= k1) break;
+            uint4 one[NV];
+#pragma unroll
+            for (int v = 0; v < NV; ++v) one[v] = b[v][i];
+            if (!put(one)) return false;
+        }
+        k = k + 4 < k1 ? k + 4 : k0;
+        return true;
+    };
+    uint4 b0[NV][4], b1[NV][4];
+    load(b0);
+    load(b1);
+    for (uint32_t g = 0; g < groups; g += 2) {
+        if (!use(b0)) return;
+        load(b0);
+        if (g + 1 >= groups || !use(b1)) return;
+        load(b1);
     }
 }
 
-// Lane l of a quad holds four words of one row; afterwards it holds word l of
-// the quad's four rows.
-__device__ __forceinline__ uint4 transpose4(uint4 v, uint32_t lane)
+// One operand's scales of a step into its four patches: the four lanes that
+// hold rows r, 32 + r, 64 + r and 96 + r exchange words, so that each writes
+// 16 bytes of one patch.
+__device__ __forceinline__ void put_patches(uint8_t* at, uint32_t warp, uint4 v, uint32_t lane)
 {
-    const bool b0 = lane & 1, b1 = lane & 2;
-    uint32_t t;
-    t = __shfl_xor_sync(~0u, b0 ? v.x : v.y, 1);
-    (b0 ? v.x : v.y) = t;
-    t = __shfl_xor_sync(~0u, b0 ? v.z : v.w, 1);
-    (b0 ? v.z : v.w) = t;
-    t = __shfl_xor_sync(~0u, b1 ? v.x : v.z, 2);
-    (b1 ? v.x : v.z) = t;
-    t = __shfl_xor_sync(~0u, b1 ? v.y : v.w, 2);
-    (b1 ? v.y : v.w) = t;
-    return v;
-}
-
-__device__ __forceinline__ void put_patches(uint8_t* at, uint32_t c, uint32_t r, uint4 v, uint32_t lane)
-{
-    *reinterpret_cast<uint4*>(at + c * kPatch + 16 * r) = transpose4(v, lane);
+    transpose4<8, 16>(v.x, v.y, v.z, v.w, lane / 8, xchg1);
+    *reinterpret_cast<uint4*>(at + (lane / 8) * kPatch + 16 * (8 * warp + lane % 8)) = v;
 }
 
 // Rows of x that belong to expert e: offsets cut to [0, m], none where they decrease.
@@ -333,7 +382,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
     uint32_t* pref = C.pref;
     volatile int& dead = C.dead;
 
-    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     uint8_t* patches = smem + NS * S::kTileBytes;
 
     const uint32_t nw = (A.n + kP - 1) / kP;
@@ -354,7 +403,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
     grid_wait();   // what is read from here on may come from the kernel before
     __syncthreads();
     fence_after();
-    const uint32_t tmem = C.tmem_base;
+    const uint32_t tmem = __shfl_sync(~0u, C.tmem_base, 0);
     const uint32_t rank = split > 1 ? cluster_rank() : 0;
     const uint32_t steps = (A.k + kStep - 1) / kStep;
     const uint32_t k0 = uint64_t(steps) * rank / split, k1 = uint64_t(steps) * (rank + 1) / split;
@@ -363,6 +412,10 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
     // a split tile's sums are joined once a cluster; the grid has a cluster for every tile that ordered offsets make
     const uint32_t tiles = split > 1 ? min(pref[groups] * nw, stride) : pref[groups] * nw;
 
+    // registers of the launch: 3 warpgroups x 80, as 56 (TMA, tensor core) + 128 (scales) + 56 (output)
+    static_assert(S::kBlocks == 2, "80 registers a thread");
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
         uint32_t it = 0;
         bool ok = true;
@@ -384,63 +437,69 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
             for (uint32_t i = it > NS ? it - NS : 0; i < it; ++i) mbar_wait(&full[i % NS], (i / NS) & 1, &never);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = (1u << 7) | (1u << 10) | (uint32_t(BN / 8) << 17) | (8u << 24);
-            uint32_t it = 0, done = 0;
-            bool ok = true;
-            for (uint32_t t = first; t < tiles && ok; t += stride) {
-                if (done > 0 && !(ok = mbar_wait(&acc_empty, (done - 1) & 1, &dead))) break;
-                fence_after();
-                for (uint32_t k = k0; k < k1; ++k, ++it) {
-                    const uint32_t s = it % NS;
-                    if (!(ok = mbar_wait(&full[s], (it / NS) & 1, &dead) && mbar_wait(&scaled[s], (it / NS) & 1, &dead))) break;
-                    fence_after();
-                    const uint32_t p = saddr(smem + s * S::kTileBytes), q = p + kP * kStepBytes;
-                    const uint32_t sc = saddr(patches + s * S::kScaleBytes);
-                    const uint32_t tp = tmem + BN + s * S::kScaleCols, tq = tp + 16;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        copy_patch(tp + 4 * j, desc_patch(sc + j * kPatch));
-                        copy_patch(tq + 4 * j, desc_patch(sc + (4 + j) * kPatch));
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma(tmem, desc_tile(p + 32 * j), desc_tile(q + 32 * j), idesc, tp + 4 * j, tq + 4 * j,
-                            k > k0 || j > 0);
-                    mma_commit(&empty[s]);
-                }
-                mma_commit(&acc_full);
-                ++done;
-            }
-            volatile int never = 0;
-            if (done) mbar_wait(&acc_full, (done - 1) & 1, &never);
-        }
-    } else if (warp >= 4 && warp < 8) {
-        const uint32_t r = (warp - 4) * 8 + lane / 4, c = lane % 4, i = 32 * c + r;   // this lane's row of each 128
-        const uint32_t n16 = A.k / 16, align[2] = {A.p_align, A.q_align};
-        uint32_t it = 0;
+        constexpr uint32_t idesc = (1u << 7) | (1u << 10) | (uint32_t(BN / 8) << 17) | (8u << 24);
+        const uint32_t base = saddr(smem), pbase = saddr(patches);
+        uint32_t done = 0, s = 0, phase = 0;
         bool ok = true;
         for (uint32_t t = first; t < tiles && ok; t += stride) {
-            const Tile tl = tile_of(A, pref, t, nw, BN, kP);
-            const uint8_t* const row[2] = {
-                tl.w0 + i < A.n ? A.p_scales + (uint64_t(tl.e) * A.n + tl.w0 + i) * n16 : nullptr,
-                i < BN && tl.x0 + i < tl.x1 ? A.q_scales + uint64_t(tl.x0 + i) * n16 : nullptr};
-            stream_scales<2>(row, align, n16, k0, k1, [&](const uint4 (&v)[2]) {
-                const uint32_t s = it % NS;
-                if (it >= NS) ok = mbar_wait(&empty[s], (it / NS - 1) & 1, &dead);
-                ok = __all_sync(~0u, ok);
-                if (!ok) return false;
-                uint8_t* at = patches + s * S::kScaleBytes;
-                put_patches(at, c, r, v[0], lane);
-                put_patches(at + 4 * kPatch, c, r, v[1], lane);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (done > 0) ok = __all_sync(~0u, mbar_wait(&acc_empty, (done - 1) & 1, &dead));
+            if (!ok) break;
+            fence_after();
+            for (uint32_t k = k0; k < k1; ++k) {
+                ok = mbar_wait(&full[s], phase, &dead) && mbar_wait(&scaled[s], phase, &dead);
+                if (!(ok = __all_sync(~0u, ok))) break;
+                fence_after();
+                const uint32_t p = base + s * S::kTileBytes;
+                const uint32_t tp = tmem + BN + s * S::kScaleCols, tq = tp + 16;
+                const uint64_t dp = desc_tile(p), dq = desc_tile(p + kP * kStepBytes), ds = desc_patch(pbase + s * S::kScaleBytes);
+                if (elect_one()) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        copy_patch(tp + 4 * j, ds + j * (kPatch / 16));
+                        copy_patch(tq + 4 * j, ds + (4 + j) * (kPatch / 16));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma(tmem, dp + 2 * j, dq + 2 * j, idesc, tp + 4 * j, tq + 4 * j, k > k0 || j > 0);
+                    mma_commit(&empty[s]);
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&scaled[s]);
-                ++it;
-                return true;
-            });
+                if (++s == NS) s = 0, phase ^= 1;
+            }
+            if (elect_one()) mma_commit(&acc_full);
+            __syncwarp();
+            ++done;
         }
-    } else if (warp >= 8) {
+        volatile int never = 0;
+        if (done) mbar_wait(&acc_full, (done - 1) & 1, &never);
+    }
+    } else if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+        const uint32_t i = 32 * (lane / 8) + 8 * (warp - 4) + (lane % 8 & ~3u);   // the first row of this lane's quad
+        const uint32_t n16 = A.k / 16, align[2] = {A.p_align, A.q_align};
+        uint32_t s = 0, phase = 1;   // the first pass over the stages finds them empty
+        auto rows = [&](uint32_t t, int v, const uint8_t*& base, int32_t& left) {
+            const Tile tl = tile_of(A, pref, t, nw, BN, kP);
+            if (v == 0) {
+                base = A.p_scales + (uint64_t(tl.e) * A.n + tl.w0 + i) * n16;
+                left = int32_t(A.n) - int32_t(tl.w0 + i);
+            } else {
+                base = A.q_scales + uint64_t(tl.x0 + i) * n16;
+                left = i < BN ? int32_t(tl.x1) - int32_t(tl.x0 + i) : 0;
+            }
+        };
+        stream_scales<2>(lane, align, n16, k0, k1, first, tiles, stride, rows, [&](const uint4 (&v)[2]) {
+            if (!__all_sync(~0u, mbar_wait(&empty[s], phase, &dead))) return false;
+            uint8_t* at = patches + s * S::kScaleBytes;
+            put_patches(at, warp - 4, v[0], lane);
+            put_patches(at + 4 * kPatch, warp - 4, v[1], lane);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&scaled[s]);
+            if (++s == NS) s = 0, phase ^= 1;
+            return true;
+        });
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const uint32_t w = warp - 8;
         uint32_t n = 0;
         for (uint32_t t = first; t < tiles; t += stride, ++n) {
@@ -510,60 +569,20 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
     }
 }
 
-// ---- many tokens: two SMs on a tile of 256 tokens by 256 weight rows -------------------------------------------------
+// ---- many tokens: tiles of 128 tokens by 256 weight rows -----------------------------------------------------------
 //
-// Block 0 of a cluster of two (the leader) issues the instructions for both:
-// each block holds the codes of its own 128 tokens and of half of the weight
-// rows, the scales of its tokens and of all weight rows, and its tokens' half
-// of the sums.  A tile so takes 2/3 of the bytes from the L2 that two tiles of
-// 128 by 256 take, and that is what bounds it.  The eight output warps take
-// all sums of a tile into registers before they write any, so that the next
-// tile's products begin at once.
+// The eight output warps take all sums of a tile into registers before they
+// write any, so that the next tile's products begin at once.
 
-struct Pair {
-    static constexpr int kStages = 5;
+struct Wide {
     static constexpr int kThreads = 512;
-    static constexpr int kTileBytes = 2 * kP * kStepBytes;          // a block's: 128 tokens, 128 weight rows
+    static constexpr int kStages = 4;
+    static constexpr int kTileBytes = (kP + 256) * kStepBytes;
     static constexpr int kScaleBytes = 3 * 4 * kPatch;              // 128 tokens, 256 weight rows
     static constexpr int kScaleCols = 48;
     static constexpr int kSmem = kStages * (kTileBytes + kScaleBytes);
     static_assert(256 + kStages * kScaleCols <= 512, "tensor memory");
 };
-
-__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank)
-{
-    uint32_t a;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-    return a;
-}
-__device__ __forceinline__ void arrive_cluster(uint32_t addr)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-// Into this block's memory, counted on the leader's barrier.
-__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
-        ::"r"(saddr(dst)), "l"(map), "r"(bar), "r"(x), "r"(y) : "memory");
-}
-__device__ __forceinline__ void copy_patch_pair(uint32_t tmem, uint64_t desc)
-{
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
-}
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t add)
-{
-    asm volatile(
-        "{ .reg .pred p; setp.ne.u32 p, %6, 0;\n"
-        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p; }"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(add) : "memory");
-}
-// Arrives on the barrier at this offset in both blocks.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar)
-{
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 ::"r"(saddr(bar)), "h"(uint16_t(3)) : "memory");
-}
 
 __device__ __forceinline__ void tmem_load32(uint32_t* v, uint32_t addr)
 {
@@ -596,134 +615,130 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __half)
 __device__ __forceinline__ uint32_t pack2(float, float, float) { return 0; }
 
 template <typename T>
-__global__ void __launch_bounds__(Pair::kThreads, 1)
-matmul_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, MatmulArgs A)
+__global__ void __launch_bounds__(Wide::kThreads, 1)
+matmul_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, MatmulArgs A)
 {
-    constexpr int NS = Pair::kStages;
+    using S = Wide;
+    constexpr int NS = S::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
-    Control<NS>& C = *reinterpret_cast<Control<NS>*>(smem + Pair::kSmem);
+    Control<NS>& C = *reinterpret_cast<Control<NS>*>(smem + S::kSmem);
     uint64_t *full = C.full, *scaled = C.scaled, *empty = C.empty, &acc_full = C.acc_full, &acc_empty = C.acc_empty;
     uint32_t* pref = C.pref;
     volatile int& dead = C.dead;
 
-    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, rank = cluster_rank();
-    uint8_t* patches = smem + NS * Pair::kTileBytes;
+    const uint32_t warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+    uint8_t* patches = smem + NS * S::kTileBytes;
     const uint32_t nw = (A.n + 255) / 256;
     const uint32_t groups = A.experts ? A.experts : 1;
     if (threadIdx.x == 0) {
-        // full, scaled and acc_empty are used in the leader alone
-        for (int i = 0; i < NS; ++i) mbar_init(&full[i], 1), mbar_init(&scaled[i], 8), mbar_init(&empty[i], 1);
+        for (int i = 0; i < NS; ++i) mbar_init(&full[i], 1), mbar_init(&scaled[i], 4), mbar_init(&empty[i], 1);
         mbar_init(&acc_full, 1);
-        mbar_init(&acc_empty, 16);
+        mbar_init(&acc_empty, 8);
         C.dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&C.tmem_base)), "r"(512) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&C.tmem_base)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         fence_before();
     }
     grid_wait();
-    if (warp == 3) count_tiles(A, 256, pref, lane);
+    if (warp == 3) count_tiles(A, kP, pref, lane);
     __syncwarp();
     __syncthreads();
-    cluster_sync();
     fence_after();
-    const uint32_t tmem = C.tmem_base;
+    const uint32_t tmem = __shfl_sync(~0u, C.tmem_base, 0);
     const uint32_t steps = (A.k + kStep - 1) / kStep;
-    const uint32_t tiles = pref[groups] * nw;
-    const uint32_t first = blockIdx.x / 2, stride = gridDim.x / 2;
+    const uint32_t tiles = pref[groups] * nw, first = blockIdx.x, stride = gridDim.x;
 
-    // registers of the launch: 4 warpgroups x 128; the two of the output take 168 each, the others 88
-    if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 0) {
-        uint32_t it = 0;
-        bool ok = true;
-        if (lane == 0) {
-            for (uint32_t t = first; t < tiles && ok; t += stride) {
-                const Tile c = tile_of(A, pref, t, nw, 256, 256);
-                const int xr = int(c.x0 + rank * kP), wr = int(c.e * A.n + c.w0 + rank * kP);
-                for (uint32_t k = 0; k < steps; ++k, ++it) {
-                    const uint32_t s = it % NS;
-                    if (it >= NS && !(ok = mbar_wait(&empty[s], (it / NS - 1) & 1, &dead))) break;
-                    uint8_t* at = smem + s * Pair::kTileBytes;
-                    const uint32_t bar = at_rank(saddr(&full[s]), 0);
-                    if (rank == 0) mbar_expect(&full[s], 2 * Pair::kTileBytes);
-                    tma_load_pair(at, &map_x, bar, int(k * kStepBytes), xr);
-                    tma_load_pair(at + kP * kStepBytes, &map_w, bar, int(k * kStepBytes), wr);
+    // registers of the launch: 4 warpgroups x 128, as 56 (TMA, tensor core) + 152 (scales) + 2 x 152 (output)
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            if (lane == 0) {
+                for (uint32_t t = first; t < tiles && ok; t += stride) {
+                    const Tile c = tile_of(A, pref, t, nw, kP, 256);
+                    const int xr = int(c.x0), wr = int(c.e * A.n + c.w0);
+                    for (uint32_t k = 0; k < steps; ++k, ++it) {
+                        const uint32_t s = it % NS;
+                        if (it >= NS && !(ok = mbar_wait(&empty[s], (it / NS - 1) & 1, &dead))) break;
+                        uint8_t* at = smem + s * S::kTileBytes;
+                        mbar_expect(&full[s], S::kTileBytes);
+                        tma_load(at, &map_x, &full[s], int(k * kStepBytes), xr);
+                        tma_load(at + kP * kStepBytes, &map_w, &full[s], int(k * kStepBytes), wr);
+                    }
                 }
-            }
-            // nothing may be in flight into either block's memory when they end: the leader sees both blocks' loads
-            volatile int never = 0;
-            if (rank == 0)
+                // nothing may be in flight into this block's memory when it ends
+                volatile int never = 0;
                 for (uint32_t i = it > NS ? it - NS : 0; i < it; ++i) mbar_wait(&full[i % NS], (i / NS) & 1, &never);
-        }
-    } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = (1u << 7) | (1u << 10) | (uint32_t(256 / 8) << 17) | (16u << 24);
-            uint32_t it = 0, done = 0;
+            }
+        } else if (warp == 1) {
+            constexpr uint32_t idesc = (1u << 7) | (1u << 10) | (uint32_t(256 / 8) << 17) | (8u << 24);
+            const uint32_t base = saddr(smem), pbase = saddr(patches);
+            uint32_t done = 0, s = 0, phase = 0;
             bool ok = true;
             for (uint32_t t = first; t < tiles && ok; t += stride) {
-                if (done > 0 && !(ok = mbar_wait(&acc_empty, (done - 1) & 1, &dead))) break;
+                if (done > 0) ok = __all_sync(~0u, mbar_wait(&acc_empty, (done - 1) & 1, &dead));
+            if (!ok) break;
                 fence_after();
-                for (uint32_t k = 0; k < steps; ++k, ++it) {
-                    const uint32_t s = it % NS;
-                    if (!(ok = mbar_wait(&full[s], (it / NS) & 1, &dead) && mbar_wait(&scaled[s], (it / NS) & 1, &dead))) break;
+                for (uint32_t k = 0; k < steps; ++k) {
+                    ok = mbar_wait(&full[s], phase, &dead) && mbar_wait(&scaled[s], phase, &dead);
+                if (!(ok = __all_sync(~0u, ok))) break;
                     fence_after();
-                    const uint32_t p = saddr(smem + s * Pair::kTileBytes), q = p + kP * kStepBytes;
-                    const uint32_t sc = saddr(patches + s * Pair::kScaleBytes);
-                    const uint32_t tp = tmem + 256 + s * Pair::kScaleCols, tq = tp + 16;
+                    const uint32_t p = base + s * S::kTileBytes;
+                    const uint32_t tp = tmem + 256 + s * S::kScaleCols, tq = tp + 16;
+                    const uint64_t dp = desc_tile(p), dq = desc_tile(p + kP * kStepBytes), ds = desc_patch(pbase + s * S::kScaleBytes);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        copy_patch_pair(tp + 4 * j, desc_patch(sc + j * kPatch));
-                        copy_patch_pair(tq + 8 * j, desc_patch(sc + (4 + j) * kPatch));
-                        copy_patch_pair(tq + 8 * j + 4, desc_patch(sc + (8 + j) * kPatch));
+                        for (int j = 0; j < 4; ++j) {
+                            copy_patch(tp + 4 * j, ds + j * (kPatch / 16));
+                            copy_patch(tq + 8 * j, ds + (4 + j) * (kPatch / 16));
+                            copy_patch(tq + 8 * j + 4, ds + (8 + j) * (kPatch / 16));
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) mma(tmem, dp + 2 * j, dq + 2 * j, idesc, tp + 4 * j, tq + 8 * j, k > 0 || j > 0);
+                        mma_commit(&empty[s]);
                     }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma_pair(tmem, desc_tile(p + 32 * j), desc_tile(q + 32 * j), idesc, tp + 4 * j, tq + 8 * j, k > 0 || j > 0);
-                    mma_commit_pair(&empty[s]);
+                    __syncwarp();
+                    if (++s == NS) s = 0, phase ^= 1;
                 }
-                mma_commit_pair(&acc_full);
+                if (elect_one()) mma_commit(&acc_full);
+                __syncwarp();
                 ++done;
             }
             volatile int never = 0;
             if (done) mbar_wait(&acc_full, (done - 1) & 1, &never);
         }
-    } else if (warp >= 4) {
-        const uint32_t r = (warp - 4) * 8 + lane / 4, c = lane % 4, i = 32 * c + r;
+    } else if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        const uint32_t i = 32 * (lane / 8) + 8 * (warp - 4) + (lane % 8 & ~3u);   // the first row of this lane's quad
         const uint32_t n16 = A.k / 16, align[3] = {A.p_align, A.q_align, A.q_align};
-        uint32_t it = 0;
-        bool ok = true;
-        for (uint32_t t = first; t < tiles && ok; t += stride) {
-            const Tile tl = tile_of(A, pref, t, nw, 256, 256);
-            const uint32_t xi = tl.x0 + rank * kP + i, wi = tl.w0 + i;
-            const uint8_t* const w = A.q_scales + (uint64_t(tl.e) * A.n + wi) * n16;
-            const uint8_t* const row[3] = {xi < tl.x1 ? A.p_scales + uint64_t(xi) * n16 : nullptr, wi < A.n ? w : nullptr,
-                                           wi + kP < A.n ? w + uint64_t(kP) * n16 : nullptr};
-            stream_scales<3>(row, align, n16, 0, steps, [&](const uint4 (&v)[3]) {
-                const uint32_t s = it % NS;
-                if (it >= NS) ok = mbar_wait(&empty[s], (it / NS - 1) & 1, &dead);
-                ok = __all_sync(~0u, ok);
-                if (!ok) return false;
-                uint8_t* at = patches + s * Pair::kScaleBytes;
+        uint32_t s = 0, phase = 1;   // the first pass over the stages finds them empty
+        auto rows = [&](uint32_t t, int v, const uint8_t*& base, int32_t& left) {
+            const Tile tl = tile_of(A, pref, t, nw, kP, 256);
+            const uint32_t wi = tl.w0 + i + (v == 2 ? kP : 0);
+            base = v == 0 ? A.p_scales + uint64_t(tl.x0 + i) * n16 : A.q_scales + (uint64_t(tl.e) * A.n + wi) * n16;
+            left = v == 0 ? int32_t(tl.x1) - int32_t(tl.x0 + i) : int32_t(A.n) - int32_t(wi);
+        };
+        stream_scales<3>(lane, align, n16, 0, steps, first, tiles, stride, rows, [&](const uint4 (&v)[3]) {
+            if (!__all_sync(~0u, mbar_wait(&empty[s], phase, &dead))) return false;
+            uint8_t* at = patches + s * S::kScaleBytes;
 #pragma unroll
-                for (int h = 0; h < 3; ++h) put_patches(at + 4 * h * kPatch, c, r, v[h], lane);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) arrive_cluster(at_rank(saddr(&scaled[s]), 0));
-                ++it;
-                return true;
-            });
-        }
-    }
+            for (int h = 0; h < 3; ++h) put_patches(at + 4 * h * kPatch, warp - 4, v[h], lane);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&scaled[s]);
+            if (++s == NS) s = 0, phase ^= 1;
+            return true;
+        });
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
         const uint32_t quarter = warp % 4, half = (warp - 8) / 4;
         uint32_t n = 0;
         for (uint32_t t = first; t < tiles; t += stride, ++n) {
-            const Tile c = tile_of(A, pref, t, nw, 256, 256);
+            const Tile c = tile_of(A, pref, t, nw, kP, 256);
             if (!__all_sync(~0u, mbar_wait(&acc_full, n & 1, &dead))) break;
             fence_after();
             uint32_t v[128];
@@ -732,8 +747,8 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             tmem_load_wait();
             fence_before();
             __syncwarp();
-            if (lane == 0) arrive_cluster(at_rank(saddr(&acc_empty), 0));
-            const uint32_t m = c.x0 + rank * kP + 32 * quarter + lane, n0 = c.w0 + 128 * half;
+            if (lane == 0) mbar_arrive(&acc_empty);
+            const uint32_t m = c.x0 + 32 * quarter + lane, n0 = c.w0 + 128 * half;
             if (m < c.x1 && n0 < A.n) {
                 const float sc = A.x_scale[A.x_scale_rows ? m : 0] * A.w_scale[A.w_scale_each ? c.e : 0];
                 T* out = static_cast<T*>(A.y) + uint64_t(m) * A.y_stride + n0;
@@ -760,10 +775,9 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     }
     __syncwarp();
     __syncthreads();
-    cluster_sync();
     if (warp == 2) {
         fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
     }
 }
 
@@ -848,44 +862,38 @@ int launch(MatmulArgs A, const dcr_nvfp4& x, const dcr_nvfp4& w, uint32_t split,
 }
 
 template <typename T>
-int launch_pair(MatmulArgs A, const dcr_nvfp4& x, const dcr_nvfp4& w, bool dependent, cudaStream_t s)
+int launch_wide(MatmulArgs A, const dcr_nvfp4& x, const dcr_nvfp4& w, bool dependent, cudaStream_t s)
 {
     const uint64_t groups = A.experts ? A.experts : 1, wrows = groups * A.n;
     CUtensorMap mx, mw;
-    if (!tile_map(&mx, x.codes, A.m, A.k, kP) || !tile_map(&mw, w.codes, wrows, A.k, kP))
+    if (!tile_map(&mx, x.codes, A.m, A.k, kP) || !tile_map(&mw, w.codes, wrows, A.k, 256))
         return set_error(DCR_ERR_CUDA, "dcr_nvfp4_matmul: tensor map");
     A.p_scales = static_cast<const uint8_t*>(x.scales);
     A.q_scales = static_cast<const uint8_t*>(w.scales);
     A.p_align = scale_align(x.scales, A.k);
     A.q_align = scale_align(w.scales, A.k);
-    auto kernel = matmul_pair_kernel<T>;
-    const int smem = Pair::kSmem + int(sizeof(Control<Pair::kStages>) + 4 * groups);
+    uint64_t xt = (A.m + kP - 1) / kP;
+    if (A.experts) xt = A.m / kP + (A.m < groups ? A.m : groups);
+    const uint64_t tiles = xt * ((A.n + 255) / 256);
+    auto kernel = matmul_wide_kernel<T>;
+    const int smem = Wide::kSmem + int(sizeof(Control<Wide::kStages>) + 4 * groups);
     cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return cuda_error(e, "NVFP4 product attributes");
-    // as many clusters as fit at once (GPCs with an odd number of SMs leave one out)
-    static const int resident = [&] {
-        const LaunchAttrs at(2, Pair::kThreads, size_t(smem), 2, false, nullptr);
-        int n = 0;
-        return cudaOccupancyMaxActiveClusters(&n, kernel, &at.cfg) == cudaSuccess && n > 0 ? n : 1;
-    }();
-    uint64_t xt = (A.m + 255) / 256;
-    if (A.experts) xt = A.m / 256 + (A.m < groups ? A.m : groups);
-    const uint64_t tiles = xt * ((A.n + 255) / 256);
-    const LaunchAttrs at(2 * (tiles < uint64_t(resident) ? tiles : resident), Pair::kThreads, size_t(smem), 2, dependent, s);
+    const LaunchAttrs at(tiles < uint64_t(sm_count()) ? tiles : sm_count(), Wide::kThreads, size_t(smem), 1, dependent, s);
     e = cudaLaunchKernelEx(&at.cfg, kernel, mx, mw, A);
     return e == cudaSuccess ? DCR_OK : cuda_error(e, "NVFP4 product launch");
 }
 
 // Which kernel: the weights are P, with Q as narrow as the tokens allow, until
-// there are enough tokens that tiles of 256 by 256 give every pair of SMs
+// there are enough tokens that tiles of 128 by 256 give half of the SMs
 // something to do.  Few tiles are split over K among the blocks of a cluster.
 template <typename T>
 int choose(const MatmulArgs& A, const dcr_nvfp4& x, const dcr_nvfp4& w, bool dependent, cudaStream_t s)
 {
     const uint64_t groups = A.experts ? A.experts : 1, sms = uint64_t(sm_count());
     const uint64_t each = (A.m + groups - 1) / groups;
-    const uint64_t wide = ((each + 255) / 256) * ((A.n + 255) / 256) * groups;
-    if (each > 64 && wide >= sms / 4) return launch_pair<T>(A, x, w, dependent, s);
+    const uint64_t wide = ((each + 127) / 128) * ((A.n + 255) / 256) * groups;
+    if (each > 64 && wide >= sms / 2) return launch_wide<T>(A, x, w, dependent, s);
     const uint64_t bn = each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : 128;
     const uint64_t tiles = ((each + bn - 1) / bn) * ((A.n + 127) / 128) * groups;
     const uint32_t steps = (A.k + kStep - 1) / kStep;
