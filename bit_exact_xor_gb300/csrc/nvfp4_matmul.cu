@@ -228,13 +228,14 @@ __device__ __forceinline__ uint4 xchg4(uint4 v, int mask)
 }
 
 // The scale warps' work.  Lane l of warp w owns row 32 (l / 8) + 8 w + l % 8
-// of each 128-row operand.  Scales are loaded for four steps at once: the
-// four lanes of a quad read 64 bytes of one row together, for each of their
-// four rows in turn (8 rows of 64 bytes an instruction instead of 32 rows of
-// 16, which bound the tensor core), and hand them to their owners by
-// shuffles.  Two such groups are in registers, the next tile's among them.
-//   rows(t, v, base, left): tile t's first row of this lane's quad of operand v, and how many rows there are from it on
+// of each 128-row operand.  Scales are loaded for two steps at once: two
+// lanes read 32 bytes (a sector) of one row together, then of the other's
+// row, and exchange what is not theirs.  kAhead such pairs are in registers,
+// the next tile's among them: a pair's load goes out six to eight steps ahead
+// of its use.
+//   rows(t, v, base, left): tile t's first row of this pair of lanes, of operand v, and how many rows there are from it on
 //   put(v): one step's scales of this lane's rows; false ends it
+constexpr int kAhead = 4;
 template <int NV, bool FAST, typename R, typename F>
 __device__ __forceinline__ void stream_scales(uint32_t lane, const uint32_t (&align)[NV], uint32_t n16, uint32_t k0, uint32_t k1,
                                               uint32_t first, uint32_t tiles, uint32_t stride, R rows, F put)
@@ -248,44 +249,44 @@ __device__ __forceinline__ void stream_scales(uint32_t lane, const uint32_t (&al
         for (int v = 0; v < NV; ++v) rows(lt, v, base[v], left[v]);
     };
     set_rows();
-    auto load = [&](uint4 (&b)[NV][4]) {
-        const uint32_t k = lk + lane % 4;
+    auto load = [&](uint4 (&b)[NV][2]) {
+        const uint32_t k = lk + lane % 2;
+        const bool there = lt < tiles && k < k1;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                b[v][q] = load_scales<FAST>(base[v] + uint64_t(q) * n16, 16 * k, n16, align[v], lt < tiles && k < k1 && q < left[v]);
-        lk += 4;
+            for (int q = 0; q < 2; ++q)
+                b[v][q] = load_scales<FAST>(base[v] + (q ? n16 : 0), 16 * k, n16, align[v], there && q < left[v]);
+        lk += 2;
         if (lk >= k1) {
             lk = k0;
             lt += stride;
             if (lt < tiles) set_rows();
         }
     };
-    const uint32_t groups = ((tiles - first + stride - 1) / stride) * ((k1 - k0 + 3) / 4);
+    uint32_t pairs = ((tiles - first + stride - 1) / stride) * ((k1 - k0 + 1) / 2);
     uint32_t k = k0;
-    auto use = [&](uint4 (&b)[NV][4]) {
+    auto use = [&](uint4 (&b)[NV][2]) {
+        uint4 one[NV], two[NV];
 #pragma unroll
-        for (int v = 0; v < NV; ++v) transpose4<1, 2>(b[v][0], b[v][1], b[v][2], b[v][3], lane, xchg4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (k + i >= k1) break;
-            uint4 one[NV];
-#pragma unroll
-            for (int v = 0; v < NV; ++v) one[v] = b[v][i];
-            if (!put(one)) return false;
+        for (int v = 0; v < NV; ++v) {
+            const uint4 t = xchg4(lane % 2 ? b[v][0] : b[v][1], 1);
+            one[v] = lane % 2 ? t : b[v][0];
+            two[v] = lane % 2 ? b[v][1] : t;
         }
-        k = k + 4 < k1 ? k + 4 : k0;
+        if (!put(one) || (k + 1 < k1 && !put(two))) return false;
+        k = k + 2 < k1 ? k + 2 : k0;
         return true;
     };
-    uint4 b0[NV][4], b1[NV][4];
-    load(b0);
-    load(b1);
-    for (uint32_t g = 0; g < groups; g += 2) {
-        if (!use(b0)) return;
-        load(b0);
-        if (g + 1 >= groups || !use(b1)) return;
-        load(b1);
+    uint4 buf[kAhead][NV][2];
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) load(buf[d]);
+    while (true) {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+            if (pairs-- == 0 || !use(buf[d])) return;
+            load(buf[d]);
+        }
     }
 }
 
@@ -477,7 +478,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
     }
     } else if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
-        const uint32_t i = 32 * (lane / 8) + 8 * (warp - 4) + (lane % 8 & ~3u);   // the first row of this lane's quad
+        const uint32_t i = 32 * (lane / 8) + 8 * (warp - 4) + (lane % 8 & ~1u);   // the first row of this pair of lanes
         const uint32_t n16 = A.k / 16, align[2] = {A.p_align, A.q_align};
         uint32_t s = 0, phase = 1;   // the first pass over the stages finds them empty
         auto rows = [&](uint32_t t, int v, const uint8_t*& base, int32_t& left) {
@@ -718,7 +719,7 @@ matmul_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         }
     } else if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-        const uint32_t i = 32 * (lane / 8) + 8 * (warp - 4) + (lane % 8 & ~3u);   // the first row of this lane's quad
+        const uint32_t i = 32 * (lane / 8) + 8 * (warp - 4) + (lane % 8 & ~1u);   // the first row of this pair of lanes
         const uint32_t n16 = A.k / 16, align[3] = {A.p_align, A.q_align, A.q_align};
         uint32_t s = 0, phase = 1;   // the first pass over the stages finds them empty
         auto rows = [&](uint32_t t, int v, const uint8_t*& base, int32_t& left) {
