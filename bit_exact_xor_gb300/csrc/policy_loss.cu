@@ -2,11 +2,11 @@
 // log-probabilities of tokens (include/dcr_ops.h).
 //
 // A row is read once: each thread keeps its share of it in registers, as
-// 16-byte words, between the statistics (maximum m and sum s of
-// exp((x - m) / T), each thread against its own maximum first) and the
-// gradient.  Long rows are shared by the blocks of a cluster, which exchange
-// (m, s) through distributed shared memory once.  What does not fit on the
-// chip that way is read a second time.
+// 16-byte words, between the statistics (maximum m, then the sum s of
+// exp((x - m) / T) against the block's maximum) and the gradient.  Long rows
+// are shared by the blocks of a cluster, which exchange (m, s) through
+// distributed shared memory once.  What does not fit on the chip that way is
+// read again.
 #include <type_traits>
 
 #include "ops_internal.h"
@@ -154,47 +154,46 @@ __device__ __forceinline__ bool word_nan(const uint4& q)
     return nan;
 }
 
-// Statistics of two stretches of a row, joined.  Maxima that are equal
-// (infinite ones among them) need no factor.
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2, float sc)
-{
-    const float t = fmaxf(m, m2);
-    s = s * (m == t ? 1.0f : exp2_fast((m - t) * sc)) + s2 * (m2 == t ? 1.0f : exp2_fast((m2 - t) * sc));
-    m = t;
-}
-
 // A row as 16-byte words, the first of which may begin before it and the last
 // end behind it: `skip` values of the first word belong to what lies before.
 template <typename T>
 struct Row {
     T* base;          // on a 16-byte boundary, at or below the row's start
-    uint32_t skip, vocab, words;
+    uint32_t skip, vocab, words, lo, hi;   // whole words: lo to hi
     __device__ __forceinline__ Row(const T* p, uint32_t v)
     {
         skip = uint32_t((uintptr_t(p) & 15) / sizeof(T));
         base = const_cast<T*>(p) - skip;
         vocab = v;
         words = (skip + v + Word<T>::kN - 1) / Word<T>::kN;
+        lo = skip ? 1 : 0;
+        hi = (skip + v) / Word<T>::kN;
     }
-    __device__ __forceinline__ bool whole(uint32_t g) const
+    __device__ __forceinline__ bool whole(uint32_t g) const { return g >= lo && g < hi; }
+    __device__ __forceinline__ bool cut(uint32_t g) const { return g < words && !whole(g); }
+    // word g, with -inf where it is not the row: whole words by a predicated load that nothing waits for before its
+    // use, the (at most two) others value by value
+    __device__ __forceinline__ uint4 load_whole(uint32_t g) const
     {
-        return (g > 0 || skip == 0) && (g + 1) * Word<T>::kN <= skip + vocab;
+        uint4 q;
+        asm volatile(
+            "{ .reg .pred p; setp.ne.u32 p, %5, 0; mov.u32 %0, %6; mov.u32 %1, %6; mov.u32 %2, %6; mov.u32 %3, %6;\n"
+            "@p ld.global.v4.u32 {%0, %1, %2, %3}, [%4]; }"
+            : "=&r"(q.x), "=&r"(q.y), "=&r"(q.z), "=&r"(q.w)
+            : "l"(base + uint64_t(g) * Word<T>::kN), "r"(uint32_t(whole(g))), "n"(Word<T>::kLow));
+        return q;
     }
-    // word g, with -inf where it is not the row
-    __device__ __forceinline__ uint4 load(uint32_t g) const
+    __device__ __noinline__ uint4 load_cut(uint32_t g) const
     {
-        if (g < words && whole(g)) return *reinterpret_cast<const uint4*>(base + uint64_t(g) * Word<T>::kN);
         union { uint4 q; T t[Word<T>::kN]; } u;
         u.q = make_uint4(Word<T>::kLow, Word<T>::kLow, Word<T>::kLow, Word<T>::kLow);
-        if (g < words) {
-#pragma unroll
-            for (int i = 0; i < Word<T>::kN; ++i) {
-                const uint32_t at = g * Word<T>::kN + i;
-                if (at >= skip && at - skip < vocab) u.t[i] = base[at];
-            }
+        for (int i = 0; i < Word<T>::kN; ++i) {
+            const uint32_t at = g * Word<T>::kN + i;
+            if (at >= skip && at - skip < vocab) u.t[i] = base[at];
         }
         return u.q;
     }
+    __device__ __forceinline__ uint4 load(uint32_t g) const { return cut(g) ? load_cut(g) : load_whole(g); }
 };
 
 // Sum of exp((x - m) / T) over words whose largest value is m.
@@ -222,26 +221,46 @@ __device__ __forceinline__ float words_sum(const uint4 (&q)[NV], float m, float 
 }
 
 // Loss of a row and its derivative by the log-probability.
-__device__ __forceinline__ void row_loss(const LossArgs& A, uint64_t row, float lp, float& loss, float& slope)
+__device__ __forceinline__ void row_loss(const LossArgs& A, float adv, float old, float ref, float lp, float& loss, float& slope)
 {
-    const float adv = A.advantages[row], ratio = expf(lp - A.old_logp[row]);
+    const float ratio = expf(lp - old);
     const float u = ratio * adv, c = fminf(fmaxf(ratio, A.lo), A.hi) * adv;
     const bool clipped = c < u;
     loss = clipped ? -c : -u;
     slope = clipped ? 0.0f : -u;
     if (A.kl != 0.0f) {
-        const float k = A.ref_logp[row] - lp, e = expf(k);
+        const float k = ref - lp, e = expf(k);
         loss += A.kl * (e - k - 1.0f);
         slope += A.kl * (1.0f - e);
     }
 }
 
+// The values of word k of a row that begins `skip` values into its first
+// word, one by one.
+template <typename T>
+__device__ __noinline__ void store_values(T* row, uint32_t skip, uint32_t vocab, uint32_t k, uint4 w)
+{
+    union { uint4 q; T t[Word<T>::kN]; } u;
+    u.q = w;
+    for (int j = 0; j < Word<T>::kN; ++j) {
+        const uint32_t at = k * Word<T>::kN + j;
+        if (at >= skip && at - skip < vocab) row[at - skip] = u.t[j];
+    }
+}
+
+// Blocks on an SM: what bounds the kernel is how many words are in flight, so
+// registers are held to what that takes (4096 rows of 128256 bf16 values,
+// 8 words a thread: 495 us with two blocks of 256 threads, 405 with three,
+// 347 with four).
+constexpr int resident_blocks(int th, int nv) { return (nv >= 6 ? 1024 : nv >= 4 ? 1536 : 2048) / th; }
+
 // TH threads a block, NV words a thread kept, `cluster` blocks a row.
 template <typename T, int TH, int NV>
-__global__ void __launch_bounds__(TH, TH == 256 ? 3 : 8) loss_kernel(LossArgs A, uint32_t cluster)
+__global__ void __launch_bounds__(TH, resident_blocks(TH, NV)) loss_kernel(LossArgs A, uint32_t cluster)
 {
     constexpr int N = Word<T>::kN;
-    __shared__ float2 part[TH / 32], all[kMaxCluster];
+    __shared__ float part[TH / 16];
+    __shared__ float2 all[kMaxCluster];
     launch_dependents();
     const uint32_t rank = cluster > 1 ? blockIdx.x % cluster : 0;
     const uint64_t row = blockIdx.x / cluster;
@@ -252,31 +271,44 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 3 : 8) loss_kernel(LossArgs A,
 
     const int64_t token = A.tokens[row];
     const float w = A.weights ? A.weights[row] : 1.0f;
+    // asked for now, so that they are there when the statistics are
+    const float adv = A.old_logp ? A.advantages[row] : 0.0f, old = A.old_logp ? A.old_logp[row] : 0.0f;
+    const float ref = A.ref_logp ? A.ref_logp[row] : 0.0f;
     const bool on = w != 0.0f && token >= 0 && token < int64_t(vocab);
     const uint32_t y = uint32_t(token);
-    float m = -INFINITY, s = 0.0f, sc = A.inv_temp * kLog2e;
+    const float sc = A.inv_temp * kLog2e;
+    float m = -INFINITY, s = 0.0f;
     uint4 q[NV];
     float xy = 0.0f;
     const Row<T> in(x, vocab);
     if (on) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) q[i] = in.load(first + i * step);
+        for (int i = 0; i < NV; ++i) q[i] = in.load_whole(first + i * step);
         xy = to_f32(x[y]);
 #pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (in.cut(first + i * step)) q[i] = in.load_cut(first + i * step);
+#pragma unroll
         for (int i = 0; i < NV; ++i) m = fmaxf(m, word_max(q[i], T()));
+        for (uint32_t k = first + NV * step; k < in.words; k += step) m = fmaxf(m, word_max(in.load(k), T()));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = m;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < TH / 32; ++i) m = fmaxf(m, part[i]);
         s = words_sum<T, NV>(q, m, sc);
         for (uint32_t k = first + NV * step; k < in.words; k += step) {
             const uint4 e[1] = {in.load(k)};
-            const float m2 = word_max(e[0], T());
-            join(m, s, m2, words_sum<T, 1>(e, m2, sc), sc);
+            s += words_sum<T, 1>(e, m, sc);
         }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) join(m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o), sc);
-        if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = make_float2(m, s);
-        __syncthreads();
-        m = part[0].x, s = part[0].y;
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+        if (threadIdx.x % 32 == 0) part[TH / 32 + threadIdx.x / 32] = s;
+        __syncthreads();   // also: grad may be logits, and everybody has read x[y]
+        s = 0.0f;
 #pragma unroll
-        for (int i = 1; i < TH / 32; ++i) join(m, s, part[i].x, part[i].y, sc);
+        for (int i = 0; i < TH / 32; ++i) s += part[TH / 32 + i];
         if (cluster > 1) {
             if (threadIdx.x < cluster) {
                 const uint32_t at = uint32_t(__cvta_generic_to_shared(&all[rank]));
@@ -286,10 +318,10 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 3 : 8) loss_kernel(LossArgs A,
                     : "memory");
             }
             asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
-            m = all[0].x, s = all[0].y;
-            for (uint32_t i = 1; i < cluster; ++i) join(m, s, all[i].x, all[i].y, sc);
-        } else {
-            __syncthreads();   // grad may be logits: everybody has read x[y]
+            for (uint32_t i = 0; i < cluster; ++i) m = fmaxf(m, all[i].x);
+            s = 0.0f;
+            // maxima that are equal (infinite ones among them) need no factor
+            for (uint32_t i = 0; i < cluster; ++i) s += all[i].x == m ? all[i].y : all[i].y * exp2_fast((all[i].x - m) * sc);
         }
         if (m == INFINITY && s == s) s = 1.0f;
     }
@@ -298,7 +330,7 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 3 : 8) loss_kernel(LossArgs A,
     if (on) {
         const float lp = (xy - m) * A.inv_temp - logf(s);
         float loss = 0.0f, slope = 0.0f;
-        if (A.old_logp) row_loss(A, row, lp, loss, slope);
+        if (A.old_logp) row_loss(A, adv, old, ref, lp, loss, slope);
         if (rank == 0 && threadIdx.x == 0) {
             A.logp[row] = lp;
             if (A.row_loss) A.row_loss[row] = w * loss;
@@ -317,20 +349,13 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 3 : 8) loss_kernel(LossArgs A,
     const Row<T> out(g, vocab);
     const bool same = out.skip == in.skip;
     auto put = [&](uint32_t k, const uint4& q, auto plain) {
-        if (k >= in.words) return;
         float v[N];
         Word<T>::values(q, v);
 #pragma unroll
         for (int j = 0; j < N; ++j) v[j] = d * e.of<decltype(plain)::value>(v[j]);
-        if (same && in.whole(k)) {
-            *reinterpret_cast<uint4*>(out.base + uint64_t(k) * N) = Word<T>::pack(v);
-        } else {
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const uint32_t at = k * N + j;
-                if (at >= in.skip && at - in.skip < vocab) g[at - in.skip] = from_f32<T>(v[j]);
-            }
-        }
+        const uint4 w = Word<T>::pack(v);
+        if (same && in.whole(k)) *reinterpret_cast<uint4*>(out.base + uint64_t(k) * N) = w;
+        else if (k < in.words) store_values<T>(g, in.skip, vocab, k, w);
     };
     auto put_all = [&](auto plain) {
 #pragma unroll
@@ -339,15 +364,8 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 3 : 8) loss_kernel(LossArgs A,
     };
     if (!on) {
         for (uint32_t k = rank * TH + threadIdx.x; k < out.words; k += step) {
-            if (out.whole(k)) {
-                *reinterpret_cast<uint4*>(out.base + uint64_t(k) * N) = make_uint4(0, 0, 0, 0);
-            } else {
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const uint32_t at = k * N + j;
-                    if (at >= out.skip && at - out.skip < vocab) out.base[at] = from_f32<T>(0.0f);
-                }
-            }
+            if (out.whole(k)) *reinterpret_cast<uint4*>(out.base + uint64_t(k) * N) = make_uint4(0, 0, 0, 0);
+            else store_values<T>(g, out.skip, vocab, k, make_uint4(0, 0, 0, 0));
         }
         return;
     }
@@ -383,16 +401,22 @@ int launch_rows(const LossArgs& A, uint32_t cluster, cudaStream_t s)
     return e == cudaSuccess ? DCR_OK : cuda_error(e, "policy loss launch");
 }
 
-// Blocks just large enough for the row, up to 32 KiB of it each; then a
-// cluster of them.
+// As few blocks of 256 threads as hold the row with up to 8 words a thread,
+// then as few words as that takes; for short rows blocks of 128.  (2048 rows
+// of 50000 f16 values: 89 us as 4 blocks x 8 words, 112 as 7 x 4, although
+// that keeps less.)
 template <typename T>
 int launch_rows(const LossArgs& A, cudaStream_t s)
 {
-    const uint64_t bytes = A.vocab * sizeof(T) + 16;
-    if (bytes <= 2048) return launch_rows<T, 128, 1>(A, 1, s);
-    if (bytes <= 8192) return launch_rows<T, 128, 4>(A, 1, s);
-    uint32_t cluster = 1;
-    while (cluster < kMaxCluster && bytes > 32768ull * cluster) cluster *= 2;
+    const bool aligned = uintptr_t(A.logits) % 16 == 0 && A.row_stride * sizeof(T) % 16 == 0;
+    const uint64_t words = (A.vocab * sizeof(T) + 15) / 16 + (aligned ? 0 : 1);
+    if (words <= 128) return launch_rows<T, 128, 1>(A, 1, s);
+    if (words <= 256) return launch_rows<T, 128, 2>(A, 1, s);
+    if (words <= 512) return launch_rows<T, 128, 4>(A, 1, s);
+    const uint32_t cluster = words > 2048 * kMaxCluster ? kMaxCluster : uint32_t((words + 2047) / 2048);
+    const uint64_t nv = (words + 256 * cluster - 1) / (256 * cluster);
+    if (nv <= 4) return launch_rows<T, 256, 4>(A, cluster, s);
+    if (nv <= 6) return launch_rows<T, 256, 6>(A, cluster, s);
     return launch_rows<T, 256, 8>(A, cluster, s);
 }
 
