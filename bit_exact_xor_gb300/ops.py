@@ -5,8 +5,10 @@ torch, and every call runs on `stream` (default: the current stream) without
 waiting for it.  What a call allocates belongs to the stream that it runs on;
 tensors handed in must be ready there.  A refused argument raises DcrError.
 
-The smallest of these operators take a few microseconds on the GPU, so the
-checks below are written out for their cost on the host.
+The smallest of these operators take a few microseconds on the GPU, so their
+common calls (tensors on the current device, new outputs, the current stream)
+go through the compiled csrc/binding.cpp; it hands back what it does not
+take, refusals among it, to the code below.
 """
 import ctypes
 from typing import NamedTuple
@@ -49,6 +51,7 @@ _ops = None
 _empty, _f32, _u8 = torch.empty, torch.float32, torch.uint8
 _SCALE_TYPES = (torch.uint8, torch.float8_e4m3fn)
 _byref = ctypes.byref
+_TYPES = (type(None), torch.dtype)
 
 
 def _lib():
@@ -68,6 +71,19 @@ def _lib():
 
 def _refuse(what):
     raise DcrError(ERR_INVALID, what)
+
+
+try:
+    from . import _binding as _fast
+except ImportError as e:
+    raise RuntimeError("the operators' binding is not built; run __graft_entry__.build()") from e
+
+
+def _result_of(r):
+    """What _fast returned: a status is raised."""
+    if type(r) is int:
+        check(r)
+    return r
 
 
 def _matrix(x, what):
@@ -143,6 +159,11 @@ def nvfp4_quantize(x, scale=None, per_row=False, values=None, out=None, stream=N
     codes stand for.  `out` is an Nvfp4 whose tensors are written (its scale
     is an output, too, unless `scale` is given), for example views of a
     trainer arena.  Returns (Nvfp4, values or None)."""
+    if out is None and stream is None:
+        r = _fast.quantize(x, scale, per_row, NONE if values is None else DTYPES.get(values, -1)) if values.__class__ in _TYPES else None
+        if r is not None:
+            codes, scales, sc, v = _result_of(r)
+            return Nvfp4(codes, scales, sc), v
     rows, cols, stride, xt = _matrix(x, "x")
     dev = x.device
     if stream is not None or dev.index != _current_device():
@@ -243,6 +264,11 @@ def nvfp4_linear(x, w, offsets=None, dtype=None, out=None, stream=None):
     or float16), which are quantised with a scale per row, so that a row's
     result does not depend on the rows beside it, then multiplied as in
     nvfp4_matmul.  dtype defaults to x's type."""
+    if out is None and stream is None:
+        t = DTYPES.get(x.dtype if dtype is None else dtype)
+        r = None if t is None else _fast.linear(x, *w, offsets, t)
+        if r is not None:
+            return _result_of(r)
     m, k, xs, xt = _matrix(x, "x")
     wrows, wk, dev, cw = _nvfp4(w, "w")
     if k != wk or x.device != dev:
@@ -270,6 +296,10 @@ def policy_loss(logits, tokens, old_logp, advantages, weights, ref_logp=None, cl
     write it to (logits itself, to save the memory).  Returns (loss, logp,
     grad): a float32 scalar, float32 [rows], and the gradient by the logits in
     their type (or None), ready for logits.backward(grad)."""
+    if stream is None and grad.__class__ is bool:
+        r = _fast.loss(logits, tokens, old_logp, advantages, weights, ref_logp, clip_low, clip_high, kl_coef, temperature, grad)
+        if r is not None:
+            return _result_of(r)
     rows, vocab, stride, t = _matrix(logits, "logits")
     dev = logits.device
     if stream is not None or dev.index != _current_device():
@@ -304,6 +334,10 @@ def policy_loss(logits, tokens, old_logp, advantages, weights, ref_logp=None, cl
 def token_logprobs(logits, tokens, temperature=1.0, out=None, stream=None):
     """dcr_token_logprobs: float32 [rows], the log-probability of each row's
     token under softmax(logits / temperature)."""
+    if out is None and stream is None:
+        r = _fast.logprobs(logits, tokens, temperature)
+        if r is not None:
+            return _result_of(r)
     rows, vocab, stride, t = _matrix(logits, "logits")
     dev = logits.device
     if stream is not None or dev.index != _current_device():
