@@ -892,21 +892,32 @@ int launch_wide(MatmulArgs A, const dcr_nvfp4& x, const dcr_nvfp4& w, bool depen
     return e == cudaSuccess ? DCR_OK : cuda_error(e, "NVFP4 product launch");
 }
 
-// Which kernel: the weights are P, with Q as narrow as the tokens allow, until
-// there are enough tokens that tiles of 128 by 256 give half of the SMs
-// something to do.  Few tiles are split over K among the blocks of a cluster.
+// Which kernel, by the number of tokens (of an expert) and of tiles; measured
+// in us, wide against the best of the others, weights not in the L2:
+//   64 experts of 4096 x 6144: 512 tokens 138 : 138, 1500 tokens 140 : 143; of 4096 x 2048: 3000 tokens 58 : 70
+//   28672 x 4096 (112 wide tiles): 20 tokens 17.8 : 15.6, 37 tokens 17.6 : 18.6, 64 tokens 16.5 : 18.2
+//   9728 x 4096, 48 tokens (38 tiles): 11.9 : 10.8;  14336 x 4096, 128 tokens (56 tiles): 14.3 : 16.6
+//   2048 x 2048, 600 tokens (40 tiles): 9.6 : 11.4;  4096 x 14336, 300 tokens (48 tiles of 56 steps): 32 : 27
+// So: wide from about 16 tokens an expert on; for one matrix from 32 tokens
+// on if it gives half of the SMs a tile, and from 96 on if it gives a quarter
+// of them one and the sums are not long.  Otherwise the weights are P, Q as
+// narrow as the tokens allow, and few tiles are split over K among the
+// blocks of a cluster, as long as the clusters find room together (two
+// blocks fit an SM, but clusters do not fill every one: 9728 x 4096, 48
+// tokens: split 2 11.2, 3 10.8, 4 (304 blocks) 15.5 us).
 template <typename T>
 int choose(const MatmulArgs& A, const dcr_nvfp4& x, const dcr_nvfp4& w, bool dependent, cudaStream_t s)
 {
     const uint64_t groups = A.experts ? A.experts : 1, sms = uint64_t(sm_count());
-    const uint64_t each = (A.m + groups - 1) / groups;
+    const uint64_t each = (A.m + groups - 1) / groups, steps = (A.k + kStep - 1) / kStep;
     const uint64_t wide = ((each + 127) / 128) * ((A.n + 255) / 256) * groups;
-    if (each > 64 && wide >= sms / 2) return launch_wide<T>(A, x, w, dependent, s);
+    if (A.experts ? each > 16 && wide * 4 >= sms
+                  : (each > 32 && wide * 2 >= sms) || (each > 96 && wide * 4 >= sms && steps <= 32))
+        return launch_wide<T>(A, x, w, dependent, s);
     const uint64_t bn = each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : 128;
-    const uint64_t tiles = ((each + bn - 1) / bn) * ((A.n + 127) / 128) * groups;
-    const uint32_t steps = (A.k + kStep - 1) / kStep;
-    uint32_t split = 1;
-    while (split < 8 && tiles * split * 2 <= sms * 2 && steps >= split * 4) split *= 2;
+    const uint64_t xt = A.experts ? A.m / bn + (A.m < groups ? A.m : groups) : (A.m + bn - 1) / bn;
+    const uint64_t room = sms * 17 / 10 / (xt * ((A.n + 127) / 128)), most = steps / 4 < 8 ? steps / 4 : 8;
+    const uint32_t split = uint32_t(room < 1 || most < 1 ? 1 : room < most ? room : most);
     if (bn == 16) return launch<16, T>(A, x, w, split, dependent, s);
     if (bn == 32) return launch<32, T>(A, x, w, split, dependent, s);
     if (bn == 64) return launch<64, T>(A, x, w, split, dependent, s);
