@@ -29,7 +29,7 @@ constexpr int kP = 128;             // rows of P
 constexpr int kStepBytes = 128;     // codes of a row in one step of K
 constexpr int kStep = 256;          // values of K in one step
 constexpr int kPatch = 512;         // a scale patch: 32 lanes x 16 bytes
-constexpr int64_t kWaitCycles = 4000000000ll;   // two seconds at the highest clock
+constexpr int64_t kWaitCycles = 2000000000ll;   // a second at the highest clock
 
 __device__ int g_error;             // a wait ran out (dcr_ops_status reads and clears it)
 
@@ -45,6 +45,7 @@ struct MatmulArgs {
     void* y;
     uint64_t y_stride;
     uint32_t y_vec;                        // y rows may be written 32 bytes at once
+    uint32_t stall;                        // test only: no tile is ever loaded, so that the waits run out
 };
 
 __device__ __forceinline__ uint32_t saddr(const void* p) { return uint32_t(__cvta_generic_to_shared(p)); }
@@ -73,7 +74,7 @@ __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity)
     return ok != 0;
 }
 
-// Every wait is bounded: after about two seconds, or once another warp of the block
+// Every wait is bounded: after about a second, or once another warp of the block
 // has given up, it returns false and the block winds down.
 __device__ __forceinline__ bool mbar_wait_long(uint64_t* b, uint32_t parity, volatile int* dead)
 {
@@ -423,7 +424,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
     if (warp == 0) {
         uint32_t it = 0;
         bool ok = true;
-        if (lane == 0) {
+        if (lane == 0 && !A.stall) {
             for (uint32_t t = first; t < tiles && ok; t += stride) {
                 const Tile c = tile_of(A, pref, t, nw, BN, kP);
                 const int xr = int(c.x0), wr = int(c.e * A.n + c.w0);
@@ -663,7 +664,7 @@ matmul_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         if (warp == 0) {
             uint32_t it = 0;
             bool ok = true;
-            if (lane == 0) {
+            if (lane == 0 && !A.stall) {
                 for (uint32_t t = first; t < tiles && ok; t += stride) {
                     const Tile c = tile_of(A, pref, t, nw, kP, 256);
                     const int xr = int(c.x0), wr = int(c.e * A.n + c.w0);
@@ -756,27 +757,34 @@ matmul_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty);
-            const uint32_t m = c.x0 + 32 * quarter + lane, n0 = c.w0 + 128 * half;
-            if (m < c.x1 && n0 < A.n) {
-                const float sc = A.x_scale[A.x_scale_rows ? m : 0] * A.w_scale[A.w_scale_each ? c.e : 0];
-                T* out = static_cast<T*>(A.y) + uint64_t(m) * A.y_stride + n0;
-                constexpr int N = 32 / sizeof(T);   // values of a sector
+            const uint32_t m0 = c.x0 + 32 * quarter, m = m0 + lane, n0 = c.w0 + 128 * half;
+            const float sc = m < c.x1 ? A.x_scale[A.x_scale_rows ? m : 0] * A.w_scale[A.w_scale_each ? c.e : 0] : 0.0f;
+            T* const y = static_cast<T*>(A.y) + n0;
+            constexpr int N = 32 / sizeof(T);   // values of a sector
+            if (A.y_vec && n0 + 128 <= A.n) {
+                // four lanes write 128 bytes of one of their rows at a time: whole lines, eight to an instruction
 #pragma unroll
-                for (int j = 0; j < 128; j += N) {
-                    if (A.y_vec && n0 + j + N <= A.n) {
-                        uint32_t w[8];
+                for (int j = 0; j < 128; j += 4 * N) {
+                    uint32_t u[4][8];
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            w[q] = sizeof(T) == 4 ? __float_as_uint(__uint_as_float(v[j + q]) * sc)
-                                                  : pack2(__uint_as_float(v[j + 2 * q % N]) * sc,
-                                                          __uint_as_float(v[j + (2 * q + 1) % N]) * sc, T());
-                        store32(out + j, w);
-                    } else {
+                    for (int i = 0; i < 8; ++i) {
 #pragma unroll
-                        for (int q = 0; q < N; ++q)
-                            if (n0 + j + q < A.n) out[j + q] = from_f32<T>(__uint_as_float(v[j + q]) * sc);
+                        for (int q = 0; q < 4; ++q)
+                            u[q][i] = sizeof(T) == 4 ? __float_as_uint(__uint_as_float(v[j + q * N + i % N]) * sc)
+                                                     : pack2(__uint_as_float(v[j + q * N + 2 * i % N]) * sc,
+                                                             __uint_as_float(v[j + q * N + (2 * i + 1) % N]) * sc, T());
+                        transpose4<1, 2>(u[0][i], u[1][i], u[2][i], u[3][i], lane, xchg1);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t row = m0 + (lane & ~3u) + q;
+                        if (row < c.x1) store32(y + uint64_t(row) * A.y_stride + j + N * (lane % 4), u[q]);
                     }
                 }
+            } else if (m < c.x1) {
+#pragma unroll
+                for (int j = 0; j < 128; ++j)
+                    if (n0 + j < A.n) y[uint64_t(m) * A.y_stride + j] = from_f32<T>(__uint_as_float(v[j]) * sc);
             }
             __syncwarp();
         }
@@ -930,6 +938,8 @@ int matmul_launch(const dcr_nvfp4& x, const dcr_nvfp4& w, uint64_t m, uint64_t n
                   uint32_t experts, void* y, uint32_t dtype, uint64_t y_stride, bool dependent, cudaStream_t s)
 {
     MatmulArgs A{};
+    A.stall = (dtype & DCR_TEST_STALL) != 0;
+    dtype &= ~DCR_TEST_STALL;
     A.x_scale = x.scale, A.w_scale = w.scale;
     A.x_scale_rows = x.scale_count > 1, A.w_scale_each = w.scale_count > 1;
     A.m = uint32_t(m), A.n = uint32_t(n), A.k = uint32_t(k), A.experts = experts;
@@ -974,7 +984,8 @@ extern "C" int dcr_nvfp4_matmul(const dcr_nvfp4* x, const dcr_nvfp4* w, uint64_t
     if (!x || !w) return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: NULL argument");
     if (x->scale_count != 1 && x->scale_count != m)
         return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: x needs one scale or one per row");
-    if (int rc = dcr::check("dcr_nvfp4_matmul", *w, m, n, k, offsets, experts, y, dtype, y_stride)) return rc > 0 ? DCR_OK : rc;
+    if (int rc = dcr::check("dcr_nvfp4_matmul", *w, m, n, k, offsets, experts, y, dtype & ~DCR_TEST_STALL, y_stride))
+        return rc > 0 ? DCR_OK : rc;
     if (!x->codes || !x->scales || !x->scale) return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: NULL argument");
     if (uintptr_t(x->codes) % 16 || uintptr_t(x->scale) % 4)
         return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: misaligned buffer");

@@ -21,6 +21,7 @@ F32, BF16, F16, NONE = 0, 1, 2, 3
 SCALE_GIVEN, SCALE_TENSOR, SCALE_ROW = 0, 1, 2
 MAX_EXPERTS = 1024
 QUANT_PARTIALS = 1216
+TEST_STALL = 0x80000000   # test only: a product whose waits run out
 DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 OP_EXPORTS = ["dcr_nvfp4_quantize", "dcr_nvfp4_matmul", "dcr_nvfp4_linear", "dcr_policy_loss", "dcr_token_logprobs",

@@ -73,8 +73,12 @@ int dcr_nvfp4_quantize(const void* x, uint32_t dtype, uint64_t rows, uint64_t co
  * (device, experts + 1 entries, not decreasing) says which rows of x belong
  * to which: rows offsets[e] to offsets[e + 1] are multiplied by matrix e.
  * Rows that no expert has are left as they are.  experts <= DCR_MAX_EXPERTS;
- * experts = 0 and offsets = NULL for one matrix. */
+ * experts = 0 and offsets = NULL for one matrix.
+ * Test only: with DCR_TEST_STALL added to dtype no operand is ever loaded, so
+ * that the kernel's waits run out (after about a second): it ends with y
+ * incomplete, and dcr_ops_status reports DCR_ERR_TIMEOUT. */
 #define DCR_MAX_EXPERTS 1024u
+#define DCR_TEST_STALL 0x80000000u
 int dcr_nvfp4_matmul(const dcr_nvfp4* x, const dcr_nvfp4* w, uint64_t m, uint64_t n, uint64_t k,
                      const int32_t* offsets, uint32_t experts, void* y, uint32_t dtype, uint64_t y_stride,
                      void* stream);
@@ -116,7 +120,7 @@ int dcr_token_logprobs(const void* logits, uint32_t dtype, uint64_t rows, uint64
 
 /* Waits for `stream` and reports whether any operator on the current device
  * gave up a wait since the last report: every wait inside a kernel is
- * bounded (two seconds), after which the kernel ends with its output
+ * bounded (about a second), after which the kernel ends with its output
  * incomplete.  DCR_OK, DCR_ERR_TIMEOUT or DCR_ERR_CUDA. */
 int dcr_ops_status(void* stream);
 

@@ -324,3 +324,24 @@ def test_calls_run_on_the_given_stream_and_in_a_graph():
     x.copy_(_x(40, 512, "bf16", 2))
     g.replay()
     assert torch.equal(out, dcr.nvfp4_linear(x, w)) and not torch.equal(out, y)
+
+
+@pytest.mark.parametrize("m,n,k", [(16, 512, 2048), (300, 5000, 256)])
+def test_a_wait_that_runs_out_is_reported(m, n, k):
+    # no operand is ever loaded: every wait of the kernel gives up after about a second, the call's status says so,
+    # and the device is as usable as before
+    import ctypes
+    from bit_exact_xor_gb300 import ops
+    x, w = _operand(m, k, 1, per_row=True), _operand(n, k, 2)
+    y = dcr.nvfp4_matmul(x, w, dtype=torch.float32)
+    dcr.ops_status()
+    out = torch.empty(m, n, device="cuda")
+    cx, cw = ops._nvfp4(x, "x")[3], ops._nvfp4(w, "w")[3]
+    rc = ops._lib().dcr_nvfp4_matmul(ctypes.byref(cx), ctypes.byref(cw), m, n, k, None, 0, out.data_ptr(), ops.F32 | ops.TEST_STALL, n,
+                                     torch.cuda.current_stream().cuda_stream)
+    assert rc == dcr.OK
+    with pytest.raises(dcr.DcrError) as e:
+        dcr.ops_status()
+    assert e.value.code == dcr.ERR_TIMEOUT
+    dcr.ops_status()
+    assert torch.equal(y, dcr.nvfp4_matmul(x, w, dtype=torch.float32))

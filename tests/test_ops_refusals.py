@@ -131,6 +131,7 @@ def test_header_constants_and_exports():
     assert vals and all(getattr(ops, k) == v for k, v in vals.items())
     assert int(re.search(r"DCR_QUANT_PARTIALS (\d+)u", src).group(1)) == ops.QUANT_PARTIALS
     assert int(re.search(r"DCR_MAX_EXPERTS (\d+)u", src).group(1)) == ops.MAX_EXPERTS
+    assert int(re.search(r"DCR_TEST_STALL (0x\w+)u", src).group(1), 0) == ops.TEST_STALL
     assert "#define DCR_LINEAR_WORKSPACE(m, k) ((m) * ((k) / 2 + (k) / 16 + 4) + 4)" in src
     declared = set(re.findall(r"^int (dcr_\w+)\(", src, flags=re.M))
     assert declared == set(ops.OP_EXPORTS)
