@@ -8,11 +8,12 @@
 // distributed shared memory once.  What does not fit on the chip that way is
 // read again.
 //
-// Bound by its traffic in long batches: 4096 rows of 128256 bf16 values in 346
-// us, 5.3 TB/s of what it moves (a quarter of the rows is left out: read 0.79
+// Bound by its traffic in long batches: 4096 rows of 128256 bf16 values in 361
+// us, 5.1 TB/s of what it moves (a quarter of the rows is left out: read 0.79
 // GB, written 1.05 GB); by the chain of loads, two block-wide steps, a
 // cluster-wide one and stores in short ones (1021 rows of 32771 values: 41
 // us, five rounds of blocks).
+#include <cmath>
 #include <type_traits>
 
 #include "ops_internal.h"
@@ -32,9 +33,10 @@ struct LossArgs {
     float* row_loss;
     float* logp;
     float inv_temp, lo, hi, kl;
+    float sc;                   // log2(e) / temperature, rounded to nearest
+    float sc_dn, sc_lo;         // the same rounded down, and the (positive) rest
 };
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ float exp2_fast(float v)
@@ -125,11 +127,24 @@ __device__ __forceinline__ float word_max(const uint4& q, T)
 // the rounded product msc = m sc, whose rounding error is the same factor on
 // every term (the row's sum is corrected for it once).  A maximum so large
 // that msc could overflow (a row of the type's lowest values) takes the
-// difference first.
+// difference first.  The row's sum takes a second multiply-add with the rest
+// of sc: over a large vocabulary most of it comes from terms far below the
+// maximum, where sc's rounding shifts every one the same way (a row's
+// log-probability by up to 1e-6).  There sc is rounded down, so that the rest
+// is positive and -inf stays -inf.
 struct Exponent {
-    float sc, m, msc;
+    float sc, lo, m, msc;
     bool plain;
-    __device__ __forceinline__ Exponent(float m_, float sc_) : sc(sc_), m(m_), msc(m_ * sc_), plain(fabsf(m_ * sc_) < 1e30f) {}
+    __device__ __forceinline__ Exponent(float m_, float sc_, float lo_)
+        : sc(sc_), lo(lo_), m(m_), msc(m_ * sc_), plain(fabsf(m_ * sc_) < 1e30f)
+    {
+    }
+    template <bool PLAIN>
+    __device__ __forceinline__ float term(float x) const
+    {
+        return exp2_fast(PLAIN ? fmaf(x, lo, fmaf(x, sc, -msc)) : (x - m) * sc);
+    }
+    __device__ __forceinline__ float term_excess() const { return plain ? fmaf(m, lo, fmaf(m, sc, -msc)) : 0.0f; }
     template <bool PLAIN>
     __device__ __forceinline__ float of(float x) const
     {
@@ -145,7 +160,7 @@ __device__ __forceinline__ float word_sum(const uint4& q, const Exponent& e)
     float v[Word<T>::kN], s[2] = {0.0f, 0.0f};
     Word<T>::values(q, v);
 #pragma unroll
-    for (int i = 0; i < Word<T>::kN; ++i) s[i & 1] += e.of<PLAIN>(v[i]);
+    for (int i = 0; i < Word<T>::kN; ++i) s[i & 1] += e.term<PLAIN>(v[i]);
     return s[0] + s[1];
 }
 
@@ -204,7 +219,7 @@ struct Row {
 
 // Sum of exp((x - m) / T) over words whose largest value is m.
 template <typename T, int NV>
-__device__ __forceinline__ float words_sum(const uint4 (&q)[NV], float m, float sc)
+__device__ __forceinline__ float words_sum(const uint4 (&q)[NV], float m, float sc, float lo)
 {
     float s = 0.0f;
     if (fabsf(m) == INFINITY || m != m) {
@@ -215,11 +230,11 @@ __device__ __forceinline__ float words_sum(const uint4 (&q)[NV], float m, float 
         for (int i = 0; i < NV; ++i) nan |= word_nan<T>(q[i]);
         return nan ? NAN : 0.0f;
     }
-    const Exponent e(m, sc);
+    const Exponent e(m, sc, lo);
     if (e.plain) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) s += word_sum<T, true>(q[i], e);
-        return s * exp2f(-e.excess());
+        return s * exp2f(-e.term_excess());
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) s += word_sum<T, false>(q[i], e);
@@ -282,7 +297,7 @@ __global__ void __launch_bounds__(TH, resident_blocks(TH, NV)) loss_kernel(LossA
     const float ref = A.ref_logp ? A.ref_logp[row] : 0.0f;
     const bool on = w != 0.0f && token >= 0 && token < int64_t(vocab);
     const uint32_t y = uint32_t(token);
-    const float sc = A.inv_temp * kLog2e;
+    const float sc = A.sc;
     float m = -INFINITY, s = 0.0f;
     uint4 q[NV];
     float xy = 0.0f;
@@ -303,10 +318,10 @@ __global__ void __launch_bounds__(TH, resident_blocks(TH, NV)) loss_kernel(LossA
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < TH / 32; ++i) m = fmaxf(m, part[i]);
-        s = words_sum<T, NV>(q, m, sc);
+        s = words_sum<T, NV>(q, m, A.sc_dn, A.sc_lo);
         for (uint32_t k = first + NV * step; k < in.words; k += step) {
             const uint4 e[1] = {in.load(k)};
-            s += words_sum<T, 1>(e, m, sc);
+            s += words_sum<T, 1>(e, m, A.sc_dn, A.sc_lo);
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
@@ -350,7 +365,7 @@ __global__ void __launch_bounds__(TH, resident_blocks(TH, NV)) loss_kernel(LossA
 
     // grad_j = c ([j = y] - exp((x_j - m) / T) / s).  The words go out as they came in where the gradient's row lies on
     // the same offset from a 16-byte boundary.
-    const Exponent e(m, sc);
+    const Exponent e(m, sc, 0.0f);
     const float d = on ? -c / s * exp2f(-e.excess()) : 0.0f;
     const Row<T> out(g, vocab);
     const bool same = out.skip == in.skip;
@@ -430,8 +445,12 @@ int launch_rows(const LossArgs& A, cudaStream_t s)
     return launch_rows<T, 256, 8>(A, cluster, s);
 }
 
-int launch(const LossArgs& A, uint32_t dtype, float* loss, cudaStream_t s)
+int launch(LossArgs A, uint32_t dtype, float temperature, float* loss, cudaStream_t s)
 {
+    const double sc = 1.4426950408889634 / temperature;
+    A.sc = float(sc);
+    A.sc_dn = A.sc > sc ? std::nextafterf(A.sc, 0.0f) : A.sc;
+    A.sc_lo = std::fmax(float(sc - A.sc_dn), 1e-37f);
     if (A.rows == 0 && !loss) return DCR_OK;
     if (A.rows) {
         const int rc = with_dtype(dtype, [&](auto t) { return launch_rows<decltype(t)>(A, s); });
@@ -485,7 +504,7 @@ extern "C" int dcr_policy_loss(const void* logits, uint32_t dtype, uint64_t rows
         return set_error(DCR_ERR_INVALID, "dcr_policy_loss: misaligned buffer");
     LossArgs A{logits, grad, rows, vocab, row_stride, grad_stride, tokens, old_logp, ref_logp, advantages, weights,
                row_loss, logp, 1.0f / opts->temperature, 1.0f - opts->clip_low, 1.0f + opts->clip_high, opts->kl_coef};
-    return launch(A, dtype, loss, static_cast<cudaStream_t>(stream));
+    return launch(A, dtype, opts->temperature, loss, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int dcr_token_logprobs(const void* logits, uint32_t dtype, uint64_t rows, uint64_t vocab, uint64_t row_stride,
@@ -495,5 +514,5 @@ extern "C" int dcr_token_logprobs(const void* logits, uint32_t dtype, uint64_t r
     LossArgs A{};
     A.logits = logits, A.rows = rows, A.vocab = vocab, A.row_stride = row_stride;
     A.tokens = tokens, A.logp = logp, A.inv_temp = 1.0f / temperature;
-    return launch(A, dtype, nullptr, static_cast<cudaStream_t>(stream));
+    return launch(A, dtype, temperature, nullptr, static_cast<cudaStream_t>(stream));
 }
