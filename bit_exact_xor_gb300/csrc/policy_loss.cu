@@ -108,6 +108,16 @@ struct Word<__half> {
     }
 };
 
+// A word with -inf in the place of its value j.
+template <typename T>
+__device__ __forceinline__ uint4 without(const uint4& q, uint32_t j)
+{
+    constexpr uint32_t kPer = 4 / sizeof(T);
+    const uint32_t at = j / kPer, mask = kPer == 1 ? ~0u : 0xFFFFu << (16 * (j % kPer)), low = Word<T>::kLow & mask;
+    return make_uint4(at == 0 ? (q.x & ~mask) | low : q.x, at == 1 ? (q.y & ~mask) | low : q.y,
+                      at == 2 ? (q.z & ~mask) | low : q.z, at == 3 ? (q.w & ~mask) | low : q.w);
+}
+
 // Largest value of a word (a NaN is passed over), two at a time where two
 // share a register.
 __device__ __forceinline__ float word_max(const uint4& q, float)
@@ -298,10 +308,14 @@ __global__ void __launch_bounds__(TH, resident_blocks(TH, NV)) loss_kernel(LossA
     const bool on = w != 0.0f && token >= 0 && token < int64_t(vocab);
     const uint32_t y = uint32_t(token);
     const float sc = A.sc;
-    float m = -INFINITY, s = 0.0f;
+    // m: the row's maximum; others: the sum of exp((x_j - m) / T) without the token's own term, which is ey.  Formed
+    // from others, 1 - p = others / (others + ey) and, for the largest value, log p = -log1p(others) keep their accuracy
+    // where the token is nearly certain: a sum over all values has rounded away what is left beside 1 there.
+    float m = -INFINITY, others = 0.0f, ey = 0.0f;
     uint4 q[NV];
     float xy = 0.0f;
     const Row<T> in(x, vocab);
+    const uint32_t yword = (in.skip + y) / N, yat = (in.skip + y) % N;   // where the token's value is
     if (on) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) q[i] = in.load_whole(first + i * step);
@@ -313,14 +327,17 @@ __global__ void __launch_bounds__(TH, resident_blocks(TH, NV)) loss_kernel(LossA
         for (int i = 0; i < NV; ++i) m = fmaxf(m, word_max(q[i], T()));
         for (uint32_t k = first + NV * step; k < in.words; k += step) m = fmaxf(m, word_max(in.load(k), T()));
 #pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (first + i * step == yword) q[i] = without<T>(q[i], yat);
+#pragma unroll
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
         if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = m;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < TH / 32; ++i) m = fmaxf(m, part[i]);
-        s = words_sum<T, NV>(q, m, A.sc_dn, A.sc_lo);
+        float s = words_sum<T, NV>(q, m, A.sc_dn, A.sc_lo);
         for (uint32_t k = first + NV * step; k < in.words; k += step) {
-            const uint4 e[1] = {in.load(k)};
+            const uint4 word = in.load(k), e[1] = {k == yword ? without<T>(word, yat) : word};
             s += words_sum<T, 1>(e, m, A.sc_dn, A.sc_lo);
         }
 #pragma unroll
@@ -345,11 +362,15 @@ __global__ void __launch_bounds__(TH, resident_blocks(TH, NV)) loss_kernel(LossA
             for (uint32_t i = 0; i < cluster; ++i) s += all[i].x == m ? all[i].y : all[i].y * exp2_fast((all[i].x - m) * sc);
         }
         if (m == INFINITY && s == s) s = 1.0f;
+        others = s;
+        // not a number where the token's value is infinite and the maximum
+        ey = xy != m ? exp2_fast((xy - m) * sc) : fabsf(m) == INFINITY ? NAN : 1.0f;
     }
+    const float s = others + ey;
 
     float c = 0.0f;
     if (on) {
-        const float lp = (xy - m) * A.inv_temp - logf(s);
+        const float lp = ey == 1.0f ? -log1pf(others) : (xy - m) * A.inv_temp - logf(s);
         float loss = 0.0f, slope = 0.0f;
         if (A.old_logp) row_loss(A, adv, old, ref, lp, loss, slope);
         if (rank == 0 && threadIdx.x == 0) {
@@ -363,8 +384,8 @@ __global__ void __launch_bounds__(TH, resident_blocks(TH, NV)) loss_kernel(LossA
     }
     if (!g) return;
 
-    // grad_j = c ([j = y] - exp((x_j - m) / T) / s).  The words go out as they came in where the gradient's row lies on
-    // the same offset from a 16-byte boundary.
+    // grad_j = -c exp((x_j - m) / T) / s, and c others / s for the token.  The words go out as they came in where the
+    // gradient's row lies on the same offset from a 16-byte boundary.
     const Exponent e(m, sc, 0.0f);
     const float d = on ? -c / s * exp2f(-e.excess()) : 0.0f;
     const Row<T> out(g, vocab);
@@ -393,7 +414,7 @@ __global__ void __launch_bounds__(TH, resident_blocks(TH, NV)) loss_kernel(LossA
     if (e.plain) put_all(std::true_type());
     else put_all(std::false_type());
     // the token's own value, by the thread that wrote its word
-    if ((in.skip + y) / N % step == first % step) g[y] = from_f32<T>(c + d * (e.plain ? e.of<true>(xy) : e.of<false>(xy)));
+    if ((in.skip + y) / N % step == first % step) g[y] = from_f32<T>(c * (others / s));
 }
 
 // The rows' losses summed in a fixed order: thread i takes rows i, i + 1024,

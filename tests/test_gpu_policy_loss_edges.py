@@ -1,0 +1,98 @@
+"""Policy loss and token log-probabilities where 32-bit arithmetic goes wrong
+most easily: tokens that are nearly certain, logits far from zero, extreme
+temperatures, ratios that overflow."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import bit_exact_xor_gb300 as dcr  # noqa: E402
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+EPS = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+TINY = {"f32": 2.0 ** -149, "bf16": 2.0 ** -133, "f16": 2.0 ** -25}
+
+
+def _exact(z, tokens, temp):
+    """In 64 bits and without a subtraction of near values: log-probabilities, 1 - p of the tokens, softmax."""
+    z = z.double() / temp
+    rows = torch.arange(len(tokens))
+    rest = torch.exp(z - z[rows, tokens][:, None])
+    rest[rows, tokens] = 0.0
+    o = rest.sum(1)
+    return -torch.log1p(o), o / (1 + o), torch.softmax(z, 1)
+
+
+def _sum_error(z, temp):
+    """A bound on the relative error of a row's sum of exponentials: two multiply-adds round an exponent (in units of
+    log 2) of at most A by 2^-24 of it each, the rest of log2(e) / T is another such part; exponential, correction of the
+    maximum's product and at most 48 additions one after another."""
+    zz = z.double() / temp * 1.4426950408889634
+    a = float((zz.amax(1) - zz.amin(1)).max())
+    return 2.0 ** -21 + (3 * a + 48) * 2.0 ** -24
+
+
+def _certain(rows, vocab, dtype, gap, seed):
+    g = torch.Generator().manual_seed(seed)
+    z = torch.randn(rows, vocab, generator=g)
+    tokens = torch.randint(0, vocab, (rows,), generator=g)
+    tokens[0], tokens[-1] = 0, vocab - 1
+    z[torch.arange(rows), tokens] += gap
+    return z.to(DT[dtype]), tokens
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("gap", [4.0, 8.0, 12.0])
+@pytest.mark.parametrize("vocab", [2, 5, 40, 200, 2047, 7001, 33001, 280001])
+def test_nearly_certain_tokens(dtype, gap, vocab):
+    # the log-probability and the token's own gradient, c (1 - p), each to an error relative to itself
+    rows, temp = 7, 0.8
+    z, tokens = _certain(rows, vocab, dtype, gap, vocab)
+    elp, eq, ep = _exact(z, tokens, temp)
+    adv = torch.where(torch.arange(rows) % 2 == 0, 64.0, -64.0)
+    old = elp.float()
+    one = torch.ones(rows)
+    loss, lp, grad = dcr.policy_loss(z.cuda(), tokens.cuda(), old.cuda(), adv.cuda(), one.cuda(), clip_low=0.5, clip_high=0.5,
+                                     temperature=temp)
+    r = _sum_error(z, temp)
+    # the token is the largest or so near to it that nothing cancels: log1p of the others' sum, or the difference of two
+    # rounded numbers of the size of lp
+    top = z[torch.arange(rows), tokens] == z.amax(1)
+    lp = lp.cpu().double()
+    bound = torch.where(top, elp.abs() * (r + 2.0 ** -22), r + (elp.abs() + math.log(vocab) + 1) * 2.0 ** -21)
+    assert bool(((lp - elp).abs() <= bound).all()), float(((lp - elp).abs() / bound).max())
+    # the ratio carries lp's error, the rounding of lp - old, and the exponential's; then a few products and a quotient
+    ratio = torch.exp(elp - old.double())
+    c = -ratio * adv.double() / temp
+    slope = bound + 2.0 ** -20
+    got = grad.cpu().double()
+    egrad = -c[:, None] * ep
+    egrad[torch.arange(rows), tokens] = c * eq
+    # a probability is the quotient of two such sums
+    limit = egrad.abs() * (slope[:, None] + 2 * r + 2.0 ** -21 + 1.01 * EPS[dtype]) + TINY[dtype]
+    bad = (got - egrad).abs() / limit
+    assert float(bad.max()) <= 1.0, (float(bad.max()), float(bad[torch.arange(rows), tokens].max()))
+    # the token's log-probability alone is the same
+    assert torch.equal(dcr.token_logprobs(z.cuda(), tokens.cuda(), temperature=temp).cpu().double(), lp)
+
+
+@pytest.mark.parametrize("vocab", [3, 130, 5000, 40000])
+def test_token_that_is_nan_infinite_or_alone(vocab):
+    z = torch.zeros(6, vocab, device="cuda")
+    t = torch.tensor([0, 1, 2, vocab - 1, vocab // 2, 1], device="cuda")
+    z[0, 0] = float("nan")                       # the token itself: not a number
+    z[1, 1] = float("inf")                       # inf - inf
+    z[2] = float("-inf")                         # alone: certain
+    z[2, 2] = -3.0
+    z[3, 0] = float("inf")                       # another one is infinite: impossible
+    z[4, vocab // 2] = float("-inf")             # masked out
+    z[5, 1] = 200.0                              # certain to 32 bits
+    one = torch.ones(6, device="cuda")
+    loss, lp, grad = dcr.policy_loss(z, t, torch.zeros(6, device="cuda"), one, one)
+    lp, grad = lp.cpu(), grad.cpu()
+    assert math.isnan(lp[0]) and math.isnan(lp[1]) and float(lp[2]) == 0.0
+    assert float(lp[3]) == float("-inf") and float(lp[4]) == float("-inf") and float(lp[5]) == 0.0
+    assert bool((grad[2] == 0).all()) and float(grad[5, 1]) == 0.0
+    assert torch.equal(torch.isnan(dcr.token_logprobs(z, t).cpu()), torch.isnan(lp))
