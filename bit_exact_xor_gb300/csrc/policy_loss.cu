@@ -317,6 +317,9 @@ __global__ void __launch_bounds__(TH, resident_blocks(TH, NV)) loss_kernel(LossA
     const Row<T> in(x, vocab);
     const uint32_t yword = (in.skip + y) / N, yat = (in.skip + y) % N;   // where the token's value is
     if (on) {
+        // another block's shared memory may be written once that block is known to run: all say so here, and wait for it
+        // before they write (a row is on in all blocks of its cluster or in none)
+        if (cluster > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
 #pragma unroll
         for (int i = 0; i < NV; ++i) q[i] = in.load_whole(first + i * step);
         xy = to_f32(x[y]);
@@ -348,6 +351,7 @@ __global__ void __launch_bounds__(TH, resident_blocks(TH, NV)) loss_kernel(LossA
 #pragma unroll
         for (int i = 0; i < TH / 32; ++i) s += part[TH / 32 + i];
         if (cluster > 1) {
+            asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
             if (threadIdx.x < cluster) {
                 const uint32_t at = uint32_t(__cvta_generic_to_shared(&all[rank]));
                 asm volatile(

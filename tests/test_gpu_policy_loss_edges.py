@@ -96,3 +96,26 @@ def test_token_that_is_nan_infinite_or_alone(vocab):
     assert float(lp[3]) == float("-inf") and float(lp[4]) == float("-inf") and float(lp[5]) == 0.0
     assert bool((grad[2] == 0).all()) and float(grad[5, 1]) == 0.0
     assert torch.equal(torch.isnan(dcr.token_logprobs(z, t).cpu()), torch.isnan(lp))
+
+
+@pytest.mark.parametrize("dtype,vocab", [("f32", 8200), ("bf16", 40000), ("f16", 131072)])
+def test_clusters_that_come_and_go(dtype, vocab):
+    # rows of two to eight blocks, most of them left out and gone at once, on two streams: each block's part of the sum
+    # reaches the others, whenever they start
+    rows = 900
+    g = torch.Generator().manual_seed(vocab)
+    z = torch.randn(4, vocab, generator=g).to(DT[dtype])
+    tokens = torch.randint(0, vocab, (rows,), generator=g)
+    which = torch.arange(rows) % 4
+    elp = torch.log_softmax(z.double(), 1)[which, tokens]
+    w = (torch.rand(rows, generator=g) < 0.3).float()
+    dev = z.cuda()[which.cuda()].contiguous()
+    args = [t.cuda() for t in (tokens, elp.float(), torch.ones(rows), w)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [dcr.policy_loss(dev, *args, grad=i % 2 == 0, stream=streams[i % 2]) for i in range(6)]
+    torch.cuda.synchronize()
+    for loss, lp, grad in got:
+        assert bool(((lp.cpu().double() - elp * (w != 0)).abs() <= 1e-5).all())
+        assert torch.equal(lp, got[0][1]) and torch.equal(loss, got[0][0])
+    assert all(torch.equal(g[2], got[0][2]) for g in got[::2])
