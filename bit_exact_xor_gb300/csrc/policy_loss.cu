@@ -309,29 +309,34 @@ __global__ void __launch_bounds__(TH, resident_blocks(TH, NV)) loss_kernel(LossA
     const uint32_t y = uint32_t(token);
     const float sc = A.sc;
     // m: the row's maximum; others: the sum of exp((x_j - m) / T) without the token's own term, which is ey.  Formed
-    // from others, 1 - p = others / (others + ey) and, for the largest value, log p = -log1p(others) keep their accuracy
-    // where the token is nearly certain: a sum over all values has rounded away what is left beside 1 there.
+    // from others, 1 - p = others / (others + ey) and log p keep their accuracy where the token is nearly certain: a sum
+    // over all values has rounded away what is left beside 1 there.
     float m = -INFINITY, others = 0.0f, ey = 0.0f;
     uint4 q[NV];
     float xy = 0.0f;
     const Row<T> in(x, vocab);
-    const uint32_t yword = (in.skip + y) / N, yat = (in.skip + y) % N;   // where the token's value is
+    // where the token's value is: its word, the place in it, whether this thread has it
+    const uint32_t yword = (in.skip + y) / N, yat = (in.skip + y) % N;
+    const bool mine = yword % step == first;
     if (on) {
         // another block's shared memory may be written once that block is known to run: all say so here, and wait for it
-        // before they write (a row is on in all blocks of its cluster or in none)
+        // while their loads are under way (a row is on in all blocks of its cluster or in none)
         if (cluster > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
 #pragma unroll
         for (int i = 0; i < NV; ++i) q[i] = in.load_whole(first + i * step);
         xy = to_f32(x[y]);
+        if (cluster > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (in.cut(first + i * step)) q[i] = in.load_cut(first + i * step);
 #pragma unroll
         for (int i = 0; i < NV; ++i) m = fmaxf(m, word_max(q[i], T()));
         for (uint32_t k = first + NV * step; k < in.words; k += step) m = fmaxf(m, word_max(in.load(k), T()));
+        if (mine) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (first + i * step == yword) q[i] = without<T>(q[i], yat);
+            for (int i = 0; i < NV; ++i)
+                if (first + i * step == yword) q[i] = without<T>(q[i], yat);
+        }
 #pragma unroll
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
         if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = m;
@@ -351,7 +356,6 @@ __global__ void __launch_bounds__(TH, resident_blocks(TH, NV)) loss_kernel(LossA
 #pragma unroll
         for (int i = 0; i < TH / 32; ++i) s += part[TH / 32 + i];
         if (cluster > 1) {
-            asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
             if (threadIdx.x < cluster) {
                 const uint32_t at = uint32_t(__cvta_generic_to_shared(&all[rank]));
                 asm volatile(
@@ -374,7 +378,8 @@ __global__ void __launch_bounds__(TH, resident_blocks(TH, NV)) loss_kernel(LossA
 
     float c = 0.0f;
     if (on) {
-        const float lp = ey == 1.0f ? -log1pf(others) : (xy - m) * A.inv_temp - logf(s);
+        // log s with what the sum's rounding left out, which is most of it beside ey = 1
+        const float lp = (xy - m) * A.inv_temp - logf(s) - __fdividef(others - (s - ey), s);
         float loss = 0.0f, slope = 0.0f;
         if (A.old_logp) row_loss(A, adv, old, ref, lp, loss, slope);
         if (rank == 0 && threadIdx.x == 0) {
@@ -418,7 +423,7 @@ __global__ void __launch_bounds__(TH, resident_blocks(TH, NV)) loss_kernel(LossA
     if (e.plain) put_all(std::true_type());
     else put_all(std::false_type());
     // the token's own value, by the thread that wrote its word
-    if ((in.skip + y) / N % step == first % step) g[y] = from_f32<T>(c * (others / s));
+    if (mine) g[y] = from_f32<T>(c * (others / s));
 }
 
 // The rows' losses summed in a fixed order: thread i takes rows i, i + 1024,
