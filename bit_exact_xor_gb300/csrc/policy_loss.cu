@@ -135,24 +135,25 @@ __device__ __forceinline__ float word_max(const uint4& q, T)
 
 // exp((x - m) / T) = 2^(x sc - m sc), sc = log2(e) / T: one multiply-add with
 // the rounded product msc = m sc, whose rounding error is the same factor on
-// every term (the row's sum is corrected for it once).  A maximum so large
-// that msc could overflow (a row of the type's lowest values) takes the
-// difference first.  The row's sum takes a second multiply-add with the rest
-// of sc: over a large vocabulary most of it comes from terms far below the
-// maximum, where sc's rounding shifts every one the same way (a row's
-// log-probability by up to 1e-6).  There sc is rounded down, so that the rest
-// is positive and -inf stays -inf.
+// every term (the row's sum is corrected for it once).  That holds while the
+// factor 2^excess is near 1: it is half a unit of msc's last place at most,
+// 2^-5 below |msc| = 2^20.  Beyond (a row far from 0, a temperature near 0)
+// the difference comes first.  The row's sum takes a second multiply-add with
+// the rest of sc: over a large vocabulary most of it comes from terms far
+// below the maximum, where sc's rounding shifts every one the same way (a
+// row's log-probability by up to 1e-6).  There sc is rounded down, so that the
+// rest is positive and -inf stays -inf.
 struct Exponent {
     float sc, lo, m, msc;
     bool plain;
     __device__ __forceinline__ Exponent(float m_, float sc_, float lo_)
-        : sc(sc_), lo(lo_), m(m_), msc(m_ * sc_), plain(fabsf(m_ * sc_) < 1e30f)
+        : sc(sc_), lo(lo_), m(m_), msc(m_ * sc_), plain(fabsf(m_ * sc_) < 1048576.0f)
     {
     }
     template <bool PLAIN>
     __device__ __forceinline__ float term(float x) const
     {
-        return exp2_fast(PLAIN ? fmaf(x, lo, fmaf(x, sc, -msc)) : (x - m) * sc);
+        return exp2_fast(PLAIN ? fmaf(x, lo, fmaf(x, sc, -msc)) : fmaf(x - m, lo, (x - m) * sc));
     }
     __device__ __forceinline__ float term_excess() const { return plain ? fmaf(m, lo, fmaf(m, sc, -msc)) : 0.0f; }
     template <bool PLAIN>

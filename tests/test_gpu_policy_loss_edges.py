@@ -119,3 +119,41 @@ def test_clusters_that_come_and_go(dtype, vocab):
         assert bool(((lp.cpu().double() - elp * (w != 0)).abs() <= 1e-5).all())
         assert torch.equal(lp, got[0][1]) and torch.equal(loss, got[0][0])
     assert all(torch.equal(g[2], got[0][2]) for g in got[::2])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("temp", [1.0, 0.3, 0.1])
+@pytest.mark.parametrize("vocab", [30, 5000, 70000])
+def test_constant_rows_far_from_zero(dtype, vocab, temp):
+    # softmax is uniform whatever the constant; log(V) has a few roundings, and the sum V + 2^-21 of it
+    for v in (1e6, 1e8, 1e9, 5e9, 1e10, 1e12, 1e20, 1e30):
+        for sign in (1, -1):
+            z = torch.full((2, vocab), sign * v, dtype=DT[dtype], device="cuda")
+            t = torch.tensor([0, vocab - 1], device="cuda")
+            one = torch.ones(2, device="cuda")
+            old = torch.full((2,), -math.log(vocab), device="cuda")
+            loss, lp, grad = dcr.policy_loss(z, t, old, one, one, clip_high=1.0, clip_low=0.5, temperature=temp)
+            assert float((lp + math.log(vocab)).abs().max()) <= 1e-5
+            assert abs(float(loss) + 2) <= 1e-4
+            exp = torch.full((2, vocab), 1.0 / vocab, dtype=torch.float64)
+            exp[0, 0] -= 1
+            exp[1, -1] -= 1
+            exp /= temp
+            err = (grad.cpu().double() - exp).abs() / exp.abs()
+            assert float(err.max()) <= 1e-4 + 1.01 * EPS[dtype], (v, sign)
+
+
+@pytest.mark.parametrize("temp", [1e-8, 1e-9, 1e-20, 1e-38])
+@pytest.mark.parametrize("vocab", [30, 5000, 40000])
+def test_temperatures_near_zero(vocab, temp):
+    # ordinary logits: equal ones share the probability, and a larger one takes it all
+    t = torch.tensor([3, 3, 4, 5], device="cuda")
+    for v in (31.7, 20.0, -17.25, 1.0):
+        z = torch.full((4, vocab), v, device="cuda")
+        z[1:, 3] = v + 8
+        z[3, 5] = v + 8
+        lp = dcr.token_logprobs(z, t, temperature=temp).cpu()
+        assert abs(float(lp[0]) + math.log(vocab)) <= 1e-5
+        assert float(lp[1]) == 0.0
+        assert float(lp[2]) <= -7.9 / temp * 0.999 or float(lp[2]) == float("-inf")
+        assert abs(float(lp[3]) + math.log(2)) <= 1e-6
