@@ -13,6 +13,7 @@
 // GB, written 1.05 GB); by the chain of loads, two block-wide steps, a
 // cluster-wide one and stores in short ones (1021 rows of 32771 values: 41
 // us, five rounds of blocks).
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -478,10 +479,13 @@ int launch_rows(const LossArgs& A, cudaStream_t s)
 
 int launch(LossArgs A, uint32_t dtype, float temperature, float* loss, cudaStream_t s)
 {
-    const double sc = 1.4426950408889634 / temperature;
+    // 1 / T and log2(e) / T stay finite for the smallest T, too (0 times them is 0); the rest of the second is positive and
+    // no larger than its rounding, and adds nothing even to the largest logits where there is none
+    const double most = FLT_MAX, sc = std::fmin(1.4426950408889634 / temperature, most);
+    A.inv_temp = float(std::fmin(1.0 / temperature, most));
     A.sc = float(sc);
     A.sc_dn = A.sc > sc ? std::nextafterf(A.sc, 0.0f) : A.sc;
-    A.sc_lo = std::fmax(float(sc - A.sc_dn), 1e-37f);
+    A.sc_lo = std::fmax(float(sc - A.sc_dn), FLT_TRUE_MIN);
     if (A.rows == 0 && !loss) return DCR_OK;
     if (A.rows) {
         const int rc = with_dtype(dtype, [&](auto t) { return launch_rows<decltype(t)>(A, s); });
@@ -534,7 +538,7 @@ extern "C" int dcr_policy_loss(const void* logits, uint32_t dtype, uint64_t rows
         uintptr_t(advantages) % 4 || uintptr_t(weights) % 4 || uintptr_t(loss) % 4 || uintptr_t(row_loss) % 4)
         return set_error(DCR_ERR_INVALID, "dcr_policy_loss: misaligned buffer");
     LossArgs A{logits, grad, rows, vocab, row_stride, grad_stride, tokens, old_logp, ref_logp, advantages, weights,
-               row_loss, logp, 1.0f / opts->temperature, 1.0f - opts->clip_low, 1.0f + opts->clip_high, opts->kl_coef};
+               row_loss, logp, 0.0f, 1.0f - opts->clip_low, 1.0f + opts->clip_high, opts->kl_coef};
     return launch(A, dtype, opts->temperature, loss, static_cast<cudaStream_t>(stream));
 }
 
@@ -544,6 +548,6 @@ extern "C" int dcr_token_logprobs(const void* logits, uint32_t dtype, uint64_t r
     if (int rc = dcr::check("dcr_token_logprobs", logits, dtype, rows, vocab, row_stride, tokens, temperature, logp)) return rc;
     LossArgs A{};
     A.logits = logits, A.rows = rows, A.vocab = vocab, A.row_stride = row_stride;
-    A.tokens = tokens, A.logp = logp, A.inv_temp = 1.0f / temperature;
+    A.tokens = tokens, A.logp = logp;
     return launch(A, dtype, temperature, nullptr, static_cast<cudaStream_t>(stream));
 }

@@ -143,7 +143,7 @@ def test_constant_rows_far_from_zero(dtype, vocab, temp):
             assert float(err.max()) <= 1e-4 + 1.01 * EPS[dtype], (v, sign)
 
 
-@pytest.mark.parametrize("temp", [1e-8, 1e-9, 1e-20, 1e-38])
+@pytest.mark.parametrize("temp", [1e-8, 1e-9, 1e-20, 1e-38, 1e-40, 1e-45])
 @pytest.mark.parametrize("vocab", [30, 5000, 40000])
 def test_temperatures_near_zero(vocab, temp):
     # ordinary logits: equal ones share the probability, and a larger one takes it all
@@ -157,3 +157,15 @@ def test_temperatures_near_zero(vocab, temp):
         assert float(lp[1]) == 0.0
         assert float(lp[2]) <= -7.9 / temp * 0.999 or float(lp[2]) == float("-inf")
         assert abs(float(lp[3]) + math.log(2)) <= 1e-6
+
+
+@pytest.mark.parametrize("vocab", [3, 5000, 40000])
+def test_temperatures_near_the_largest(vocab):
+    # z = x / T of ordinary size from logits near the type's largest
+    for big, temp in ((1e38, 1e38), (1e37, 1e37), (3e30, 1e30)):
+        z = torch.zeros(2, vocab, device="cuda")
+        z[0, 0], z[0, 1], z[1, 2] = big, -big, -big
+        t = torch.tensor([1, 0], device="cuda")
+        exp = torch.log_softmax(z.cpu().double() / float(torch.tensor(temp)), 1)[torch.arange(2), t.cpu()]
+        lp = dcr.token_logprobs(z, t, temperature=temp).cpu().double()
+        assert float((lp - exp).abs().max()) <= 1e-5, (big, temp)
