@@ -253,16 +253,25 @@ __device__ __forceinline__ float words_sum(const uint4 (&q)[NV], float m, float 
     return s;
 }
 
+// exp(v), the largest number where that overflows although v is finite: what
+// is multiplied by 0 then (an advantage, a probability) is 0 as in exact
+// arithmetic, and not NaN.
+__device__ __forceinline__ float exp_finite(float v)
+{
+    const float e = expf(v);
+    return v < INFINITY ? fminf(e, FLT_MAX) : e;
+}
+
 // Loss of a row and its derivative by the log-probability.
 __device__ __forceinline__ void row_loss(const LossArgs& A, float adv, float old, float ref, float lp, float& loss, float& slope)
 {
-    const float ratio = expf(lp - old);
+    const float ratio = exp_finite(lp - old);
     const float u = ratio * adv, c = fminf(fmaxf(ratio, A.lo), A.hi) * adv;
     const bool clipped = c < u;
     loss = clipped ? -c : -u;
     slope = clipped ? 0.0f : -u;
     if (A.kl != 0.0f) {
-        const float k = ref - lp, e = expf(k);
+        const float k = ref - lp, e = exp_finite(k);
         loss += A.kl * (e - k - 1.0f);
         slope += A.kl * (1.0f - e);
     }

@@ -169,3 +169,15 @@ def test_temperatures_near_the_largest(vocab):
         exp = torch.log_softmax(z.cpu().double() / float(torch.tensor(temp)), 1)[torch.arange(2), t.cpu()]
         lp = dcr.token_logprobs(z, t, temperature=temp).cpu().double()
         assert float((lp - exp).abs().max()) <= 1e-5, (big, temp)
+
+
+def test_overflowing_ratio_without_an_advantage():
+    # exp(lp - old) passes the largest 32-bit number; times an advantage of 0 that is 0, as in 64 bits, and with an
+    # advantage above 0 it is clipped
+    z = torch.randn(3, 50, generator=torch.Generator().manual_seed(3)).cuda()
+    t = torch.tensor([1, 2, 3], device="cuda")
+    old = torch.tensor([-100.0, -2000.0, -100.0], device="cuda")
+    adv = torch.tensor([0.0, 0.0, 0.5], device="cuda")
+    loss, lp, grad = dcr.policy_loss(z, t, old, adv, torch.ones(3, device="cuda"), clip_high=0.25)
+    assert abs(float(loss) + 1.25 * 0.5) <= 1e-6
+    assert int(grad.count_nonzero()) == 0 and bool(torch.isfinite(grad).all())
