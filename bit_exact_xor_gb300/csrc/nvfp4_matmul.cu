@@ -839,6 +839,9 @@ int sm_count()
     return n;
 }
 
+// Comes after a call of the runtime's that needs the device's context: on a
+// thread whose first call this is there is none before, and the driver's
+// function fails.
 bool tile_map(CUtensorMap* map, const void* codes, uint64_t rows, uint32_t k, uint32_t box_rows)
 {
     const cuuint64_t dims[2] = {k / 2, rows}, strides[1] = {k / 2};
@@ -867,9 +870,6 @@ int launch(MatmulArgs A, const dcr_nvfp4& x, const dcr_nvfp4& w, uint32_t split,
 {
     using S = Shape<BN>;
     const uint64_t groups = A.experts ? A.experts : 1, wrows = groups * A.n;
-    CUtensorMap mp, mq;
-    if (!tile_map(&mp, w.codes, wrows, A.k, kP) || !tile_map(&mq, x.codes, A.m, A.k, BN))
-        return set_error(DCR_ERR_CUDA, "dcr_nvfp4_matmul: tensor map");
     A.p_scales = static_cast<const uint8_t*>(w.scales);
     A.q_scales = static_cast<const uint8_t*>(x.scales);
     A.p_align = scale_align(w.scales, A.k);
@@ -885,6 +885,9 @@ int launch(MatmulArgs A, const dcr_nvfp4& x, const dcr_nvfp4& w, uint32_t split,
     const int smem = S::kSmem + int(sizeof(Control<S::kStages>) + 4 * groups);
     cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return cuda_error(e, "NVFP4 product attributes");
+    CUtensorMap mp, mq;
+    if (!tile_map(&mp, w.codes, wrows, A.k, kP) || !tile_map(&mq, x.codes, A.m, A.k, BN))
+        return set_error(DCR_ERR_CUDA, "dcr_nvfp4_matmul: tensor map");
     const LaunchAttrs at(grid, kThreads, size_t(smem), split, dependent, s);
     e = cudaLaunchKernelEx(&at.cfg, kernel, mp, mq, A, split);
     return e == cudaSuccess ? DCR_OK : cuda_error(e, "NVFP4 product launch");
@@ -894,9 +897,6 @@ template <typename T>
 int launch_wide(MatmulArgs A, const dcr_nvfp4& x, const dcr_nvfp4& w, bool dependent, cudaStream_t s)
 {
     const uint64_t groups = A.experts ? A.experts : 1, wrows = groups * A.n;
-    CUtensorMap mx, mw;
-    if (!tile_map(&mx, x.codes, A.m, A.k, kP) || !tile_map(&mw, w.codes, wrows, A.k, 256))
-        return set_error(DCR_ERR_CUDA, "dcr_nvfp4_matmul: tensor map");
     A.p_scales = static_cast<const uint8_t*>(x.scales);
     A.q_scales = static_cast<const uint8_t*>(w.scales);
     A.p_align = scale_align(x.scales, A.k);
@@ -908,6 +908,9 @@ int launch_wide(MatmulArgs A, const dcr_nvfp4& x, const dcr_nvfp4& w, bool depen
     const int smem = Wide::kSmem + int(sizeof(Control<Wide::kStages>) + 4 * groups);
     cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return cuda_error(e, "NVFP4 product attributes");
+    CUtensorMap mx, mw;
+    if (!tile_map(&mx, x.codes, A.m, A.k, kP) || !tile_map(&mw, w.codes, wrows, A.k, 256))
+        return set_error(DCR_ERR_CUDA, "dcr_nvfp4_matmul: tensor map");
     const LaunchAttrs at(tiles < uint64_t(sm_count()) ? tiles : sm_count(), Wide::kThreads, size_t(smem), 1, dependent, s);
     e = cudaLaunchKernelEx(&at.cfg, kernel, mx, mw, A);
     return e == cudaSuccess ? DCR_OK : cuda_error(e, "NVFP4 product launch");
