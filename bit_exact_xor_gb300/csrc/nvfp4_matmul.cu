@@ -858,11 +858,13 @@ uint32_t scale_align(const void* p, uint32_t k)
     return a % 16 == 0 ? 16 : a % 4 == 0 ? 4 : 1;
 }
 
-// Shared memory of a kernel whose tile counts take an entry an expert, allowed.
+// Shared memory of a kernel whose tile counts take an entry an expert,
+// allowed for the most experts in every call: the limit belongs to the kernel,
+// not to the call, and another thread may launch it between this and our launch.
 template <typename K>
-cudaError_t allow_smem(K kernel, int smem)
+cudaError_t allow_smem(K kernel, size_t without_counts)
 {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(without_counts + 4 * DCR_MAX_EXPERTS));
 }
 
 template <int BN, typename T>
@@ -882,13 +884,13 @@ int launch(MatmulArgs A, const dcr_nvfp4& x, const dcr_nvfp4& w, uint32_t split,
     if (tiles < grid || split > 1) grid = tiles * split;
     if (grid == 0 || grid >= 1ull << 31) return set_error(DCR_ERR_INVALID, "dcr_nvfp4_matmul: matrix too large");
     auto kernel = matmul_kernel<BN, T>;
-    const int smem = S::kSmem + int(sizeof(Control<S::kStages>) + 4 * groups);
-    cudaError_t e = allow_smem(kernel, smem);
+    const size_t fixed = S::kSmem + sizeof(Control<S::kStages>);
+    cudaError_t e = allow_smem(kernel, fixed);
     if (e != cudaSuccess) return cuda_error(e, "NVFP4 product attributes");
     CUtensorMap mp, mq;
     if (!tile_map(&mp, w.codes, wrows, A.k, kP) || !tile_map(&mq, x.codes, A.m, A.k, BN))
         return set_error(DCR_ERR_CUDA, "dcr_nvfp4_matmul: tensor map");
-    const LaunchAttrs at(grid, kThreads, size_t(smem), split, dependent, s);
+    const LaunchAttrs at(grid, kThreads, fixed + 4 * groups, split, dependent, s);
     e = cudaLaunchKernelEx(&at.cfg, kernel, mp, mq, A, split);
     return e == cudaSuccess ? DCR_OK : cuda_error(e, "NVFP4 product launch");
 }
@@ -905,13 +907,13 @@ int launch_wide(MatmulArgs A, const dcr_nvfp4& x, const dcr_nvfp4& w, bool depen
     if (A.experts) xt = A.m / kP + (A.m < groups ? A.m : groups);
     const uint64_t tiles = xt * ((A.n + 255) / 256);
     auto kernel = matmul_wide_kernel<T>;
-    const int smem = Wide::kSmem + int(sizeof(Control<Wide::kStages>) + 4 * groups);
-    cudaError_t e = allow_smem(kernel, smem);
+    const size_t fixed = Wide::kSmem + sizeof(Control<Wide::kStages>);
+    cudaError_t e = allow_smem(kernel, fixed);
     if (e != cudaSuccess) return cuda_error(e, "NVFP4 product attributes");
     CUtensorMap mx, mw;
     if (!tile_map(&mx, x.codes, A.m, A.k, kP) || !tile_map(&mw, w.codes, wrows, A.k, 256))
         return set_error(DCR_ERR_CUDA, "dcr_nvfp4_matmul: tensor map");
-    const LaunchAttrs at(tiles < uint64_t(sm_count()) ? tiles : sm_count(), Wide::kThreads, size_t(smem), 1, dependent, s);
+    const LaunchAttrs at(tiles < uint64_t(sm_count()) ? tiles : sm_count(), Wide::kThreads, fixed + 4 * groups, 1, dependent, s);
     e = cudaLaunchKernelEx(&at.cfg, kernel, mx, mw, A);
     return e == cudaSuccess ? DCR_OK : cuda_error(e, "NVFP4 product launch");
 }

@@ -2,6 +2,7 @@
 of every size through the compiled binding, back to back; from several
 threads; without the compiled binding."""
 import ctypes
+import sys
 import threading
 
 import pytest
@@ -43,3 +44,43 @@ def test_first_call_of_a_thread(m, n):
     torch.cuda.synchronize()
     assert said[0] == dcr.OK, said
     assert torch.equal(out, exp)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_two_threads_with_and_without_experts(wide):
+    # a product's shared memory grows with the number of experts: calls of both kinds at once, from C, each on its own
+    # stream (ctypes lets go of the interpreter's lock)
+    n, k, e = (256, 64, 1024) if wide else (16, 64, 1024)
+    m = 20 * e if wide else e
+    w, q = _weights(e * n, k, 1), dcr.nvfp4_quantize(_randn(m, k, "f32", 3), per_row=True)[0]
+    off = torch.arange(0, m + 1, m // e, dtype=torch.int32, device="cuda")
+    md, nd = (256, 256 * 80) if wide else (4, 64)
+    wd, qd = _weights(nd, k, 2), dcr.nvfp4_quantize(_randn(md, k, "f32", 4), per_row=True)[0]
+    jobs = [(q, w, m, n, off, e), (qd, wd, md, nd, None, 0)]
+    exp = [dcr.nvfp4_matmul(x, y, offsets=o) for x, y, _, _, o, _ in jobs]
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    call, codes, out = ops._lib().dcr_nvfp4_matmul, [[], []], [torch.empty_like(y) for y in exp]
+    ready = threading.Barrier(2)
+
+    def work(i):
+        x, y, rows, cols, offsets, experts = jobs[i]
+        args = (ctypes.byref(ops._nvfp4(x, "x")[3]), ctypes.byref(ops._nvfp4(y, "w")[3]), rows, cols, k,
+                None if offsets is None else offsets.data_ptr(), experts, out[i].data_ptr(), ops.BF16, cols, streams[i].cuda_stream)
+        ready.wait()
+        codes[i] += [call(*args) for _ in range(10000)]
+
+    before = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(before)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(codes[i]) == 10000 and set(codes[i]) == {dcr.OK}, sum(c != dcr.OK for c in codes[i])
+        assert torch.equal(out[i], exp[i])
