@@ -331,34 +331,39 @@ auto with_bool(bool v, F f)
     return v ? f(std::true_type()) : f(std::false_type());
 }
 
+// By the launch's own status: the thread's last error may be another call's.
+template <typename K, typename... X>
+cudaError_t go(K kernel, unsigned grid, bool dependent, cudaStream_t s, const X&... args)
+{
+    const LaunchAttrs at(grid, kThreads, 0, 1, dependent, s);
+    return cudaLaunchKernelEx(&at.cfg, kernel, args...);
+}
+
 template <typename T, typename V, bool VALUES>
-void launch(const QuantArgs& A, uint32_t mode, float* partial, cudaStream_t s)
+cudaError_t launch(const QuantArgs& A, uint32_t mode, float* partial, cudaStream_t s)
 {
     const bool vec = uintptr_t(A.x) % 16 == 0 && A.row_stride * sizeof(T) % 16 == 0;
     const bool flat = A.row_stride == 16ull * A.bpr || A.rows == 1;
     if (mode == DCR_SCALE_ROW) {
         const uint64_t per = A.bpr <= 32 * kRowBlocks ? kThreads / 32 : 1, want = (A.rows + per - 1) / per;
         const unsigned grid = unsigned(want < 1u << 20 ? want : 1u << 20);
-        with_bool(vec, [&](auto ve) {
-            if (per == 1) quantize_rows_kernel<T, V, kThreads, VALUES, ve.value><<<grid, kThreads, 0, s>>>(A);
-            else quantize_rows_kernel<T, V, 32, VALUES, ve.value><<<grid, kThreads, 0, s>>>(A);
+        return with_bool(vec, [&](auto ve) {
+            if (per == 1) return go(quantize_rows_kernel<T, V, kThreads, VALUES, ve.value>, grid, false, s, A);
+            return go(quantize_rows_kernel<T, V, 32, VALUES, ve.value>, grid, false, s, A);
         });
-        return;
     }
     const uint64_t want = (A.blocks + kThreads - 1) / kThreads;
     const unsigned grid = unsigned(want < DCR_QUANT_PARTIALS ? want : DCR_QUANT_PARTIALS);
-    with_bool(vec, [&](auto ve) {
-        with_bool(flat, [&](auto fl) {
-            if (mode == DCR_SCALE_TENSOR) {
-                QuantArgs B = A;
-                B.partial = partial;
-                B.n_partial = grid;
-                amax_kernel<T, ve.value, fl.value><<<grid, kThreads, 0, s>>>(A, partial);
-                const LaunchAttrs at(grid, kThreads, 0, 1, true, s);
-                cudaLaunchKernelEx(&at.cfg, quantize_kernel<T, V, DCR_SCALE_TENSOR, VALUES, ve.value, fl.value>, B);
-            } else {
-                quantize_kernel<T, V, DCR_SCALE_GIVEN, VALUES, ve.value, fl.value><<<grid, kThreads, 0, s>>>(A);
-            }
+    return with_bool(vec, [&](auto ve) {
+        return with_bool(flat, [&](auto fl) {
+            if (mode != DCR_SCALE_TENSOR)
+                return go(quantize_kernel<T, V, DCR_SCALE_GIVEN, VALUES, ve.value, fl.value>, grid, false, s, A);
+            QuantArgs B = A;
+            B.partial = partial;
+            B.n_partial = grid;
+            const cudaError_t e = go(amax_kernel<T, ve.value, fl.value>, grid, false, s, A, partial);
+            if (e != cudaSuccess) return e;
+            return go(quantize_kernel<T, V, DCR_SCALE_TENSOR, VALUES, ve.value, fl.value>, grid, true, s, B);
         });
     });
 }
@@ -372,11 +377,10 @@ int quantize_launch(const void* x, uint32_t dtype, uint64_t rows, uint64_t cols,
     QuantArgs A{x, scale, nullptr, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), values, rows, row_stride,
                 rows * (cols / 16), uint32_t(cols / 16), 0};
     float* partial = static_cast<float*>(workspace);
-    with_dtype(dtype, [&](auto t) {
+    const cudaError_t e = with_dtype(dtype, [&](auto t) {
         if (!values) return launch<decltype(t), float, false>(A, scale_mode, partial, s);
-        with_dtype(values_dtype, [&](auto v) { launch<decltype(t), decltype(v), true>(A, scale_mode, partial, s); });
+        return with_dtype(values_dtype, [&](auto v) { return launch<decltype(t), decltype(v), true>(A, scale_mode, partial, s); });
     });
-    cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? DCR_OK : cuda_error(e, "NVFP4 quantise launch");
 }
 

@@ -31,6 +31,7 @@ int set_error(int code, const char* fmt, ...)
 
 int cuda_error(cudaError_t e, const char* what)
 {
+    cudaGetLastError();   // it is reported here: the thread's next launch, ours or the caller's, does not find it again
     return set_error(DCR_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 

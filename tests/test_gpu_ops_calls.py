@@ -84,3 +84,34 @@ def test_two_threads_with_and_without_experts(wide):
     for i in range(2):
         assert len(codes[i]) == 10000 and set(codes[i]) == {dcr.OK}, sum(c != dcr.OK for c in codes[i])
         assert torch.equal(out[i], exp[i])
+
+
+def test_a_reported_error_is_not_reported_again():
+    # a status call is not allowed while its stream is being captured: that call says so, and the next ones are good
+    x, w = _randn(5, 64, "f32", 1), _weights(32, 64, 2)
+    y = dcr.nvfp4_linear(x, w)
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        g.capture_begin(capture_error_mode="relaxed")
+        rc = ops._lib().dcr_ops_status(s.cuda_stream)
+        try:
+            g.capture_end()
+        except RuntimeError:
+            pass
+    assert rc == dcr.ERR_CUDA, rc
+    assert ops._lib().dcr_ops_status(torch.cuda.current_stream().cuda_stream) == dcr.OK
+    # straight from C, and through the binding: nothing has cleared the thread's last error in between
+    q = torch.empty(5 * 32, dtype=torch.uint8, device="cuda")
+    sc, t = torch.empty(5 * 4, dtype=torch.uint8, device="cuda"), torch.empty(5, device="cuda")
+    with torch.cuda.stream(s):
+        g2 = torch.cuda.CUDAGraph()
+        g2.capture_begin(capture_error_mode="relaxed")
+        ops._lib().dcr_ops_status(s.cuda_stream)
+        rc = ops._lib().dcr_nvfp4_quantize(x.data_ptr(), ops.F32, 5, 64, 64, ops.SCALE_ROW, t.data_ptr(), q.data_ptr(), sc.data_ptr(),
+                                           None, ops.NONE, None, torch.cuda.default_stream().cuda_stream)
+        try:
+            g2.capture_end()
+        except RuntimeError:
+            pass
+    assert rc == dcr.OK, dcr.last_error()
+    assert torch.equal(dcr.nvfp4_linear(x, w), y)
