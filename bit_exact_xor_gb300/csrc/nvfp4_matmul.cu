@@ -411,6 +411,8 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         fence_before();
     }
+    // The offsets may be read ahead of the wait only because the kernel ahead of a dependent launch is the call's own
+    // quantisation, which is itself launched without that attribute: whatever wrote the offsets has ended before it began.
     if (warp == 3) count_tiles(A, BN, pref, lane);
     grid_wait();   // what is read from here on may come from the kernel before
     __syncthreads();

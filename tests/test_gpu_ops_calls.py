@@ -115,3 +115,48 @@ def test_a_reported_error_is_not_reported_again():
             pass
     assert rc == dcr.OK, dcr.last_error()
     assert torch.equal(dcr.nvfp4_linear(x, w), y)
+
+
+def _then(x, w, offsets=None, dtype=None):
+    q, _ = dcr.nvfp4_quantize(x, per_row=True)
+    return dcr.nvfp4_matmul(q, w, offsets=offsets, dtype=dtype or x.dtype)
+
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f16")])
+@pytest.mark.parametrize("m,n,k", [(1, 6000, 2048), (37, 9728, 96), (40, 9800, 544), (300, 5121, 544), (700, 3333, 2080),
+                                   (257, 5000, 96)])
+def test_linear_of_many_sizes_back_to_back(m, n, k, dtype, out):
+    # the workspace of one call is the next one's: a product that read ahead of its quantisation would take the last one's
+    w = _weights(n, k, 1)
+    xs = [_randn(m, k, dtype, i) * (4.0 ** i) for i in range(5)]
+    exp = [_then(x, w, dtype=DT[out]) for x in xs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = [dcr.nvfp4_linear(x, w, dtype=DT[out]) for x in xs]
+        assert all(torch.equal(a, b) for a, b in zip(got, exp))
+    dcr.ops_status()
+
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f32")])
+@pytest.mark.parametrize("counts", [[3, 0, 1, 9, 0], [1] * 64, [0, 40, 0, 0, 17, 1, 0, 90], [300, 0, 90, 257, 5], [0, 0, 700], [1000] + [0] * 63])
+@pytest.mark.parametrize("n,k", [(72, 96), (2601, 416)])
+def test_linear_of_experts_back_to_back(counts, n, k, dtype, out):
+    # offsets come from a kernel just ahead of the call, as from a router, and change from call to call
+    e, m = len(counts), sum(counts)
+    w = _weights(e * n, k, 2)
+    w = dcr.Nvfp4(w.codes, w.scales, torch.linspace(0.5, 2.0, e, device="cuda"))
+    xs = [_randn(m, k, dtype, i) * (4.0 ** i) for i in range(4)]
+    each = [torch.tensor(counts[i:] + counts[:i], device="cuda") for i in range(4)]
+    offs = [torch.cat([c.new_zeros(1), c.cumsum(0)]).to(torch.int32) for c in each]
+    exp = [_then(x, w, o, DT[out]) for x, o in zip(xs, offs)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for x, c in zip(xs, each):
+            off = torch.cat([c.new_zeros(1), c.cumsum(0)]).to(torch.int32)
+            got.append(dcr.nvfp4_linear(x, w, offsets=off, dtype=DT[out]))
+        assert all(torch.equal(a, b) for a, b in zip(got, exp))
+    # through the call with every argument spelled out, too
+    into = torch.empty(m, n, dtype=DT[out], device="cuda")
+    assert torch.equal(dcr.nvfp4_linear(xs[0], w, offsets=offs[0], out=into), exp[0])
+    dcr.ops_status()
