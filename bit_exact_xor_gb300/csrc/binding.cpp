@@ -62,7 +62,9 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n)
     HANDLE_TH_ERRORS
     Matrix x;
     if (n != 4 || !x.set(a[0]) || x.cols % 16) Py_RETURN_NONE;
-    const bool per_row = a[2] == Py_True, given = a[1] != Py_None;
+    const int per_row = PyObject_IsTrue(a[2]);
+    if (per_row < 0) return nullptr;
+    const bool given = a[1] != Py_None;
     const long vt = PyLong_AsLong(a[3]);
     if (vt < DCR_F32 || vt > DCR_NONE) Py_RETURN_NONE;
     void* sp = nullptr;

@@ -160,3 +160,11 @@ def test_linear_of_experts_back_to_back(counts, n, k, dtype, out):
     into = torch.empty(m, n, dtype=DT[out], device="cuda")
     assert torch.equal(dcr.nvfp4_linear(xs[0], w, offsets=offs[0], out=into), exp[0])
     dcr.ops_status()
+
+
+def test_per_row_is_a_truth_value():
+    x = _randn(5, 64, "f32", 1)
+    for yes in (True, 1):
+        assert dcr.nvfp4_quantize(x, per_row=yes)[0].scale.shape == (5,)
+    for no in (False, 0):
+        assert dcr.nvfp4_quantize(x, per_row=no)[0].scale.shape == (1,)
