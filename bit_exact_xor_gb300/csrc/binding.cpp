@@ -61,7 +61,7 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
     Matrix x;
-    if (n != 4 || !x.set(a[0]) || x.cols % 16) Py_RETURN_NONE;
+    if (n != 4 || !x.set(a[0]) || x.cols % 16 || x.t.numel() == 0) Py_RETURN_NONE;
     const int per_row = PyObject_IsTrue(a[2]);
     if (per_row < 0) return nullptr;
     const bool given = a[1] != Py_None;

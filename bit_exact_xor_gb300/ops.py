@@ -159,7 +159,8 @@ def nvfp4_quantize(x, scale=None, per_row=False, values=None, out=None, stream=N
     is a tensor [rows, cols], or a type to make one of, that receives what the
     codes stand for.  `out` is an Nvfp4 whose tensors are written (its scale
     is an output, too, unless `scale` is given), for example views of a
-    trainer arena.  Returns (Nvfp4, values or None)."""
+    trainer arena.  Returns (Nvfp4, values or None); the computed scale of an
+    empty matrix is 1."""
     if out is None and stream is None:
         r = _fast.quantize(x, scale, per_row, NONE if values is None else DTYPES.get(values, -1)) if values.__class__ in _TYPES else None
         if r is not None:
@@ -196,6 +197,8 @@ def nvfp4_quantize(x, scale=None, per_row=False, values=None, out=None, stream=N
             sc = _empty(n, dtype=_f32, device=dev)
         else:
             _flat(sc, n, _f32, "scale", dev)
+        if x.numel() == 0:
+            sc.fill_(1.0)    # the library launches nothing
     vt = NONE
     if values is not None:
         if isinstance(values, torch.dtype):

@@ -7,9 +7,9 @@
  * stream-ordered and return without waiting for the GPU (as dcr_dense_refit
  * does), so they can be captured into a CUDA graph.  A bad argument is
  * refused with DCR_ERR_INVALID before anything is launched; sizes of zero are
- * valid and launch nothing (dcr_policy_loss of no rows still writes a loss of
- * 0).  Device buffers belong to the caller; no call keeps an address after it
- * returns, so calls on several streams may overlap.
+ * valid and launch nothing (no scale is written, but dcr_policy_loss of no rows
+ * still writes a loss of 0).  Device buffers belong to the caller; no call
+ * keeps an address after it returns, so calls on several streams may overlap.
  *
  * NVFP4.  A matrix [rows, cols] is held as codes [rows, cols / 2] (e2m1, two
  * per byte, the even column in the low nibble), scales [rows, cols / 16]

@@ -168,3 +168,16 @@ def test_per_row_is_a_truth_value():
         assert dcr.nvfp4_quantize(x, per_row=yes)[0].scale.shape == (5,)
     for no in (False, 0):
         assert dcr.nvfp4_quantize(x, per_row=no)[0].scale.shape == (1,)
+
+
+@pytest.mark.parametrize("per_row", [False, True])
+@pytest.mark.parametrize("shape", [(0, 32), (3, 0), (0, 0)])
+def test_scale_of_an_empty_matrix_is_one(shape, per_row):
+    # as of any matrix without a finite value other than 0
+    junk = [torch.full((64,), 7.0, device="cuda") for _ in range(64)]   # what a new tensor may find in its memory
+    del junk
+    for out in (None, dcr.Nvfp4(torch.empty(shape[0], shape[1] // 2, dtype=torch.uint8, device="cuda"),
+                                torch.empty(shape[0], shape[1] // 16, dtype=torch.uint8, device="cuda"),
+                                torch.full((shape[0] if per_row else 1,), 7.0, device="cuda"))):
+        q, _ = dcr.nvfp4_quantize(torch.empty(shape, device="cuda"), per_row=per_row, out=out)
+        assert q.scale.shape == (shape[0] if per_row else 1,) and bool((q.scale == 1).all())
