@@ -3,6 +3,7 @@
 // kernels want them, on the current stream.  Each function returns None where
 // a call is not of that kind; ops.py then takes it, with every check and
 // message spelled out.  A status other than DCR_OK comes back as an int.
+// torch_version names the torch that it was built for (-DDCR_TORCH_VERSION).
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -174,4 +175,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding()
+{
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", DCR_TORCH_VERSION) < 0) Py_CLEAR(m);
+    return m;
+}

@@ -8,9 +8,11 @@ tensors handed in must be ready there.  A refused argument raises DcrError.
 The smallest of these operators take a few microseconds on the GPU, so their
 common calls (tensors on the current device, new outputs, the current stream)
 go through the compiled csrc/binding.cpp; it hands back what it does not
-take, refusals among it, to the code below.
+take, refusals among it, to the code below.  Where it is missing or was built
+for another torch, a warning says so and every call takes that code.
 """
 import ctypes
+import warnings
 from typing import NamedTuple
 
 import torch
@@ -74,10 +76,27 @@ def _refuse(what):
     raise DcrError(ERR_INVALID, what)
 
 
-try:
-    from . import _binding as _fast
-except ImportError as e:
-    raise RuntimeError("the operators' binding is not built; run __graft_entry__.build()") from e
+class _NoBinding:
+    """In the compiled binding's place: takes no call, so that each goes on to
+    the code below and through ctypes to the same kernels."""
+    quantize = linear = loss = logprobs = staticmethod(lambda *args: None)
+
+
+def _binding():
+    """The compiled binding if it is there and was built for this torch."""
+    try:
+        from . import _binding as fast
+        if fast.torch_version == torch.__version__:
+            return fast
+        why = "it was built for torch %s" % fast.torch_version
+    except (ImportError, AttributeError) as e:
+        why = str(e)
+    warnings.warn("the operators' compiled binding is not used (%s): calls take a few microseconds more; "
+                  "__graft_entry__.build() makes it" % why)
+    return _NoBinding
+
+
+_fast = _binding()
 
 
 def _result_of(r):

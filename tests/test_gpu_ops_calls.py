@@ -2,6 +2,8 @@
 of every size through the compiled binding, back to back; from several
 threads; without the compiled binding."""
 import ctypes
+import os
+import subprocess
 import sys
 import threading
 
@@ -13,6 +15,7 @@ pytestmark = pytest.mark.gpu
 import bit_exact_xor_gb300 as dcr  # noqa: E402
 from bit_exact_xor_gb300 import ops  # noqa: E402
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 
 
@@ -181,3 +184,31 @@ def test_scale_of_an_empty_matrix_is_one(shape, per_row):
                                 torch.full((shape[0] if per_row else 1,), 7.0, device="cuda"))):
         q, _ = dcr.nvfp4_quantize(torch.empty(shape, device="cuda"), per_row=per_row, out=out)
         assert q.scale.shape == (shape[0] if per_row else 1,) and bool((q.scale == 1).all())
+
+
+WITHOUT = """
+import sys, warnings
+warnings.simplefilter("ignore")
+sys.modules["bit_exact_xor_gb300._binding"] = None    # as if it had not been built
+import torch
+import bit_exact_xor_gb300 as dcr
+x = torch.randn(40, 512, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+w, v = dcr.nvfp4_quantize(torch.randn(96, 512, generator=torch.Generator().manual_seed(2)).cuda(), values=torch.float32)
+y = dcr.nvfp4_linear(x, w)
+t = torch.arange(40, device="cuda")
+one = torch.ones(40, device="cuda")
+lp = dcr.token_logprobs(y, t)
+out = dcr.policy_loss(y, t, lp, one, one)
+torch.save([a.cpu() for a in (w.codes, w.scales, w.scale, v, y, lp) + tuple(out)], sys.argv[1])
+"""
+
+
+def test_every_operator_without_the_compiled_binding(tmp_path):
+    # the library's kernels run through ctypes then, with the same results
+    got = []
+    for i, code in enumerate((WITHOUT, WITHOUT.replace("sys.modules[", "dict()["))):
+        path = str(tmp_path / ("%d.pt" % i))
+        p = subprocess.run([sys.executable, "-c", code, path], cwd=ROOT, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, timeout=600)
+        assert p.returncode == 0, p.stdout.decode()[-2000:]
+        got.append(torch.load(path))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
