@@ -87,8 +87,16 @@ int dcr_nvfp4_matmul(const dcr_nvfp4* x, const dcr_nvfp4* w, uint64_t m, uint64_
  * x is quantised with a scale per row, so that a row's result does not depend
  * on the rows beside it, then multiplied as in dcr_nvfp4_matmul.  workspace
  * (device, 16-byte aligned, DCR_LINEAR_WORKSPACE bytes) holds the quantised
- * activations during the call. */
+ * activations during the call.  The size is a function's, in 64 bits whatever
+ * the types of m and k. */
 #define DCR_LINEAR_WORKSPACE(m, k) ((m) * ((k) / 2 + (k) / 16 + 4) + 4)
+#ifdef __cplusplus
+    constexpr uint64_t dcr_linear_workspace(uint64_t m, uint64_t k) { return DCR_LINEAR_WORKSPACE(m, k); }
+#else
+    static inline uint64_t dcr_linear_workspace(uint64_t m, uint64_t k) { return DCR_LINEAR_WORKSPACE(m, k); }
+#endif
+#undef DCR_LINEAR_WORKSPACE
+#define DCR_LINEAR_WORKSPACE(m, k) dcr_linear_workspace(m, k)
 int dcr_nvfp4_linear(const void* x, uint32_t x_dtype, uint64_t x_stride, const dcr_nvfp4* w, uint64_t m, uint64_t n,
                      uint64_t k, const int32_t* offsets, uint32_t experts, void* y, uint32_t dtype,
                      uint64_t y_stride, void* workspace, void* stream);
