@@ -8,11 +8,12 @@
 // distributed shared memory once.  What does not fit on the chip that way is
 // read again.
 //
-// Bound by its traffic in long batches: 4096 rows of 128256 bf16 values in 361
-// us, 5.1 TB/s of what it moves (a quarter of the rows is left out: read 0.79
-// GB, written 1.05 GB); by the chain of loads, two block-wide steps, a
-// cluster-wide one and stores in short ones (1021 rows of 32771 values: 41
-// us, five rounds of blocks).
+// Bound by its traffic in long batches: 4096 rows of 128256 bf16 values in 375
+// us, 4.9 TB/s of what it moves (a quarter of the rows is left out: read 0.79
+// GB, written 1.05 GB), of which keeping the token's term apart is about 9;
+// by the chain of loads, two block-wide steps, two cluster-wide ones and
+// stores in short ones (1021 rows of 32771 values: 43 us, five rounds of
+// blocks).
 #include <cfloat>
 #include <cmath>
 #include <type_traits>
@@ -292,8 +293,8 @@ __device__ __noinline__ void store_values(T* row, uint32_t skip, uint32_t vocab,
 
 // Blocks on an SM: what bounds the kernel is how many words are in flight, so
 // registers are held to what that takes (4096 rows of 128256 bf16 values,
-// 8 words a thread: 495 us with two blocks of 256 threads, 405 with three,
-// 347 with four).
+// 8 words a thread, before sums and the token's term took their present form:
+// 495 us with two blocks of 256 threads, 405 with three, 347 with four).
 constexpr int resident_blocks(int th, int nv) { return (nv >= 6 ? 1024 : nv >= 4 ? 1536 : 2048) / th; }
 
 // TH threads a block, NV words a thread kept, `cluster` blocks a row.
@@ -476,7 +477,7 @@ int launch_rows(const LossArgs& A, cudaStream_t s)
     if (words <= 256) return launch_rows<T, 128, 2>(A, 1, s);
     if (words <= 512) return launch_rows<T, 128, 4>(A, 1, s);
     // a row that eight such blocks do not hold: blocks of 512 (512 rows of 300000 f32 values: 356 -> 282 us; on rows
-    // that the smaller blocks hold they are no faster: 347 -> 365 us at 128256 bf16 values)
+    // that the smaller blocks hold they are no faster: 347 -> 365 us at 128256 bf16 values then)
     if (words > 2048 * kMaxCluster)
         return launch_rows<T, 512, 8>(A, words > 4096 * kMaxCluster ? kMaxCluster : uint32_t((words + 4095) / 4096), s);
     const uint32_t cluster = uint32_t((words + 2047) / 2048);

@@ -3,7 +3,8 @@ product of NVFP4 operands, and the policy loss.  Argument marshalling only, as
 in the rest of the binding; tensors that are not given are allocated with
 torch, and every call runs on `stream` (default: the current stream) without
 waiting for it.  What a call allocates belongs to the stream that it runs on;
-tensors handed in must be ready there.  A refused argument raises DcrError.
+tensors handed in must be ready there, and are kept by the caller until the
+call has run.  A refused argument raises DcrError.
 
 The smallest of these operators take a few microseconds on the GPU, so their
 common calls (tensors on the current device, new outputs, the current stream)
@@ -285,7 +286,7 @@ def nvfp4_matmul(x, w, offsets=None, dtype=torch.bfloat16, out=None, stream=None
 def nvfp4_linear(x, w, offsets=None, dtype=None, out=None, stream=None):
     """dcr_nvfp4_linear: y = x w^T for activations x [m, k] (float32, bfloat16
     or float16), which are quantised with a scale per row, so that a row's
-    result does not depend on the rows beside it, then multiplied as in
+    codes do not depend on the rows beside it, then multiplied as in
     nvfp4_matmul.  dtype defaults to x's type."""
     if out is None and stream is None:
         t = DTYPES.get(x.dtype if dtype is None else dtype)

@@ -57,18 +57,25 @@ typedef struct {
  * (nullable, [rows, cols] contiguous, 16-byte aligned, of values_dtype;
  * DCR_NONE without) receives what the codes stand for, rounded once to its
  * type: the weights that a quantisation-aware forward pass computes with.
- * The gradient of a quantisation-aware pass goes straight through: no value
- * saturates, except under a GIVEN scale.  workspace (TENSOR only, device, at
- * least DCR_QUANT_PARTIALS floats) holds partial maxima during the call. */
+ * The gradient of a quantisation-aware pass goes straight through.  A block's
+ * largest value is kept to a sixteenth, the rounding of its scale, unless the
+ * scale is GIVEN and too small or the block lies far below its matrix or row:
+ * where its largest value is under amax / 28672 the scale is a subnormal e4m3
+ * number, rounded down by as much as a third (largest values then saturate) or
+ * to 0.  workspace (TENSOR only, device, at least DCR_QUANT_PARTIALS floats)
+ * holds partial maxima during the call. */
 #define DCR_QUANT_PARTIALS 1216u
 int dcr_nvfp4_quantize(const void* x, uint32_t dtype, uint64_t rows, uint64_t cols, uint64_t row_stride,
                        uint32_t scale_mode, float* scale, void* codes, void* scales, void* values,
                        uint32_t values_dtype, void* workspace, void* stream);
 
 /* y [m, n] (dtype, rows y_stride elements apart) = x w^T, x [m, k] and w
- * [n, k] both NVFP4, k a multiple of 32.  The sums are held in 32 bits and
- * rounded once.  x->scale_count is 1 or m, w->scale_count 1 or the number
- * of experts.
+ * [n, k] both NVFP4, k a multiple of 32: the product of the two 32-bit scales
+ * times a sum that is held in 32 bits, rounded once.  e4m3 scales are not
+ * negative.  x->scale_count is 1 or m, w->scale_count 1 or the number of
+ * experts.  The same call gives the same bits every time; which kernel and how
+ * many parts of k a row's sum has goes by the sizes, so that a row alone and the
+ * same row in a larger batch may differ by the rounding of 32-bit sums.
  * experts > 0: w is [experts * n, k], one matrix after another, and offsets
  * (device, experts + 1 entries, not decreasing) says which rows of x belong
  * to which: rows offsets[e] to offsets[e + 1] are multiplied by matrix e.
@@ -84,8 +91,8 @@ int dcr_nvfp4_matmul(const dcr_nvfp4* x, const dcr_nvfp4* w, uint64_t m, uint64_
                      void* stream);
 
 /* y = x w^T for activations x [m, k] (x_dtype, rows x_stride elements apart):
- * x is quantised with a scale per row, so that a row's result does not depend
- * on the rows beside it, then multiplied as in dcr_nvfp4_matmul.  workspace
+ * x is quantised with a scale per row, so that a row's codes and scales do not
+ * depend on the rows beside it, then multiplied as in dcr_nvfp4_matmul.  workspace
  * (device, 16-byte aligned, DCR_LINEAR_WORKSPACE bytes) holds the quantised
  * activations during the call.  The size is a function's, in 64 bits whatever
  * the types of m and k. */
@@ -108,6 +115,8 @@ int dcr_nvfp4_linear(const void* x, uint32_t x_dtype, uint64_t x_stride, const d
  *   u = exp(lp - o) A,  c = clip(exp(lp - o), 1 - clip_low, 1 + clip_high) A,
  *   l = -min(u, c) + kl_coef (exp(q - lp) - (q - lp) - 1),
  *   loss = sum_rows w l,  grad_j = d loss / d logits_j.
+ * An exponential that overflows 32 bits at a finite argument counts as the
+ * largest 32-bit number, so that an advantage of 0 times it is 0.
  * A row whose weight is 0 or whose token lies outside [0, vocab) is left out:
  * its logits are not read, its log-probability and loss are 0 and its
  * gradient is 0, whatever its logits hold.  ref_logp may be NULL if kl_coef
