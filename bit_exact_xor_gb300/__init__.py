@@ -425,15 +425,21 @@ def make_desc(name, elem_bits, rows, cols, split, tp, shard_offset, recv_offset,
 
 
 # The operators around a refit need torch, which the calls above import only
-# when they use it: they are looked up in .ops at their first use.
-_OPS = ("Nvfp4", "nvfp4_quantize", "nvfp4_matmul", "nvfp4_linear", "policy_loss", "token_logprobs",
-        "ops_status")
+# when they use it: they are looked up in their modules at their first use.
+_OPS = {
+    "ops": ("Nvfp4", "nvfp4_quantize", "nvfp4_matmul", "nvfp4_linear", "policy_loss", "token_logprobs", "ops_status"),
+    "scores": ("TokenScores", "token_scores", "token_scores_grad"),
+    "experts": ("Route", "route_experts", "route_experts_grad", "experts_gather", "experts_combine", "experts_combine_grad"),
+    "adamw": ("AdamState32", "AdamState8", "adamw_states", "adamw_step", "grad_norm"),
+}
 
 
 def __getattr__(name):
-    if name in _OPS:
-        from . import ops
-        for n in _OPS:
-            globals()[n] = getattr(ops, n)
-        return globals()[name]
+    for module, names in _OPS.items():
+        if name in names:
+            from importlib import import_module
+            found = import_module("." + module, __name__)
+            for n in names:
+                globals()[n] = getattr(found, n)
+            return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))

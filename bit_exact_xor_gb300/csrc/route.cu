@@ -1,0 +1,619 @@
+// Routing of tokens to experts, and its gradient (include/dcr_ops.h).
+//
+// A warp takes a token: each lane holds PER consecutive experts, and k rounds
+// of a maximum over the warp find the chosen ones in order.  Where scores are
+// compared (with a bias, or for groups), 32 bits do not tell near ones apart:
+// it is noted whether two neighbours in that order, or the last chosen
+// and one that is not, lie nearer than the error of 32-bit scores allows, which happens to about one token in a
+// thousand, and such a token is decided again with scores in 64 bits.
+//
+// The experts' order is a counting sort that keeps the tokens' order: blocks
+// count what their tokens chose (route_kernel), a warp an expert adds up the
+// blocks' counts (scan_kernel), and the same blocks place their slots
+// (place_kernel).  A small batch takes one block and one launch.
+#include <algorithm>
+#include <cmath>
+
+#include "ops_internal.h"
+
+namespace dcr {
+namespace {
+
+struct RouteArgs {
+    const void* logits;
+    const float* bias;
+    const uint8_t* mask;
+    int32_t* chosen;
+    float* weights;
+    int32_t* offsets;
+    int32_t* order;
+    int32_t* positions;
+    uint32_t* counts;       // [parts][experts], then a total for each expert
+    uint64_t tokens, row_stride;
+    uint32_t experts, parts, per_part;
+    uint32_t k, groups, group_top, group_by, group_size;
+    bool sigmoid, renormalise, by_logit;
+    float scale;
+};
+
+// Order of values as whole numbers: 0 for what cannot be chosen.
+__device__ __forceinline__ uint32_t order_of(float v)
+{
+    const uint32_t b = __float_as_uint(v + 0.0f);    // -0 is 0
+    return !(v > -INFINITY) ? 0u : b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t order_of(double v)
+{
+    const uint64_t b = uint64_t(__double_as_longlong(v + 0.0));
+    return !(v > -double(INFINITY)) ? 0ull : b >> 63 ? ~b : b | 1ull << 63;
+}
+__device__ __forceinline__ float value_of(uint32_t o, float) { return __uint_as_float(o >> 31 ? o & 0x7FFFFFFFu : ~o); }
+__device__ __forceinline__ double value_of(uint64_t o, double)
+{
+    return __longlong_as_double(static_cast<long long>(o >> 63 ? o & ~(1ull << 63) : ~o));
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(~0u, v); }
+__device__ __forceinline__ uint64_t warp_max(uint64_t v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = max(v, uint64_t(__shfl_xor_sync(~0u, static_cast<unsigned long long>(v), o)));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
+__device__ __forceinline__ double warp_sum(double v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
+    return v;
+}
+
+__device__ __forceinline__ float exp_of(float v) { return expf(v); }
+__device__ __forceinline__ double exp_of(double v) { return exp(v); }
+
+template <typename V>
+__device__ __forceinline__ V sigmoid_of(V x)
+{
+    const V e = exp_of(x < V(0) ? x : -x);
+    return (x < V(0) ? e : V(1)) / (V(1) + e);
+}
+
+// exp(x - m) where m is the largest; equal infinities are 1
+template <typename V>
+__device__ __forceinline__ V below(V x, V m)
+{
+    return x == m ? V(1) : exp_of(x - m);
+}
+
+// What a token chose: lane j has its j-th expert (-1: none) and that one's logit.
+struct Choice {
+    int32_t expert;
+    float logit;
+};
+
+// The k best experts by keys of type V.  Returns whether keys of 32 bits left
+// an order open that the choice or its order depends on.
+template <int PER, typename V>
+__device__ __forceinline__ bool choose(const float (&x)[PER], const RouteArgs& A, Choice& out)
+{
+    using O = decltype(order_of(V()));
+    const uint32_t lane = threadIdx.x % 32, first = lane * PER;
+    O key[PER];
+    V most = V(1);     // the largest score
+    if (A.by_logit) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[i] = order_of(V(x[i]));
+    } else {
+        V m = V(0), total = V(1);
+        if (!A.sigmoid) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) top = fmaxf(top, x[i]);
+            m = V(warp_max(top));
+            V s = V(0);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) s += x[i] > -INFINITY ? below(V(x[i]), m) : V(0);
+            total = warp_sum(s);
+            most = V(1) / total;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            V v = A.sigmoid ? sigmoid_of(V(x[i])) : below(V(x[i]), m) / total;
+            if (A.bias && first + i < A.experts) v += V(A.bias[first + i]);
+            key[i] = x[i] > -INFINITY ? order_of(v) : O(0);
+        }
+    }
+    // The error of a 32-bit key in units of 2^-24: the exponential's 4, a sum's and a quotient's; for softmax those of up
+    // to 37 additions and of a difference of up to 60 from the maximum, too.  Beside it half a unit of s + bias.
+    const bool exact = sizeof(V) == 8 || A.by_logit;
+    const V slack = V(0x1p-24) * (A.sigmoid ? V(12) : V(256)) * most;
+    auto near = [&](V a, V b, V parts) { return !exact && a - b <= slack * parts + V(0x1p-23) * parts * (fabs(a) + fabs(b)); };
+    bool open = false;
+    if (A.groups > 1) {
+        // lane g: the order of group g's score
+        O score = 0;
+        const uint32_t lanes = A.group_size / PER;
+        auto join = [&](O a, O b) { return a == 0 ? O(0) : b == 0 || A.group_by == 1 ? a : order_of(value_of(a, V()) + value_of(b, V())); };
+        if (lanes * PER == A.group_size && (lanes & (lanes - 1)) == 0) {
+            // groups of whole lanes, a power of two of them
+            O a = 0, b = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                b = max(b, min(a, key[i]));
+                a = max(a, key[i]);
+            }
+            for (uint32_t o = 1; o < lanes; o <<= 1) {
+                const O c = __shfl_xor_sync(~0u, a, o), d = __shfl_xor_sync(~0u, b, o);
+                b = max(min(a, c), max(b, d));
+                a = max(a, c);
+            }
+            score = __shfl_sync(~0u, join(a, b), (lane * lanes) & 31);
+            if (lane >= A.groups) score = 0;
+        } else {
+            for (uint32_t g = 0; g < A.groups; ++g) {
+                O a = 0, b = 0;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const uint32_t e = first + i;
+                    const O v = e >= g * A.group_size && e < (g + 1) * A.group_size ? key[i] : O(0);
+                    b = max(b, min(a, v));
+                    a = max(a, v);
+                }
+                const O top = warp_max(a);
+                const uint32_t who = __ffs(__ballot_sync(~0u, a == top)) - 1;
+                const O next = warp_max(lane == who ? b : a);
+                if (lane == g) score = join(top, next);
+            }
+        }
+        uint32_t taken = 0;
+        O last = 0;
+        for (uint32_t r = 0; r <= A.group_top; ++r) {
+            const O top = warp_max(score);
+            if (top == 0) break;
+            if (r == A.group_top) {
+                open |= near(value_of(last, V()), value_of(top, V()), V(2));
+                break;
+            }
+            const uint32_t who = __ffs(__ballot_sync(~0u, score == top)) - 1;
+            taken |= 1u << who;
+            if (lane == who) score = 0;
+            last = top;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (!(taken >> min((first + i) / A.group_size, 31u) & 1)) key[i] = 0;
+    }
+    out = {-1, 0.0f};
+    O last = 0;
+    int32_t last_expert = -1;
+    float last_logit = 0.0f;
+    for (uint32_t r = 0; r < A.k; ++r) {
+        O best = 0;
+        int32_t at = 0;
+        float logit = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (key[i] > best) best = key[i], at = i, logit = x[i];
+        const O top = warp_max(best);
+        if (top == 0) {
+            last = 0;
+            break;
+        }
+        const uint32_t who = __ffs(__ballot_sync(~0u, best == top)) - 1;    // lanes hold ascending experts: the lowest of equal ones
+        const int32_t expert = __shfl_sync(~0u, int32_t(first) + at, who);
+        logit = __shfl_sync(~0u, logit, who);
+        // equal ones are so in any precision
+        if (r && near(value_of(last, V()), value_of(top, V()), V(1)))
+            open |= !(last_logit == logit && (!A.bias || A.bias[last_expert] == A.bias[expert]));
+        if (lane == r) out = {expert, logit};
+        if (lane == who) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (i == at) key[i] = 0;
+        }
+        last = top, last_expert = expert, last_logit = logit;
+    }
+    if (!exact && last != 0) {
+        // whatever was not chosen, against the last that was
+        const V worst = value_of(last, V());
+        bool tie = false;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (key[i] != 0 && near(worst, value_of(key[i], V()), V(1)))
+                tie |= !(last_logit == x[i] && (!A.bias || A.bias[last_expert] == A.bias[first + i]));
+        open |= __any_sync(~0u, tie);
+    }
+    return open;
+}
+
+template <int PER, typename T>
+__device__ __forceinline__ void load_row(const T* row, uint32_t experts, float (&x)[PER])
+{
+    const uint32_t first = threadIdx.x % 32 * PER;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) x[i] = first + i < experts ? to_f32(row[first + i]) : -INFINITY;
+}
+
+// Weights of the chosen experts from their logits, before the scale; for a
+// softmax that is not renormalised m and total are the row's.
+__device__ __forceinline__ float weight_of(const Choice& c, bool sigmoid, bool renormalise, float m, float total)
+{
+    const bool on = c.expert >= 0;
+    if (!renormalise) return !on ? 0.0f : sigmoid ? sigmoid_of(c.logit) : below(c.logit, m) / total;
+    // relative to the largest, so that a sum of tiny scores keeps its digits
+    const float top = warp_max(on ? c.logit : -INFINITY);
+    float w = 0.0f;
+    if (on && !sigmoid) w = below(c.logit, top);
+    if (on && sigmoid) w = c.logit >= 0.0f ? sigmoid_of(c.logit) : expf(c.logit - fminf(top, 0.0f)) / (1.0f + expf(c.logit));
+    const float s = warp_sum(w);
+    return s > 0.0f ? w / s : 0.0f;
+}
+
+template <int PER>
+__device__ __forceinline__ void softmax_of(const float (&x)[PER], float& m, float& total)
+{
+    m = -INFINITY, total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) m = fmaxf(m, x[i]);
+    m = warp_max(m);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) total += x[i] > -INFINITY ? below(x[i], m) : 0.0f;
+    total = warp_sum(total);
+}
+
+// Decided again in 64 bits; apart, so that its registers do not weigh on the others.
+template <int PER>
+__device__ __noinline__ void choose_again(const float* x, const RouteArgs& A, Choice* c)
+{
+    float v[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = x[i];
+    Choice out;
+    choose<PER, double>(v, A, out);
+    *c = out;
+}
+
+// A token by a warp; its experts are counted in `counts`.
+template <int PER, typename T>
+__device__ __forceinline__ Choice route_token(const RouteArgs& A, uint64_t token, uint32_t* counts)
+{
+    const uint32_t lane = threadIdx.x % 32;
+    Choice c = {-1, 0.0f};
+    float w = 0.0f;
+    if (!A.mask || A.mask[token]) {
+        float x[PER], m = 0.0f, total = 1.0f;
+        load_row<PER, T>(static_cast<const T*>(A.logits) + token * A.row_stride, A.experts, x);
+        if (choose<PER, float>(x, A, c)) choose_again<PER>(x, A, &c);
+        if (!A.sigmoid && !A.renormalise) softmax_of(x, m, total);
+        w = weight_of(c, A.sigmoid, A.renormalise, m, total) * A.scale;
+    }
+    if (lane < A.k) {
+        A.chosen[token * A.k + lane] = c.expert;
+        A.weights[token * A.k + lane] = c.expert < 0 ? 0.0f : w;
+        if (c.expert >= 0) atomicAdd(&counts[c.expert], 1u);
+    }
+    return c;
+}
+
+// Exclusive sums of v[0..n) in place, by a whole block; returns the total.
+template <int TH>
+__device__ __forceinline__ uint32_t scan(uint32_t* v, uint32_t n)
+{
+    __shared__ uint32_t part[TH / 32];
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    uint32_t base = 0;
+    for (uint32_t at = 0; at < n; at += TH) {
+        const uint32_t i = at + threadIdx.x, mine = i < n ? v[i] : 0;
+        uint32_t s = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(~0u, s, o);
+            if (lane >= uint32_t(o)) s += u;
+        }
+        if (lane == 31) part[warp] = s;
+        __syncthreads();
+        uint32_t before = base;
+        for (uint32_t w = 0; w < TH / 32; ++w) {
+            if (w < warp) before += part[w];
+            base += part[w];
+        }
+        __syncthreads();
+        if (i < n) v[i] = before + s - mine;
+    }
+    __syncthreads();
+    return base;
+}
+
+// Slots begin to end into their rows, in their order; next[e]: the next row of expert e.
+template <int TH>
+__device__ __forceinline__ void place(const RouteArgs& A, const int32_t* chosen, uint64_t begin, uint64_t end, uint32_t* next)
+{
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    for (uint64_t at = begin; at < end; at += TH) {
+        const uint64_t slot = at + threadIdx.x;
+        const int32_t e = slot < end ? chosen[slot - begin] : -1;
+        const uint32_t same = __match_any_sync(~0u, e), before = __popc(same & ((1u << lane) - 1));
+        for (uint32_t w = 0; w < TH / 32 && at + w * 32 < end; ++w) {
+            if (w == warp) {
+                const uint32_t row = e >= 0 ? next[e] + before : 0;
+                __syncwarp();
+                if (e >= 0) {
+                    if (before == 0) next[e] = row + __popc(same);
+                    A.order[row] = int32_t(slot);
+                }
+                if (slot < end) A.positions[slot] = e >= 0 ? int32_t(row) : -1;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+constexpr int kThreads = 256;
+constexpr uint32_t kMaxParts = DCR_ROUTE_PARTS;
+
+template <int PER, typename T>
+__global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs A)
+{
+    __shared__ uint32_t counts[DCR_MAX_EXPERTS];
+    launch_dependents();
+    for (uint32_t e = threadIdx.x; e < A.experts; e += kThreads) counts[e] = 0;
+    __syncthreads();
+    const uint64_t begin = uint64_t(blockIdx.x) * A.per_part, end = min(begin + A.per_part, A.tokens);
+    for (uint64_t t = begin + threadIdx.x / 32; t < end; t += kThreads / 32) route_token<PER, T>(A, t, counts);
+    __syncthreads();
+    for (uint32_t e = threadIdx.x; e < A.experts; e += kThreads) A.counts[uint64_t(blockIdx.x) * A.experts + e] = counts[e];
+}
+
+// A warp an expert: the parts' counts become what lies before each part.
+__global__ void __launch_bounds__(kThreads) scan_kernel(const RouteArgs A)
+{
+    launch_dependents();
+    grid_wait();
+    const uint32_t e = blockIdx.x * (kThreads / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (e >= A.experts) return;
+    uint32_t base = 0;
+    for (uint32_t p = 0; p < A.parts; p += 32) {
+        const uint32_t mine = p + lane < A.parts ? A.counts[uint64_t(p + lane) * A.experts + e] : 0;
+        uint32_t s = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(~0u, s, o);
+            if (lane >= uint32_t(o)) s += u;
+        }
+        if (p + lane < A.parts) A.counts[uint64_t(p + lane) * A.experts + e] = base + s - mine;
+        base += __shfl_sync(~0u, s, 31);
+    }
+    if (lane == 0) A.counts[uint64_t(A.parts) * A.experts + e] = base;
+}
+
+__global__ void __launch_bounds__(kThreads) place_kernel(const RouteArgs A)
+{
+    __shared__ uint32_t next[DCR_MAX_EXPERTS];
+    grid_wait();
+    for (uint32_t e = threadIdx.x; e < A.experts; e += kThreads) next[e] = A.counts[uint64_t(A.parts) * A.experts + e];
+    __syncthreads();
+    const uint32_t total = scan<kThreads>(next, A.experts);
+    const uint64_t slots = A.tokens * A.k;
+    if (blockIdx.x == 0) {
+        for (uint32_t e = threadIdx.x; e < A.experts; e += kThreads) A.offsets[e] = int32_t(next[e]);
+        if (threadIdx.x == 0) A.offsets[A.experts] = int32_t(total);
+        __syncthreads();
+    }
+    for (uint64_t r = total + uint64_t(blockIdx.x) * kThreads + threadIdx.x; r < slots; r += uint64_t(gridDim.x) * kThreads) A.order[r] = -1;
+    for (uint32_t e = threadIdx.x; e < A.experts; e += kThreads) next[e] += A.counts[uint64_t(blockIdx.x) * A.experts + e];
+    __syncthreads();
+    const uint64_t begin = min(uint64_t(blockIdx.x) * A.per_part * A.k, slots), end = min(begin + uint64_t(A.per_part) * A.k, slots);
+    place<kThreads>(A, A.chosen + begin, begin, end, next);
+}
+
+// All of it for a batch of few slots.
+constexpr int kOneThreads = 512;
+constexpr uint32_t kOneSlots = 1024;
+
+template <int PER, typename T>
+__global__ void __launch_bounds__(kOneThreads) route_one_kernel(const RouteArgs A)
+{
+    __shared__ uint32_t next[DCR_MAX_EXPERTS];
+    __shared__ int32_t chosen[kOneSlots];
+    for (uint32_t e = threadIdx.x; e < A.experts; e += kOneThreads) next[e] = 0;
+    __syncthreads();
+    for (uint64_t t = threadIdx.x / 32; t < A.tokens; t += kOneThreads / 32) {
+        const Choice c = route_token<PER, T>(A, t, next);
+        if (threadIdx.x % 32 < A.k) chosen[t * A.k + threadIdx.x % 32] = c.expert;
+    }
+    __syncthreads();
+    const uint32_t total = scan<kOneThreads>(next, A.experts), slots = uint32_t(A.tokens) * A.k;
+    for (uint32_t e = threadIdx.x; e < A.experts; e += kOneThreads) A.offsets[e] = int32_t(next[e]);
+    if (threadIdx.x == 0) A.offsets[A.experts] = int32_t(total);
+    for (uint32_t r = total + threadIdx.x; r < slots; r += kOneThreads) A.order[r] = -1;
+    __syncthreads();
+    place<kOneThreads>(A, chosen, 0, slots, next);
+}
+
+struct RouteGradArgs {
+    const void* logits;
+    const int32_t* chosen;
+    const float* grad_weights;
+    void* grad;
+    uint64_t tokens, row_stride, grad_stride;
+    uint32_t experts, k;
+    bool sigmoid, renormalise;
+    float scale;
+};
+
+// A warp a token.  With d the derivative by the weights, times the scale:
+//   softmax over the chosen: w (d - sum d w);  over all: p (d - sum d p);
+//   sigmoid: d s (1 - s), renormalised w (1 - s) (d - sum d w).
+template <int PER, typename T>
+__global__ void __launch_bounds__(kThreads) route_grad_kernel(const RouteGradArgs A)
+{
+    __shared__ float rows[kThreads / 32][PER * 32];
+    const uint32_t lane = threadIdx.x % 32;
+    float* row = rows[threadIdx.x / 32];
+    for (uint64_t t = uint64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; t < A.tokens; t += uint64_t(gridDim.x) * (kThreads / 32)) {
+        const T* x = static_cast<const T*>(A.logits) + t * A.row_stride;
+        Choice c = {-1, 0.0f};
+        float d = 0.0f;
+        if (lane < A.k) {
+            c.expert = A.chosen[t * A.k + lane];
+            if (uint32_t(c.expert) >= A.experts) c.expert = -1;
+            if (c.expert >= 0) c.logit = to_f32(x[c.expert]), d = A.grad_weights[t * A.k + lane] * A.scale;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) row[i * 32 + lane] = 0.0f;
+        __syncwarp();
+        if (__any_sync(~0u, c.expert >= 0)) {
+            if (A.sigmoid || A.renormalise) {
+                const float w = weight_of(c, A.sigmoid, A.renormalise, 0.0f, 1.0f);
+                float g = d;
+                if (A.renormalise) g = w * (d - warp_sum(d * w));
+                else g = w * d;
+                if (A.sigmoid) g *= sigmoid_of(-c.logit);
+                if (c.expert >= 0) row[c.expert] = g;
+                __syncwarp();
+            } else {
+                float v[PER], m, total;
+                load_row<PER, T>(x, A.experts, v);
+                softmax_of(v, m, total);
+                const float dot = warp_sum(d * weight_of(c, false, false, m, total));
+                if (c.expert >= 0) row[c.expert] = d;
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const float p = v[i] > -INFINITY ? below(v[i], m) / total : 0.0f;
+                    v[i] = p * (row[lane * PER + i] - dot);
+                }
+#pragma unroll
+                for (int i = 0; i < PER; ++i) row[lane * PER + i] = v[i];
+                __syncwarp();
+            }
+        }
+        T* g = static_cast<T*>(A.grad) + t * A.grad_stride;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (i * 32 + lane < A.experts) g[i * 32 + lane] = from_f32<T>(row[i * 32 + lane]);
+        __syncwarp();
+    }
+}
+
+// Calls f with the experts a lane holds, as a compile-time number.
+template <typename F>
+int with_per(uint32_t experts, F f)
+{
+    if (experts <= 32) return f(std::integral_constant<int, 1>());
+    if (experts <= 64) return f(std::integral_constant<int, 2>());
+    if (experts <= 128) return f(std::integral_constant<int, 4>());
+    if (experts <= 256) return f(std::integral_constant<int, 8>());
+    if (experts <= 512) return f(std::integral_constant<int, 16>());
+    return f(std::integral_constant<int, 32>());
+}
+
+int route_launch(RouteArgs A, uint32_t dtype, cudaStream_t s)
+{
+    cudaError_t e = cudaSuccess;
+    if (A.tokens * A.k <= kOneSlots) {
+        const LaunchAttrs at(1, kOneThreads, 0, 1, false, s);
+        with_dtype(dtype, [&](auto t) {
+            return with_per(A.experts, [&](auto per) {
+                e = cudaLaunchKernelEx(&at.cfg, route_one_kernel<decltype(per)::value, decltype(t)>, A);
+                return 0;
+            });
+        });
+        return e == cudaSuccess ? DCR_OK : cuda_error(e, "route launch");
+    }
+    // a warp's tokens come one after another: parts as small as fill two blocks an SM
+    A.per_part = uint32_t(std::max<uint64_t>((A.tokens + kMaxParts - 1) / kMaxParts, kThreads / 32));
+    A.parts = uint32_t((A.tokens + A.per_part - 1) / A.per_part);
+    const LaunchAttrs at(A.parts, kThreads, 0, 1, false, s);
+    with_dtype(dtype, [&](auto t) {
+        return with_per(A.experts, [&](auto per) {
+            e = cudaLaunchKernelEx(&at.cfg, route_kernel<decltype(per)::value, decltype(t)>, A);
+            return 0;
+        });
+    });
+    if (e != cudaSuccess) return cuda_error(e, "route launch");
+    const LaunchAttrs at2((A.experts + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0, 1, true, s), at3(A.parts, kThreads, 0, 1, true, s);
+    e = cudaLaunchKernelEx(&at2.cfg, scan_kernel, A);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&at3.cfg, place_kernel, A);
+    return e == cudaSuccess ? DCR_OK : cuda_error(e, "route launch");
+}
+
+int check_opts(const char* what, uint32_t dtype, uint64_t tokens, uint32_t experts, uint64_t row_stride, const dcr_route_opts* o)
+{
+    if (!o) return set_error(DCR_ERR_INVALID, "%s: NULL argument", what);
+    if (dtype > DCR_F16) return set_error(DCR_ERR_INVALID, "%s: unknown dtype %u", what, dtype);
+    if (experts == 0 || experts > DCR_MAX_EXPERTS) return set_error(DCR_ERR_INVALID, "%s: experts must be 1 to %u", what, DCR_MAX_EXPERTS);
+    if (o->k == 0 || o->k > DCR_MAX_CHOSEN || o->k > experts)
+        return set_error(DCR_ERR_INVALID, "%s: k must be 1 to %u and at most the number of experts", what, DCR_MAX_CHOSEN);
+    if (o->scoring > DCR_SIGMOID) return set_error(DCR_ERR_INVALID, "%s: unknown scoring %u", what, o->scoring);
+    if (!std::isfinite(o->scale)) return set_error(DCR_ERR_INVALID, "%s: scale must be finite", what);
+    if (tokens >= 1ull << 31 || tokens * o->k >= 1ull << 31) return set_error(DCR_ERR_INVALID, "%s: tokens * k must be below 2^31", what);
+    if (row_stride < experts || row_stride >= 1ull << 40) return set_error(DCR_ERR_INVALID, "%s: bad row_stride", what);
+    return DCR_OK;
+}
+
+}  // namespace
+}  // namespace dcr
+
+using namespace dcr;
+
+extern "C" int dcr_route(const void* logits, uint32_t dtype, uint64_t tokens, uint32_t experts, uint64_t row_stride, const float* bias,
+                         const uint8_t* mask, const dcr_route_opts* opts, int32_t* chosen, float* weights, int32_t* offsets, int32_t* order,
+                         int32_t* positions, void* workspace, void* stream)
+{
+    if (int rc = check_opts("dcr_route", dtype, tokens, experts, row_stride, opts)) return rc;
+    const dcr_route_opts& o = *opts;
+    if (o.groups == 0 || o.groups > DCR_MAX_GROUPS || experts % o.groups)
+        return set_error(DCR_ERR_INVALID, "dcr_route: groups must be 1 to %u and divide the experts", DCR_MAX_GROUPS);
+    if (o.group_top == 0 || o.group_top > o.groups) return set_error(DCR_ERR_INVALID, "dcr_route: group_top must be 1 to groups");
+    if (o.group_by != 1 && o.group_by != 2) return set_error(DCR_ERR_INVALID, "dcr_route: group_by must be 1 or 2");
+    if (o.k > experts / o.groups * o.group_top) return set_error(DCR_ERR_INVALID, "dcr_route: the groups taken hold fewer than k experts");
+    if (!offsets || (tokens && (!logits || !chosen || !weights || !order || !positions || !workspace)))
+        return set_error(DCR_ERR_INVALID, "dcr_route: NULL argument");
+    if (uintptr_t(logits) % dtype_size(dtype) || uintptr_t(bias) % 4 || uintptr_t(chosen) % 4 || uintptr_t(weights) % 4 ||
+        uintptr_t(offsets) % 4 || uintptr_t(order) % 4 || uintptr_t(positions) % 4 || uintptr_t(workspace) % 4)
+        return set_error(DCR_ERR_INVALID, "dcr_route: misaligned buffer");
+    RouteArgs A{};
+    A.logits = logits, A.bias = bias, A.mask = mask, A.chosen = chosen, A.weights = weights, A.offsets = offsets, A.order = order;
+    A.positions = positions, A.counts = static_cast<uint32_t*>(workspace), A.tokens = tokens, A.row_stride = row_stride, A.experts = experts;
+    A.k = o.k, A.groups = o.groups, A.group_top = o.group_top, A.group_by = o.group_by, A.group_size = experts / o.groups;
+    A.sigmoid = o.scoring == DCR_SIGMOID, A.renormalise = o.renormalise != 0, A.scale = o.scale;
+    // one group's scores decide in the same order as the logits
+    A.by_logit = !bias && (o.groups == 1 || o.group_by == 1);
+    return route_launch(A, dtype, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int dcr_route_grad(const void* logits, uint32_t dtype, uint64_t tokens, uint32_t experts, uint64_t row_stride,
+                              const int32_t* chosen, const float* grad_weights, const dcr_route_opts* opts, void* grad,
+                              uint64_t grad_stride, void* stream)
+{
+    if (int rc = check_opts("dcr_route_grad", dtype, tokens, experts, row_stride, opts)) return rc;
+    if (tokens && (!logits || !chosen || !grad_weights || !grad)) return set_error(DCR_ERR_INVALID, "dcr_route_grad: NULL argument");
+    if (grad_stride < experts || grad_stride >= 1ull << 40) return set_error(DCR_ERR_INVALID, "dcr_route_grad: bad grad_stride");
+    if (grad == logits && grad && grad_stride != row_stride)
+        return set_error(DCR_ERR_INVALID, "dcr_route_grad: grad in place of logits needs the same stride");
+    if (uintptr_t(logits) % dtype_size(dtype) || uintptr_t(chosen) % 4 || uintptr_t(grad_weights) % 4 || uintptr_t(grad) % dtype_size(dtype))
+        return set_error(DCR_ERR_INVALID, "dcr_route_grad: misaligned buffer");
+    if (tokens == 0) return DCR_OK;
+    const RouteGradArgs A{logits, chosen, grad_weights, grad, tokens, row_stride, grad_stride, experts, opts->k,
+                          opts->scoring == DCR_SIGMOID, opts->renormalise != 0, opts->scale};
+    const LaunchAttrs at(std::min<uint64_t>((tokens + kThreads / 32 - 1) / (kThreads / 32), 1u << 20), kThreads, 0, 1, false, static_cast<cudaStream_t>(stream));
+    cudaError_t e = cudaSuccess;
+    with_dtype(dtype, [&](auto t) {
+        return with_per(experts, [&](auto per) {
+            e = cudaLaunchKernelEx(&at.cfg, route_grad_kernel<decltype(per)::value, decltype(t)>, A);
+            return 0;
+        });
+    });
+    return e == cudaSuccess ? DCR_OK : cuda_error(e, "route gradient launch");
+}

@@ -1,0 +1,612 @@
+// Scores of given tokens: log-probability, entropy and likeliest alternatives
+// of each row of logits, and the gradient of the first two
+// (include/dcr_ops.h).
+//
+// One pass: each thread reads its words of the row in chunks of 8 and keeps a
+// running maximum m, the sum of exp((x - m) / T) and the sum of that times the
+// exponent; maxima and sums meet once, at the end.  The chunk that holds a
+// thread's maximum is summed apart, so that the threads whose maximum is the
+// row's can read that chunk again and leave the maximum itself out: the sum
+// of the others keeps the digits that are lost beside a 1, and with them the
+// log-probability and the entropy of nearly certain rows.
+//
+// Alternatives: the pass also leaves the maximum of each chunk.  From the
+// threads' maxima comes a bound that at least `top` values reach; the few
+// chunks that reach it are read again, and their values of that size sorted.
+// Where those are too many (equal ones above all: masked rows), the values
+// above the bound are taken, and the first of the equal ones in the order of
+// their indexes; where that does not fit either, the largest is searched
+// `top` times.
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+
+#include "logits.cuh"
+
+namespace dcr {
+namespace {
+
+struct ScoreArgs {
+    const void* logits;
+    uint64_t rows, vocab, row_stride;
+    const int64_t* tokens;
+    float* logp;
+    float* entropy;
+    float* top_logp;
+    int64_t* top_tokens;
+    float* stats;
+    uint32_t top;
+    float inv_temp;
+    float sc;             // log2(e) / temperature, rounded to nearest
+    float sc_dn, sc_lo;   // the same rounded down, and the (positive) rest
+};
+
+constexpr int kWords = 8;          // words of a chunk
+constexpr uint32_t kBuckets = 16;  // chunk maxima that a thread keeps
+constexpr uint32_t kList = 1024;   // values that are sorted
+constexpr int kMaxBlocks = 8;      // of a cluster
+constexpr float kLn2 = 0.69314718055994531f;
+
+// The larger one, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Sum of exp((x - m) / T) =: e over words, and of e log2(e).
+struct Sums {
+    float s, t;
+};
+
+template <bool PLAIN, int N>
+__device__ __forceinline__ void add_values(Sums& a, const float (&v)[N], const Exponent& e)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        // -200: exp of it is 0, and so is its product with it, which with -inf would not be a number
+        const float d = max_nan(PLAIN ? fmaf(v[i], e.lo, fmaf(v[i], e.sc, -e.msc)) : fmaf(v[i] - e.m, e.lo, (v[i] - e.m) * e.sc), -200.0f);
+        const float p = exp2_fast(d);
+        a.s += p;
+        a.t = fmaf(p, d, a.t);
+    }
+}
+
+// count: null, or receives how many values are equal to m, which are left out.
+template <typename T, int NV>
+__device__ __forceinline__ Sums chunk_sums(const uint4 (&q)[NV], float m, const ScoreArgs& A, float* count)
+{
+    Sums a = {0.0f, 0.0f};
+    if (fabsf(m) == INFINITY) {
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) nan |= word_nan<T>(q[i]);
+        if (nan) a.s = a.t = NAN;
+        return a;
+    }
+    const Exponent e(m, A.sc_dn, A.sc_lo);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float v[Word<T>::kN];
+        Word<T>::values(q[i], v);
+        if (count) {
+#pragma unroll
+            for (int j = 0; j < Word<T>::kN; ++j) {
+                if (v[j] == m) *count += 1.0f;
+                v[j] = v[j] == m ? -INFINITY : v[j];
+            }
+        }
+        if (e.plain) add_values<true>(a, v, e);
+        else add_values<false>(a, v, e);
+    }
+    // what every exponent has too much
+    const float x = e.term_excess(), f = exp2f(-x);
+    a.t = fmaf(-x, a.s, a.t) * f;
+    a.s *= f;
+    return a;
+}
+
+// A maximum, the values that are equal to it, and the sums over the others.
+struct Part {
+    float m, count, s, t;
+    // b's share from its own maximum to this one's, which is no smaller
+    __device__ __forceinline__ void add(const Part& b, float sc)
+    {
+        if (b.m == m) {
+            count += b.count, s += b.s, t += b.t;
+        } else if (b.m == -INFINITY) {
+            s += b.s, t += b.t;      // nothing, or NaN
+        } else {
+            const float d = (b.m - m) * sc, f = exp2_fast(d), all = b.s + b.count;
+            s = fmaf(f, all, s);
+            if (f != 0.0f) t = fmaf(f, fmaf(d, all, b.t), t);
+        }
+    }
+};
+
+// Order of values, and of (value, index) with the lower index above.
+__device__ __forceinline__ uint32_t order_of(float x)
+{
+    const uint32_t b = __float_as_uint(x + 0.0f);    // -0 is 0
+    return x != x ? 0u : b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o)
+{
+    return o == 0 ? NAN : __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t index) { return uint64_t(order_of(x)) << 32 | uint32_t(~index); }
+
+// This block's words of a row.
+template <typename T>
+struct Share {
+    Row<T> in;
+    uint32_t first, step;   // of this thread
+    uint32_t chunks;        // of the block
+    __device__ __forceinline__ Share(const T* x, uint32_t vocab, uint32_t rank, uint32_t blocks)
+        : in(x, vocab), first(rank * blockDim.x + threadIdx.x), step(blocks * blockDim.x), chunks((in.words + kWords * step - 1) / (kWords * step))
+    {
+    }
+    __device__ __forceinline__ void load(uint32_t c, uint4 (&q)[kWords]) const
+    {
+        const uint32_t k = first + c * kWords * step;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) q[i] = in.load_whole(k + i * step);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            if (in.cut(k + i * step)) q[i] = in.load_cut(k + i * step);
+    }
+    // f(value, index) for the values of word k
+    template <typename F>
+    __device__ __forceinline__ void each(const uint4& q, uint32_t k, F f) const
+    {
+        float v[Word<T>::kN];
+        Word<T>::values(q, v);
+#pragma unroll
+        for (int j = 0; j < Word<T>::kN; ++j) {
+            const uint32_t at = k * Word<T>::kN + j - in.skip;
+            if (k < in.words && at < in.vocab) f(v[j], at);      // before the row: at is huge
+        }
+    }
+    template <typename F>
+    __device__ __forceinline__ void each_of_chunk(uint32_t c, F f) const
+    {
+        uint4 q[kWords];
+        load(c, q);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) each(q[i], first + (c * kWords + i) * step, f);
+    }
+};
+
+template <int TH>
+struct TopMemory {
+    float chunk_max[kBuckets][TH];
+    uint64_t list[kList];
+    uint64_t best[DCR_MAX_TOP];    // this block's, the largest first; 0: none
+    uint64_t part[TH / 32];
+    uint32_t bound[TH / 32];
+    uint32_t count, scan[TH / 32];
+};
+
+// The n largest of list[0..count) to best.
+template <int TH>
+__device__ __forceinline__ void sort_list(TopMemory<TH>& M, uint32_t count, uint32_t n)
+{
+    for (uint32_t i = threadIdx.x; i < count; i += TH) {
+        const uint64_t mine = M.list[i];
+        uint32_t above = 0;
+        for (uint32_t j = 0; j < count; ++j) above += M.list[j] > mine;
+        if (above < n && mine != 0) M.best[above] = mine;
+    }
+}
+
+// The n largest of the block's share to best, sorted.  mine: the thread's maximum.
+template <typename T, int TH>
+__device__ void find_top(TopMemory<TH>& M, const Share<T>& S, float mine, uint32_t n)
+{
+    constexpr uint32_t W = TH / 32;
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    // the bound: in each warp at least ceil(n / W) lanes' maxima reach it
+    uint32_t left = order_of(mine), most = 0;
+    for (uint32_t i = 0; i < (n + W - 1) / W; ++i) {
+        most = __reduce_max_sync(~0u, left);
+        const uint32_t who = __ballot_sync(~0u, left == most);
+        if (lane == __ffs(who) - 1) left = 0;
+    }
+    if (lane == 0) M.bound[warp] = most;
+    if (threadIdx.x == 0) M.count = 0;
+    if (threadIdx.x < n) M.best[threadIdx.x] = 0;
+    __syncthreads();
+    uint32_t bound = M.bound[0];
+    for (uint32_t i = 1; i < W; ++i) bound = min(bound, M.bound[i]);
+    auto collect = [&](uint32_t least) {
+        for (uint32_t b = 0; b < min(S.chunks, kBuckets); ++b)
+            if (order_of(M.chunk_max[b][threadIdx.x]) >= least)
+                for (uint32_t c = b; c < S.chunks; c += kBuckets)
+                    S.each_of_chunk(c, [&](float v, uint32_t at) {
+                        if (order_of(v) >= least) {
+                            const uint32_t p = atomicAdd(&M.count, 1u);   // where a value stands in the list does not matter
+                            if (p < kList) M.list[p] = key_of(v, at);
+                        }
+                    });
+    };
+    if (bound != 0) collect(bound);
+    __syncthreads();
+    uint32_t count = M.count;
+    if (count >= n && count <= kList) {
+        sort_list(M, count, n);
+        __syncthreads();
+        return;
+    }
+    bool done = false;
+    if (count > kList) {
+        // more than the list holds: those above the bound, then the first that are equal to it
+        __syncthreads();
+        if (threadIdx.x == 0) M.count = 0;
+        __syncthreads();
+        collect(bound + 1);
+        __syncthreads();
+        count = M.count;
+        if (count <= kList - DCR_MAX_TOP) {
+            uint32_t need = count < n ? n - count : 0, at = count;
+            for (uint32_t k = S.first; need && k - threadIdx.x < S.in.words; k += S.step) {
+                // all threads go through words of one stride at a time, in the order of the indexes
+                uint4 q = S.in.load(k);
+                uint32_t equal = 0;
+                S.each(q, k, [&](float v, uint32_t) { equal += order_of(v) == bound; });
+                uint32_t before = equal;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t u = __shfl_up_sync(~0u, before, o);
+                    if (lane >= uint32_t(o)) before += u;
+                }
+                __syncthreads();
+                if (lane == 31) M.scan[warp] = before;
+                __syncthreads();
+                before -= equal;
+                uint32_t all = 0;
+                for (uint32_t i = 0; i < W; ++i) {
+                    if (i < warp) before += M.scan[i];
+                    all += M.scan[i];
+                }
+                S.each(q, k, [&](float v, uint32_t i) {
+                    if (order_of(v) == bound && before++ < need) M.list[at + before - 1] = key_of(v, i);
+                });
+                const uint32_t taken = min(all, need);
+                at += taken, need -= taken;
+            }
+            __syncthreads();
+            sort_list(M, at, n);
+            done = true;
+        }
+    }
+    // fewer than n numbers in the share, or more than the list holds in another way: the largest, n times
+    uint64_t last = ~0ull;
+    for (uint32_t i = 0; i < n && !done; ++i) {
+        uint64_t best = 0;
+        for (uint32_t c = 0; c < S.chunks; ++c)
+            S.each_of_chunk(c, [&](float v, uint32_t at) {
+                const uint64_t key = key_of(v, at);
+                if (key < last && key > best) best = key;
+            });
+#pragma unroll
+        for (int o = 16; o; o >>= 1) best = max(best, uint64_t(__shfl_xor_sync(~0u, static_cast<unsigned long long>(best), o)));
+        __syncthreads();
+        if (lane == 0) M.part[warp] = best;
+        __syncthreads();
+        for (uint32_t w = 0; w < W; ++w) best = max(best, M.part[w]);
+        if (threadIdx.x == 0) M.best[i] = best;
+        if (best == 0) break;
+        last = best;
+    }
+    __syncthreads();
+}
+
+// A value of another block's shared memory.
+template <typename V>
+__device__ __forceinline__ V remote(const V* p, uint32_t rank)
+{
+    static_assert(sizeof(V) == 4 || sizeof(V) == 8, "one word");
+    uint32_t at = uint32_t(__cvta_generic_to_shared(p));
+    asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(rank));
+    if constexpr (sizeof(V) == 4) {
+        uint32_t r;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
+        V v;
+        memcpy(&v, &r, 4);
+        return v;
+    } else {
+        uint64_t r;
+        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(r) : "r"(at) : "memory");
+        return V(r);
+    }
+}
+__device__ __forceinline__ void cluster_barrier() { asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory"); }
+
+template <typename T, int TH, bool TOP>
+__global__ void __launch_bounds__(TH, 1024 / TH) scores_kernel(ScoreArgs A, uint32_t cluster)
+{
+    constexpr uint32_t W = TH / 32;
+    __shared__ float4 parts[W];
+    __shared__ float4 whole;
+    __shared__ TopMemory<TOP ? TH : 32> top_memory;
+    const uint32_t rank = cluster > 1 ? blockIdx.x % cluster : 0, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const uint64_t row = blockIdx.x / cluster;
+    const uint32_t vocab = uint32_t(A.vocab);
+    const T* x = static_cast<const T*>(A.logits) + row * A.row_stride;
+    const int64_t token = A.tokens[row];
+    if (token < 0 || token >= int64_t(vocab)) {     // in all blocks of the row's cluster or in none
+        if (rank == 0) {
+            if (threadIdx.x == 0) {
+                if (A.logp) A.logp[row] = 0.0f;
+                if (A.entropy) A.entropy[row] = 0.0f;
+                if (A.stats) A.stats[row * 3] = A.stats[row * 3 + 1] = A.stats[row * 3 + 2] = 0.0f;
+            }
+            for (uint32_t i = threadIdx.x; i < A.top; i += TH) A.top_logp[row * A.top + i] = 0.0f, A.top_tokens[row * A.top + i] = -1;
+        }
+        return;
+    }
+    const float xy = to_f32(x[token]);
+    const Share<T> S(x, vocab, rank, cluster);
+    // top: the sums over the chunk that the maximum m comes from (`at`); rest: those over the others
+    float m = -INFINITY;
+    Sums rest = {0.0f, 0.0f}, top = {0.0f, 0.0f};
+    uint32_t at = 0;
+    for (uint32_t c = 0; c < S.chunks; ++c) {
+        uint4 q[kWords];
+        S.load(c, q);
+        float cm = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) cm = fmaxf(cm, word_max(q[i], T()));
+        if constexpr (TOP) {
+            float& b = top_memory.chunk_max[c % kBuckets][threadIdx.x];
+            b = c < kBuckets ? cm : fmaxf(b, cm);
+        }
+        const bool higher = cm > m;
+        if (higher) {
+            rest.s += top.s, rest.t += top.t;
+            if (m != -INFINITY) {       // otherwise nothing, or NaN
+                const float d = (m - cm) * A.sc, f = exp2_fast(d);
+                rest.t = f != 0.0f ? f * fmaf(d, rest.s, rest.t) : 0.0f * rest.s;
+                rest.s *= f;
+            }
+            top = {0.0f, 0.0f}, m = cm, at = c;
+        }
+        const Sums a = chunk_sums<T, kWords>(q, m, A, nullptr);
+        if (higher) top = a;
+        else rest.s += a.s, rest.t += a.t;
+    }
+    // the row's maximum in this block, and which threads have it
+    float bm = m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, o));
+    if (lane == 0) parts[warp].x = bm;
+    __syncthreads();
+#pragma unroll
+    for (uint32_t i = 0; i < W; ++i) bm = fmaxf(bm, parts[i].x);
+    Part p = {m, 0.0f, rest.s + top.s, rest.t + top.t}, all = {bm, 0.0f, 0.0f, 0.0f};
+    if (m == bm && m != -INFINITY) {
+        // the chunk of the maximum again, without what is equal to it
+        uint4 q[kWords];
+        S.load(at, q);
+        top = chunk_sums<T, kWords>(q, m, A, &p.count);
+        p.s = rest.s + top.s, p.t = rest.t + top.t;
+    }
+    all.add(p, A.sc);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        all.count += __shfl_xor_sync(~0u, all.count, o);
+        all.s += __shfl_xor_sync(~0u, all.s, o);
+        all.t += __shfl_xor_sync(~0u, all.t, o);
+    }
+    __syncthreads();
+    if (lane == 0) parts[warp] = make_float4(bm, all.count, all.s, all.t);
+    if constexpr (TOP) find_top<T, TH>(top_memory, S, m, A.top);
+    else __syncthreads();
+    all = {bm, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (uint32_t i = 0; i < W; ++i) all.count += parts[i].y, all.s += parts[i].z, all.t += parts[i].w;
+    if (cluster > 1) {
+        if (threadIdx.x == 0) whole = make_float4(all.m, all.count, all.s, all.t);
+        cluster_barrier();      // every block of the cluster runs, and has written what the first one reads
+        if (rank == 0) {
+            Part b[kMaxBlocks];
+            for (uint32_t i = 0; i < cluster; ++i) {
+                b[i] = {remote(&whole.x, i), remote(&whole.y, i), remote(&whole.z, i), remote(&whole.w, i)};
+                bm = fmaxf(bm, b[i].m);
+            }
+            all = {bm, 0.0f, 0.0f, 0.0f};
+            for (uint32_t i = 0; i < cluster; ++i) all.add(b[i], A.sc);
+            if constexpr (TOP) {
+                const uint32_t n = cluster * A.top;
+                for (uint32_t i = threadIdx.x; i < n; i += TH) top_memory.list[i] = remote(&top_memory.best[i % A.top], i / A.top);
+                __syncthreads();     // also: this block's own part of best is read
+                sort_list(top_memory, n, A.top);
+                __syncthreads();
+            }
+        }
+        cluster_barrier();      // what the first block reads stays until it has
+    }
+    if (rank != 0) return;
+    const float r = bm == INFINITY && all.s == all.s ? 0.0f : all.s + (all.count - 1.0f);
+    const float lr = log1pf(r);
+    const float d = fabsf(bm) == INFINITY ? NAN : -kLn2 * all.t / (1.0f + r);
+    if (threadIdx.x == 0) {
+        if (A.logp) A.logp[row] = (xy - bm) * A.inv_temp - lr;
+        if (A.entropy) A.entropy[row] = lr + d;
+        if (A.stats) A.stats[row * 3] = bm, A.stats[row * 3 + 1] = r, A.stats[row * 3 + 2] = d;
+    }
+    if constexpr (TOP) {
+        for (uint32_t i = threadIdx.x; i < A.top; i += TH) {
+            const uint64_t key = top_memory.best[i];
+            A.top_logp[row * A.top + i] = (value_of(uint32_t(key >> 32)) - bm) * A.inv_temp - lr;
+            A.top_tokens[row * A.top + i] = int64_t(uint32_t(~uint32_t(key)));
+        }
+    }
+}
+
+struct GradArgs {
+    const void* logits;
+    void* grad;
+    uint64_t rows, vocab, row_stride, grad_stride;
+    const int64_t* tokens;
+    const float* stats;
+    const float* grad_logp;
+    const float* grad_entropy;
+    float inv_temp, sc;
+};
+
+// `parts` blocks a row, each of which takes every parts-th piece of TH * NV
+// words of it.
+template <typename T, int TH, int NV>
+__global__ void __launch_bounds__(TH) grad_kernel(GradArgs A, uint32_t parts)
+{
+    constexpr int N = Word<T>::kN;
+    const uint64_t row = blockIdx.x / parts;
+    const uint32_t vocab = uint32_t(A.vocab);
+    const T* x = static_cast<const T*>(A.logits) + row * A.row_stride;
+    T* g = static_cast<T*>(A.grad) + row * A.grad_stride;
+    const int64_t token = A.tokens[row];
+    const float ga = A.grad_logp ? A.grad_logp[row] : 0.0f, gb = A.grad_entropy ? A.grad_entropy[row] : 0.0f;
+    const Row<T> in(x, vocab), out(g, vocab);
+    if (token < 0 || token >= int64_t(vocab) || (ga == 0.0f && gb == 0.0f)) {
+        for (uint32_t k = blockIdx.x % parts * TH + threadIdx.x; k < out.words; k += parts * TH) {
+            if (out.whole(k)) *reinterpret_cast<uint4*>(out.base + uint64_t(k) * N) = make_uint4(0, 0, 0, 0);
+            else store_values<T>(g, out.skip, vocab, k, make_uint4(0, 0, 0, 0));
+        }
+        return;
+    }
+    const float m = A.stats[row * 3], r = A.stats[row * 3 + 1], mean = A.stats[row * 3 + 2];
+    // grad_j = e (a + b d) with d = log2 e, e = exp((x_j - m) / T), both with what their exponent has too much
+    const Exponent e(m, A.sc, 0.0f);
+    const float f = A.inv_temp / (1.0f + r), over = e.excess(), back = exp2f(-over);
+    const float b = -gb * kLn2 * f * back, a = -(ga + (gb == 0.0f ? 0.0f : gb * mean)) * f * back - b * over;
+    const bool same = out.skip == in.skip;
+    const uint32_t yword = (in.skip + uint32_t(token)) / N, yat = (in.skip + uint32_t(token)) % N;
+    for (uint32_t first = (blockIdx.x % parts) * (TH * NV) + threadIdx.x; first < in.words; first += parts * (TH * NV)) {
+        uint4 q[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) q[i] = in.load_whole(first + i * TH);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (in.cut(first + i * TH)) q[i] = in.load_cut(first + i * TH);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const uint32_t k = first + i * TH;
+            float v[N], w[N];
+            Word<T>::values(q[i], v);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float d = max_nan(e.plain ? fmaf(v[j], e.sc, -e.msc) : (v[j] - m) * e.sc, -200.0f);
+                w[j] = exp2_fast(d) * fmaf(b, d, a);
+            }
+            if (k == yword) {
+                // the token's own value: 1 - p from the sum of the others where it is the largest
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (j == int(yat)) w[j] = fmaf(ga * A.inv_temp, v[j] == m ? r / (1.0f + r) : 1.0f, v[j] == m ? -gb * mean * f : w[j]);
+            }
+            const uint4 z = Word<T>::pack(w);
+            if (same && in.whole(k)) *reinterpret_cast<uint4*>(out.base + uint64_t(k) * N) = z;
+            else if (k < in.words) store_values<T>(g, in.skip, vocab, k, z);
+        }
+    }
+}
+
+// 1 / T and log2(e) / T, which stay finite for the smallest T, too (0 times
+// them is 0).
+void scales_of(float temperature, float& inv, float& sc, float* dn, float* lo)
+{
+    const double most = FLT_MAX, s = std::fmin(1.4426950408889634 / temperature, most);
+    inv = float(std::fmin(1.0 / temperature, most));
+    sc = float(s);
+    if (dn) {
+        *dn = sc > s ? std::nextafterf(sc, 0.0f) : sc;
+        *lo = std::fmax(float(s - *dn), FLT_TRUE_MIN);
+    }
+}
+
+template <typename T, int TH>
+int scores_launch(const ScoreArgs& A, uint32_t cluster, cudaStream_t s)
+{
+    const LaunchAttrs at(A.rows * cluster, TH, 0, cluster, false, s);
+    const cudaError_t e = A.top ? cudaLaunchKernelEx(&at.cfg, scores_kernel<T, TH, true>, A, cluster)
+                                : cudaLaunchKernelEx(&at.cfg, scores_kernel<T, TH, false>, A, cluster);
+    return e == cudaSuccess ? DCR_OK : cuda_error(e, "token scores launch");
+}
+
+// Few long rows are shared by the blocks of a cluster, as long as each has a
+// chunk of its own.
+template <typename T>
+int scores_launch(const ScoreArgs& A, cudaStream_t s)
+{
+    const uint64_t words = (A.vocab * sizeof(T) + 15) / 16 + 1;
+    if (words <= 1024) return scores_launch<T, 128>(A, 1, s);
+    uint32_t cluster = 1;
+    while (cluster < kMaxBlocks && A.rows * cluster < 2 * 152 && words / cluster > 256 * kWords) cluster *= 2;
+    return scores_launch<T, 256>(A, cluster, s);
+}
+
+template <typename T, int TH, int NV>
+int grad_launch(const GradArgs& A, uint64_t words, cudaStream_t s)
+{
+    const uint64_t parts = std::max<uint64_t>(1, std::min<uint64_t>((words + TH * NV - 1) / (TH * NV), ((1ull << 31) - 1) / A.rows));
+    const LaunchAttrs at(A.rows * parts, TH, 0, 1, false, s);
+    const cudaError_t e = cudaLaunchKernelEx(&at.cfg, grad_kernel<T, TH, NV>, A, uint32_t(parts));
+    return e == cudaSuccess ? DCR_OK : cuda_error(e, "token scores gradient launch");
+}
+
+int check(const char* what, const void* logits, uint32_t dtype, uint64_t rows, uint64_t vocab, uint64_t row_stride, const int64_t* tokens,
+          float temperature)
+{
+    if (dtype > DCR_F16) return set_error(DCR_ERR_INVALID, "%s: unknown dtype %u", what, dtype);
+    if (!(temperature > 0.0f) || temperature > 3.0e38f) return set_error(DCR_ERR_INVALID, "%s: temperature must be positive and finite", what);
+    if (vocab == 0 || vocab >= 1ull << 31 || rows >= 1ull << 28 || row_stride >= 1ull << 40)
+        return set_error(DCR_ERR_INVALID, "%s: vocab must be at least 1 and below 2^31, rows below 2^28", what);
+    if (row_stride < vocab) return set_error(DCR_ERR_INVALID, "%s: row_stride below vocab", what);
+    if (rows && (!logits || !tokens)) return set_error(DCR_ERR_INVALID, "%s: NULL argument", what);
+    if (uintptr_t(logits) % dtype_size(dtype) || uintptr_t(tokens) % 8) return set_error(DCR_ERR_INVALID, "%s: misaligned buffer", what);
+    return DCR_OK;
+}
+
+}  // namespace
+}  // namespace dcr
+
+using namespace dcr;
+
+extern "C" int dcr_token_scores(const void* logits, uint32_t dtype, uint64_t rows, uint64_t vocab, uint64_t row_stride, const int64_t* tokens,
+                                float temperature, uint32_t top, float* logp, float* entropy, float* top_logp, int64_t* top_tokens,
+                                float* stats, void* stream)
+{
+    if (int rc = dcr::check("dcr_token_scores", logits, dtype, rows, vocab, row_stride, tokens, temperature)) return rc;
+    if (top > DCR_MAX_TOP || top > vocab) return set_error(DCR_ERR_INVALID, "dcr_token_scores: top must be at most %u and vocab", DCR_MAX_TOP);
+    if (rows && top && (!top_logp || !top_tokens)) return set_error(DCR_ERR_INVALID, "dcr_token_scores: NULL argument");
+    if (uintptr_t(logp) % 4 || uintptr_t(entropy) % 4 || uintptr_t(top_logp) % 4 || uintptr_t(top_tokens) % 8 || uintptr_t(stats) % 4)
+        return set_error(DCR_ERR_INVALID, "dcr_token_scores: misaligned buffer");
+    if (rows == 0 || (!logp && !entropy && !stats && !top)) return DCR_OK;
+    ScoreArgs A{logits, rows, vocab, row_stride, tokens, logp, entropy, top_logp, top_tokens, stats, top};
+    scales_of(temperature, A.inv_temp, A.sc, &A.sc_dn, &A.sc_lo);
+    return with_dtype(dtype, [&](auto t) { return scores_launch<decltype(t)>(A, static_cast<cudaStream_t>(stream)); });
+}
+
+extern "C" int dcr_token_scores_grad(const void* logits, uint32_t dtype, uint64_t rows, uint64_t vocab, uint64_t row_stride,
+                                     const int64_t* tokens, const float* stats, const float* grad_logp, const float* grad_entropy,
+                                     float temperature, void* grad, uint64_t grad_stride, void* stream)
+{
+    if (int rc = dcr::check("dcr_token_scores_grad", logits, dtype, rows, vocab, row_stride, tokens, temperature)) return rc;
+    if (rows && (!stats || !grad)) return set_error(DCR_ERR_INVALID, "dcr_token_scores_grad: NULL argument");
+    if (grad_stride < vocab || grad_stride >= 1ull << 40) return set_error(DCR_ERR_INVALID, "dcr_token_scores_grad: bad grad_stride");
+    if (grad == logits && grad && grad_stride != row_stride)
+        return set_error(DCR_ERR_INVALID, "dcr_token_scores_grad: grad in place of logits needs the same stride");
+    if (uintptr_t(grad) % dtype_size(dtype) || uintptr_t(stats) % 4 || uintptr_t(grad_logp) % 4 || uintptr_t(grad_entropy) % 4)
+        return set_error(DCR_ERR_INVALID, "dcr_token_scores_grad: misaligned buffer");
+    if (rows == 0) return DCR_OK;
+    GradArgs A{logits, grad, rows, vocab, row_stride, grad_stride, tokens, stats, grad_logp, grad_entropy};
+    scales_of(temperature, A.inv_temp, A.sc, nullptr, nullptr);
+    const uint64_t words = (vocab * dtype_size(dtype) + 15) / 16 + 1;
+    return with_dtype(dtype, [&](auto t) {
+        using T = decltype(t);
+        const cudaStream_t s = static_cast<cudaStream_t>(stream);
+        return words <= 128 ? grad_launch<T, 128, 1>(A, words, s) : words <= 512 ? grad_launch<T, 128, 4>(A, words, s) : grad_launch<T, 256, 4>(A, words, s);
+    });
+}

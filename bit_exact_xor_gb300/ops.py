@@ -25,10 +25,12 @@ SCALE_GIVEN, SCALE_TENSOR, SCALE_ROW = 0, 1, 2
 MAX_EXPERTS = 1024
 QUANT_PARTIALS = 1216
 TEST_STALL = 0x80000000   # test only: a product whose waits run out
+SOFTMAX, SIGMOID = 0, 1   # scores of a router
 DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 OP_EXPORTS = ["dcr_nvfp4_quantize", "dcr_nvfp4_matmul", "dcr_nvfp4_linear", "dcr_policy_loss", "dcr_token_logprobs",
-              "dcr_ops_status"]
+              "dcr_token_scores", "dcr_token_scores_grad", "dcr_route", "dcr_route_grad", "dcr_experts_gather",
+              "dcr_experts_combine", "dcr_experts_combine_grad", "dcr_grad_norm", "dcr_adamw", "dcr_ops_status"]
 
 
 class Nvfp4(NamedTuple):
