@@ -7,7 +7,7 @@ from typing import NamedTuple
 import torch
 
 from . import OK, check
-from .ops import DTYPES, NONE, _elsewhere, _flat, _lib, _raw_stream, _refuse
+from .ops import DTYPES, NONE, _elsewhere, _fast, _flat, _lib, _raw_stream, _refuse, _result_of
 
 ADAMW_BLOCK = 256
 NORM_WORKSPACE = 9728
@@ -77,6 +77,10 @@ def _list(tensors, what, like=None):
 def grad_norm(grads, stream=None):
     """dcr_grad_norm: a float32 scalar on the device, the 2-norm of all the
     tensors' values together (all float32, all bfloat16 or all float16)."""
+    if stream is None:
+        r = _fast.norm(grads)
+        if r is not None:
+            return _result_of(r)
     grads = _list(grads, "grads")
     if not grads:
         _refuse("grads must have at least one tensor")
@@ -133,6 +137,12 @@ def adamw_step(weights, grads, states, step, lr, betas=(0.9, 0.999), eps=1e-8, w
     from grad_norm) and max_norm gradients are scaled down to that norm, and a
     norm that is not finite leaves the whole step out.  seed: for the rounding
     of 8-bit moments."""
+    kind = type(states[0]) if states.__class__ is list and states else None
+    if stream is None and (kind is AdamState32 or kind is AdamState8):
+        r = _fast.adamw(weights, grads, states, 32 if kind is AdamState32 else 8, copies, norm, step, lr, betas[0], betas[1], eps, weight_decay,
+                        max_norm or 0.0, grad_scale, seed & 0xFFFFFFFF)
+        if r is not None:
+            return None if r == OK else check(r)
     weights = _list(weights, "weights")
     if not weights:
         _refuse("weights must have at least one tensor")

@@ -134,70 +134,97 @@ __device__ __forceinline__ void write8(const Raw8<BYTES>& r, void* base, uint64_
     }
 }
 
-__device__ __forceinline__ void values(const Raw8<4>& r, float (&v)[8], bool)
+__device__ __forceinline__ void values(const Raw8<4>& r, float2 (&v)[4], bool)
 {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r.w[j]);
+    for (int j = 0; j < 4; ++j) v[j] = make_float2(__uint_as_float(r.w[2 * j]), __uint_as_float(r.w[2 * j + 1]));
 }
-__device__ __forceinline__ void values(const Raw8<2>& r, float (&v)[8], bool half)
+__device__ __forceinline__ void values(const Raw8<2>& r, float2 (&v)[4], bool half)
 {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.w[j]));
-        v[2 * j] = half ? f.x : __uint_as_float(r.w[j] << 16);
-        v[2 * j + 1] = half ? f.y : __uint_as_float(r.w[j] & 0xFFFF0000u);
-    }
+    for (int j = 0; j < 4; ++j)
+        v[j] = half ? __half22float2(*reinterpret_cast<const __half2*>(&r.w[j]))
+                    : make_float2(__uint_as_float(r.w[j] << 16), __uint_as_float(r.w[j] & 0xFFFF0000u));
 }
 // e4m3 codes
-__device__ __forceinline__ void values(const Raw8<1>& r, float (&v)[8])
+__device__ __forceinline__ void values(const Raw8<1>& r, float2 (&v)[4])
 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(r.w[j / 2] >> (16 * (j % 2))), __NV_E4M3);
-        const float2 f = __half22float2(__half2(h));
-        v[2 * j] = f.x, v[2 * j + 1] = f.y;
+        v[j] = __half22float2(__half2(h));
     }
 }
-__device__ __forceinline__ Raw8<4> packed(const float (&v)[8], Raw8<4>, bool)
+__device__ __forceinline__ Raw8<4> packed(const float2 (&v)[4], Raw8<4>, bool)
 {
     Raw8<4> r;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r.w[j] = __float_as_uint(v[j]);
+    for (int j = 0; j < 4; ++j) r.w[2 * j] = __float_as_uint(v[j].x), r.w[2 * j + 1] = __float_as_uint(v[j].y);
     return r;
 }
-__device__ __forceinline__ Raw8<2> packed(const float (&v)[8], Raw8<2>, bool half)
+__device__ __forceinline__ Raw8<2> packed(const float2 (&v)[4], Raw8<2>, bool half)
 {
     Raw8<2> r;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-        r.w[j] = half ? *reinterpret_cast<const uint32_t*>(&h) : *reinterpret_cast<const uint32_t*>(&b);
+        if (half) {
+            const __half2 h = __float22half2_rn(v[j]);
+            r.w[j] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            const __nv_bfloat162 b = __float22bfloat162_rn(v[j]);
+            r.w[j] = *reinterpret_cast<const uint32_t*>(&b);
+        }
     }
+    return r;
+}
+
+// Two products in one instruction, each rounded to nearest.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    uint64_t r;
+    asm("{ .reg .b64 x, y; mov.b64 x, {%1, %2}; mov.b64 y, {%3, %4}; mul.rn.f32x2 %0, x, y; }" : "=l"(r) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(r));
+    return f;
+}
+// Not in one instruction: that would be merged with the product into a
+// multiply-add, which rounds once.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// The largest magnitude of three, NaN if one is.
+__device__ __forceinline__ float largest(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
     return r;
 }
 
 // The scale of a block of 256 values from the lanes' own, and 1 / it.
 struct Scale {
     float s, inv;
-    __device__ __forceinline__ explicit Scale(const float (&x)[8])
+    __device__ __forceinline__ explicit Scale(const float2 (&x)[4])
     {
-        uint32_t a = 0;   // magnitudes order as their bits do, NaN above all
+        float a = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-        s = __fmul_rn(__uint_as_float(__reduce_max_sync(~0u, a)), 1.0f / 448.0f);
+        for (int j = 0; j < 4; ++j) a = largest(a, x[j].x, x[j].y);
+        // magnitudes order as their bits do, NaN above all
+        s = __fmul_rn(__uint_as_float(__reduce_max_sync(~0u, __float_as_uint(a) & 0x7FFFFFFFu)), 1.0f / 448.0f);
         if (!(s <= FLT_MAX)) s = NAN;
         inv = s > 0.0f ? fminf(__frcp_rn(s), FLT_MAX) : 0.0f;
     }
 };
 
-// |x| inv as an e4m3 code: a value of e4m3 is one of 32 bits whose exponent is
-// 120 larger, cut to 3 bits of mantissa; 16 random bits, a half below their
-// last one, are added to what is cut off.
-__device__ __forceinline__ uint32_t encode(float x, float inv, uint32_t random)
+// |x| inv as e4m3 codes, in bits 20 to 26: a value of e4m3 is one of 32 bits
+// whose exponent is 120 larger, cut to 3 bits of mantissa; 16 random bits, a
+// half below their last one, are added to what is cut off.  The largest value
+// is 448 within three units of its last place, which leaves the code at 448's
+// whatever is added (at most 2^20 - 8).  (A block that is not finite has a NaN
+// for its scale, and any codes.)
+__device__ __forceinline__ uint2 encode2(float2 x, float inv, uint32_t random0, uint32_t random1)
 {
-    const float y = fminf(__fmul_rn(fabsf(x), inv), 448.0f);
-    return (__float_as_uint(__fmul_rn(y, 0x1p-120f)) + (random * 16 + 8)) >> 20;
+    const float2 y = mul2(mul2(make_float2(fabsf(x.x), fabsf(x.y)), both(inv)), both(0x1p-120f));
+    return make_uint2(__float_as_uint(y.x) + random0, __float_as_uint(y.y) + random1);
 }
 
 // What a whole launch shares.
@@ -229,44 +256,58 @@ struct Common {
     }
 };
 
+// What a lane reads of 256 values.
+template <int WB, int GB, int BITS>
+struct Loaded {
+    Raw8<WB> w;
+    Raw8<GB> g;
+    Raw8<BITS / 8> m, v;
+    float ms, vs;
+    template <bool VEC>
+    __device__ __forceinline__ void read(const Entry& E, uint64_t at)
+    {
+        read8<VEC>(w, E.t.w, at, E.t.n);
+        read8<VEC>(g, E.t.grad, at, E.t.n);
+        read8<VEC>(m, E.t.m, at, E.t.n);
+        read8<VEC>(v, E.t.v, at, E.t.n);
+        if (BITS == 8) ms = E.t.m_scale[at / kBlock], vs = E.t.v_scale[at / kBlock];
+    }
+};
+
 template <int WB, int GB, int BITS, bool VEC>
-__device__ __forceinline__ void update(const Entry& E, const AdamwArgs& A, const Common& C, uint64_t at)
+__device__ __forceinline__ void update(const Entry& E, const AdamwArgs& A, const Common& C, uint64_t at, const Loaded<WB, GB, BITS>& L)
 {
     const uint64_t n = E.t.n;
     const uint32_t lane = threadIdx.x % 32;
-    Raw8<WB> rw;
-    Raw8<GB> rg;
-    Raw8<BITS / 8> rm, rv;
-    float ms = 0.0f, vs = 0.0f;
-    read8<VEC>(rw, E.t.w, at, n);
-    read8<VEC>(rg, E.t.grad, at, n);
-    read8<VEC>(rm, E.t.m, at, n);
-    read8<VEC>(rv, E.t.v, at, n);
-    if (BITS == 8) ms = E.t.m_scale[at / kBlock], vs = E.t.v_scale[at / kBlock];
-    float w[8], g[8], m[8], v[8], root[8];
+    const Raw8<WB>& rw = L.w;
+    const Raw8<GB>& rg = L.g;
+    const Raw8<BITS / 8>&rm = L.m, &rv = L.v;
+    const float ms = L.ms, vs = L.vs;
+    float2 w[4], g[4], m[4], v[4], root[4];
     values(rw, w, A.w_half);
     values(rg, g, A.g_half);
     if constexpr (BITS == 8) {
         values(rm, m);
         values(rv, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            m[j] = __fmul_rn(m[j], ms);
-            v[j] = __fmul_rn(v[j], vs);
-            v[j] = __fmul_rn(v[j], v[j]);
+        for (int j = 0; j < 4; ++j) {
+            m[j] = mul2(m[j], both(ms));
+            v[j] = mul2(v[j], both(vs));
+            v[j] = mul2(v[j], v[j]);
         }
     } else {
         values(rm, m, false);
         values(rv, v, false);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        g[j] = __fmul_rn(g[j], C.coef);
-        m[j] = __fadd_rn(__fmul_rn(m[j], A.beta1), __fmul_rn(g[j], A.rest1));
-        v[j] = __fadd_rn(__fmul_rn(v[j], A.beta2), __fmul_rn(__fmul_rn(g[j], g[j]), A.rest2));
-        root[j] = __fsqrt_rn(v[j]);
-        const float d = __fdiv_rn(m[j], __fadd_rn(__fmul_rn(root[j], C.inv_root), A.eps));
-        w[j] = __fsub_rn(__fmul_rn(w[j], C.decay), __fmul_rn(d, C.step_size));
+    for (int j = 0; j < 4; ++j) {
+        g[j] = mul2(g[j], both(C.coef));
+        m[j] = add2(mul2(m[j], both(A.beta1)), mul2(g[j], both(A.rest1)));
+        v[j] = add2(mul2(v[j], both(A.beta2)), mul2(mul2(g[j], g[j]), both(A.rest2)));
+        root[j] = make_float2(__fsqrt_rn(v[j].x), __fsqrt_rn(v[j].y));
+        const float2 below = add2(mul2(root[j], both(C.inv_root)), both(A.eps));
+        const float2 d = make_float2(__fdiv_rn(m[j].x, below.x), __fdiv_rn(m[j].y, below.y));
+        w[j] = add2(mul2(w[j], both(C.decay)), mul2(d, both(-C.step_size)));
     }
     write8<VEC>(packed(w, rw, A.w_half), E.t.w, at, n);
     if (A.copy_dtype == DCR_F32) write8<VEC>(packed(w, Raw8<4>(), false), E.t.copy, at, n);
@@ -277,21 +318,44 @@ __device__ __forceinline__ void update(const Entry& E, const AdamwArgs& A, const
     } else {
         if (!VEC) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (at + lane + 32 * j >= n) m[j] = root[j] = 0.0f;
+            for (int j = 0; j < 4; ++j) {
+                if (at + lane + 64 * j >= n) m[j].x = root[j].x = 0.0f;
+                if (at + lane + 64 * j + 32 >= n) m[j].y = root[j].y = 0.0f;
+            }
         }
         const Scale sm(m), sv(root);
+        // a random number for each value's number in the call, whose upper half is nearly always the same for all 256
         const uint64_t first = E.first + at;
-        Raw8<1> cm = {}, cv = {};
+        const uint32_t low = uint32_t(first), key = mix(C.key + uint32_t(first >> 32));
+        uint32_t h[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint64_t i = first + (VEC ? lane * 8 + j : lane + 32 * j);
-            const uint32_t h = mix(uint32_t(i) ^ mix(C.key + uint32_t(i >> 32)));
-            const uint32_t a = encode(m[j], sm.inv, h & 0xFFFFu) | (__float_as_uint(m[j]) >> 24 & 0x80u);
-            uint32_t b = encode(root[j], sv.inv, h >> 16);
-            if (b == 0 && root[j] != 0.0f) b = 1;
-            cm.w[j / 4] |= a << (8 * (j % 4));
-            cv.w[j / 4] |= b << (8 * (j % 4));
+        for (int j = 0; j < 8; ++j) h[j] = mix((low + (VEC ? lane * 8 + j : lane + 32 * j)) ^ key);
+        if (low > 0xFFFFFFFFu - kBlock) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint64_t i = first + (VEC ? lane * 8 + j : lane + 32 * j);
+                h[j] = mix(uint32_t(i) ^ mix(C.key + uint32_t(i >> 32)));
+            }
+        }
+        Raw8<1> cm, cv;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t a[4], b[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float2 x = m[2 * i + j], y = root[2 * i + j];
+                const uint32_t h0 = h[4 * i + 2 * j], h1 = h[4 * i + 2 * j + 1];
+                const uint2 p = encode2(x, sm.inv, (h0 << 4 & 0xFFFF0u) | 8, (h1 << 4 & 0xFFFF0u) | 8);
+                uint2 q = encode2(y, sv.inv, (h0 >> 12 & 0xFFFF0u) | 8, (h1 >> 12 & 0xFFFF0u) | 8);
+                if (y.x != 0.0f) q.x = max(q.x, 1u << 20);
+                if (y.y != 0.0f) q.y = max(q.y, 1u << 20);
+                // the codes to the last byte, where the first moment's sign is
+                a[2 * j] = (p.x << 4 & 0x7FFFFFFFu) | (__float_as_uint(x.x) & 0x80000000u);
+                a[2 * j + 1] = (p.y << 4 & 0x7FFFFFFFu) | (__float_as_uint(x.y) & 0x80000000u);
+                b[2 * j] = q.x << 4, b[2 * j + 1] = q.y << 4;
+            }
+            cm.w[i] = __byte_perm(__byte_perm(a[0], a[1], 0x0073), __byte_perm(a[2], a[3], 0x0073), 0x5410);
+            cv.w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0073), __byte_perm(b[2], b[3], 0x0073), 0x5410);
         }
         write8<VEC>(cm, E.t.m, at, n);
         write8<VEC>(cv, E.t.v, at, n);
@@ -313,7 +377,7 @@ __device__ __forceinline__ uint32_t tensor_of(const TABLE& T, uint32_t c)
 }
 
 template <int WB, int GB, int BITS, int N>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<N> T, const AdamwArgs A)
+__global__ void __launch_bounds__(kThreads, BITS == 8 ? 3 : 2) adamw_kernel(const __grid_constant__ Table<N> T, const AdamwArgs A)
 {
     const Common C(A);
     if (C.skip) return;
@@ -323,9 +387,22 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     // 8 consecutive values of each kind as one access
     const uintptr_t odd = (uintptr_t(E.t.w) & (8 * WB - 1)) | (uintptr_t(E.t.grad) & (8 * GB - 1)) | ((uintptr_t(E.t.m) | uintptr_t(E.t.v)) & (BITS - 1)) |
                           (uintptr_t(E.t.copy) & (A.copy_dtype == DCR_F32 ? 31 : 15));
-    for (uint64_t at = begin + threadIdx.x / 32 * kBlock; at < end; at += kRound) {
-        if (odd == 0 && at + kBlock <= E.t.n) update<WB, GB, BITS, true>(E, A, C, at);
-        else update<WB, GB, BITS, false>(E, A, C, at);
+    uint64_t at = begin + threadIdx.x / 32 * kBlock;
+    const uint64_t whole = odd == 0 ? min(end, E.t.n / kBlock * kBlock) : begin;
+    if (at < whole) {
+        // the next values are on their way while these are computed
+        Loaded<WB, GB, BITS> now, next;
+        next.template read<true>(E, at);
+        for (; at < whole; at += kRound) {
+            now = next;
+            if (at + kRound < whole) next.template read<true>(E, at + kRound);
+            update<WB, GB, BITS, true>(E, A, C, at, now);
+        }
+    }
+    for (; at < end; at += kRound) {
+        Loaded<WB, GB, BITS> now;
+        now.template read<false>(E, at);
+        update<WB, GB, BITS, false>(E, A, C, at, now);
     }
 }
 

@@ -9,6 +9,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <vector>
+
 #include "../../include/dcr_ops.h"
 
 namespace {
@@ -164,11 +166,300 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// A number from a Python float or int; false with no error set where it is neither.
+bool number(PyObject* o, double* v)
+{
+    if (!PyFloat_Check(o) && !PyLong_Check(o)) return false;
+    *v = PyFloat_AsDouble(o);
+    if (!PyErr_Occurred()) return true;
+    PyErr_Clear();
+    return false;
+}
+bool whole(PyObject* o, uint64_t most, uint64_t* v)
+{
+    if (!PyLong_Check(o)) return false;
+    *v = PyLong_AsUnsignedLongLong(o);
+    if (!PyErr_Occurred()) return *v <= most;
+    PyErr_Clear();
+    return false;
+}
+// A contiguous tensor of such a shape, or None where that is allowed.
+bool slots(PyObject* o, const Tensor& like, at::ScalarType type, int64_t tokens, int64_t k, void** p)
+{
+    return flat(o, like, type, tokens * k, p) && THPVariable_Unpack(o).dim() == 2 && THPVariable_Unpack(o).size(1) == k;
+}
+PyObject* none() { return Py_INCREF(Py_None), Py_None; }
+
+// scores(logits, tokens, top, temperature) -> (logp, entropy, top_logp or None, top_tokens or None, stats)
+PyObject* scores(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Matrix z;
+    void* tokens;
+    uint64_t top;
+    double temperature;
+    if (n != 4 || !z.set(a[0]) || !flat(a[1], z.t, at::kLong, z.rows, &tokens) || !whole(a[2], DCR_MAX_TOP, &top) || !number(a[3], &temperature) ||
+        int64_t(top) > z.cols)
+        Py_RETURN_NONE;
+    Tensor logp = make({z.rows}, at::kFloat, z.t), entropy = make({z.rows}, at::kFloat, z.t), stats = make({z.rows, 3}, at::kFloat, z.t), tl, tt;
+    if (top) tl = make({z.rows, int64_t(top)}, at::kFloat, z.t), tt = make({z.rows, int64_t(top)}, at::kLong, z.t);
+    const int rc = dcr_token_scores(z.t.data_ptr(), z.type, z.rows, z.cols, z.stride, static_cast<const int64_t*>(tokens), float(temperature),
+                                    uint32_t(top), logp.data_ptr<float>(), entropy.data_ptr<float>(), top ? tl.data_ptr<float>() : nullptr,
+                                    top ? tt.data_ptr<int64_t>() : nullptr, stats.data_ptr<float>(), stream_of(z.t));
+    if (rc != DCR_OK) return PyLong_FromLong(rc);
+    PyObject *l = top ? wrap(std::move(tl)) : none(), *t = top ? wrap(std::move(tt)) : none();
+    return Py_BuildValue("(NNNNN)", wrap(std::move(logp)), wrap(std::move(entropy)), l, t, wrap(std::move(stats)));
+    END_HANDLE_TH_ERRORS
+}
+
+// scores_grad(logits, tokens, stats, grad_logp or None, grad_entropy or None, temperature) -> grad
+PyObject* scores_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Matrix z;
+    void *tokens, *stats, *gl = nullptr, *ge = nullptr;
+    double temperature;
+    if (n != 6 || !z.set(a[0]) || !flat(a[1], z.t, at::kLong, z.rows, &tokens) || !flat(a[2], z.t, at::kFloat, z.rows * 3, &stats) ||
+        (a[3] != Py_None && !flat(a[3], z.t, at::kFloat, z.rows, &gl)) || (a[4] != Py_None && !flat(a[4], z.t, at::kFloat, z.rows, &ge)) ||
+        !number(a[5], &temperature))
+        Py_RETURN_NONE;
+    Tensor grad = make({z.rows, z.cols}, z.t.scalar_type(), z.t);
+    const int rc = dcr_token_scores_grad(z.t.data_ptr(), z.type, z.rows, z.cols, z.stride, static_cast<const int64_t*>(tokens),
+                                         static_cast<const float*>(stats), static_cast<const float*>(gl), static_cast<const float*>(ge),
+                                         float(temperature), grad.data_ptr(), z.cols, stream_of(z.t));
+    if (rc != DCR_OK) return PyLong_FromLong(rc);
+    return wrap(std::move(grad));
+    END_HANDLE_TH_ERRORS
+}
+
+bool route_opts(PyObject* scoring, uint64_t k, PyObject* renormalise, PyObject* scale, dcr_route_opts* o)
+{
+    uint64_t s;
+    double f;
+    const int r = PyObject_IsTrue(renormalise);
+    if (r < 0) PyErr_Clear();
+    if (r < 0 || !whole(scoring, 1, &s) || !number(scale, &f)) return false;
+    *o = {uint32_t(s), uint32_t(k), 1, 1, 1, uint32_t(r), float(f)};
+    return true;
+}
+
+// route(logits, k, scoring code, bias or None, groups, group_top, group_by, renormalise, scale, mask or None)
+// -> (experts, weights, offsets, order, positions)
+PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Matrix z;
+    uint64_t k, groups, group_top, group_by;
+    dcr_route_opts o;
+    void *bias = nullptr, *mask = nullptr;
+    if (n != 10 || !z.set(a[0]) || !whole(a[1], DCR_MAX_CHOSEN, &k) || k == 0 || int64_t(k) > z.cols || z.cols > int64_t(DCR_MAX_EXPERTS) ||
+        !route_opts(a[2], k, a[7], a[8], &o) || (a[3] != Py_None && !flat(a[3], z.t, at::kFloat, z.cols, &bias)) || !whole(a[4], 1 << 20, &groups) ||
+        !whole(a[5], 1 << 20, &group_top) || !whole(a[6], 1 << 20, &group_by) ||
+        (a[9] != Py_None && !flat(a[9], z.t, at::kBool, z.rows, &mask) && !flat(a[9], z.t, at::kByte, z.rows, &mask)))
+        Py_RETURN_NONE;
+    o.groups = uint32_t(groups), o.group_top = uint32_t(group_top), o.group_by = uint32_t(group_by);
+    const int64_t kk = int64_t(k);
+    Tensor experts = make({z.rows, kk}, at::kInt, z.t), weights = make({z.rows, kk}, at::kFloat, z.t), offsets = make({z.cols + 1}, at::kInt, z.t),
+           order = make({z.rows * kk}, at::kInt, z.t), positions = make({z.rows, kk}, at::kInt, z.t),
+           work = make({int64_t(DCR_ROUTE_WORKSPACE(z.cols))}, at::kByte, z.t);
+    const int rc = dcr_route(z.t.data_ptr(), z.type, z.rows, uint32_t(z.cols), z.stride, static_cast<const float*>(bias),
+                             static_cast<const uint8_t*>(mask), &o, experts.data_ptr<int32_t>(), weights.data_ptr<float>(),
+                             offsets.data_ptr<int32_t>(), order.data_ptr<int32_t>(), positions.data_ptr<int32_t>(), work.data_ptr(), stream_of(z.t));
+    if (rc != DCR_OK) return PyLong_FromLong(rc);
+    return Py_BuildValue("(NNNNN)", wrap(std::move(experts)), wrap(std::move(weights)), wrap(std::move(offsets)), wrap(std::move(order)),
+                         wrap(std::move(positions)));
+    END_HANDLE_TH_ERRORS
+}
+
+// route_grad(logits, experts, grad_weights, scoring code, renormalise, scale) -> grad
+PyObject* route_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Matrix z;
+    void *chosen, *gw;
+    dcr_route_opts o;
+    if (n != 6 || !z.set(a[0]) || !THPVariable_Check(a[1]) || THPVariable_Unpack(a[1]).dim() != 2) Py_RETURN_NONE;
+    const int64_t k = THPVariable_Unpack(a[1]).size(1);
+    if (k < 1 || k > int64_t(DCR_MAX_CHOSEN) || !slots(a[1], z.t, at::kInt, z.rows, k, &chosen) || !slots(a[2], z.t, at::kFloat, z.rows, k, &gw) ||
+        !route_opts(a[3], k, a[4], a[5], &o))
+        Py_RETURN_NONE;
+    Tensor grad = make({z.rows, z.cols}, z.t.scalar_type(), z.t);
+    const int rc = dcr_route_grad(z.t.data_ptr(), z.type, z.rows, uint32_t(z.cols), z.stride, static_cast<const int32_t*>(chosen),
+                                  static_cast<const float*>(gw), &o, grad.data_ptr(), z.cols, stream_of(z.t));
+    if (rc != DCR_OK) return PyLong_FromLong(rc);
+    return wrap(std::move(grad));
+    END_HANDLE_TH_ERRORS
+}
+
+// A Route's positions and, if asked for, weights.
+struct Slots {
+    int64_t tokens = 0, k = 0;
+    void *positions = nullptr, *weights = nullptr;
+    bool set(PyObject* pos, PyObject* w, const Tensor& like)
+    {
+        if (!THPVariable_Check(pos) || THPVariable_Unpack(pos).dim() != 2) return false;
+        tokens = THPVariable_Unpack(pos).size(0), k = THPVariable_Unpack(pos).size(1);
+        return k >= 1 && k <= int64_t(DCR_MAX_CHOSEN) && slots(pos, like, at::kInt, tokens, k, &positions) &&
+               (w == Py_None || slots(w, like, at::kFloat, tokens, k, &weights));
+    }
+};
+
+// A new matrix, or the one that is given if it is of that shape (and type, if t is one): its tensor, row stride and type code.
+bool output(PyObject* o, int64_t rows, int64_t cols, int type, const Tensor& like, Matrix* m)
+{
+    if (o == Py_None) {
+        m->t = make({rows, cols}, type_of(type), like);
+        m->rows = rows, m->cols = cols, m->stride = cols, m->type = type;
+        return true;
+    }
+    return m->set(o) && m->rows == rows && m->cols == cols && m->t.device() == like.device();
+}
+
+// gather(x, positions, weights or None, type code, out or None) -> rows
+PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Matrix x, y;
+    Slots s;
+    uint64_t type;
+    if (n != 5 || !x.set(a[0]) || !s.set(a[1], a[2], x.t) || s.tokens != x.rows || !whole(a[3], DCR_F16, &type) ||
+        !output(a[4], s.tokens * s.k, x.cols, int(type), x.t, &y))
+        Py_RETURN_NONE;
+    const int rc = dcr_experts_gather(x.t.data_ptr(), x.type, x.rows, x.cols, x.stride, static_cast<const int32_t*>(s.positions), uint32_t(s.k),
+                                      static_cast<const float*>(s.weights), y.t.data_ptr(), y.type, y.rows, y.stride, stream_of(x.t));
+    if (rc != DCR_OK) return PyLong_FromLong(rc);
+    return a[4] == Py_None ? wrap(std::move(y.t)) : (Py_INCREF(a[4]), a[4]);
+    END_HANDLE_TH_ERRORS
+}
+
+// combine(y, positions, weights or None, type code, out or None) -> sums
+PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Matrix y, out;
+    Slots s;
+    uint64_t type;
+    if (n != 5 || !y.set(a[0]) || !s.set(a[1], a[2], y.t) || s.tokens * s.k != y.rows || !whole(a[3], DCR_F16, &type) ||
+        !output(a[4], s.tokens, y.cols, int(type), y.t, &out))
+        Py_RETURN_NONE;
+    const int rc = dcr_experts_combine(y.t.data_ptr(), y.type, y.rows, y.cols, y.stride, static_cast<const int32_t*>(s.positions),
+                                       static_cast<const float*>(s.weights), s.tokens, uint32_t(s.k), out.t.data_ptr(), out.type, out.stride,
+                                       stream_of(y.t));
+    if (rc != DCR_OK) return PyLong_FromLong(rc);
+    return a[4] == Py_None ? wrap(std::move(out.t)) : (Py_INCREF(a[4]), a[4]);
+    END_HANDLE_TH_ERRORS
+}
+
+// combine_grad(y, positions, weights, grad, out or None) -> (gradient by y, by the weights)
+PyObject* combine_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Matrix y, g, out;
+    Slots s;
+    if (n != 5 || a[2] == Py_None || !y.set(a[0]) || !s.set(a[1], a[2], y.t) || s.tokens * s.k != y.rows || !g.set(a[3]) || g.rows != s.tokens ||
+        g.cols != y.cols || !output(a[4], y.rows, y.cols, y.type, y.t, &out) || out.type != y.type)
+        Py_RETURN_NONE;
+    Tensor gw = make({s.tokens, s.k}, at::kFloat, y.t);
+    const int rc = dcr_experts_combine_grad(y.t.data_ptr(), y.type, y.rows, y.cols, y.stride, static_cast<const int32_t*>(s.positions),
+                                            static_cast<const float*>(s.weights), s.tokens, uint32_t(s.k), g.t.data_ptr(), g.type, g.stride,
+                                            out.t.data_ptr(), out.stride, gw.data_ptr<float>(), stream_of(y.t));
+    if (rc != DCR_OK) return PyLong_FromLong(rc);
+    PyObject* first = a[4] == Py_None ? wrap(std::move(out.t)) : (Py_INCREF(a[4]), a[4]);
+    return Py_BuildValue("(NN)", first, wrap(std::move(gw)));
+    END_HANDLE_TH_ERRORS
+}
+
+// Contiguous tensors of one type code on the current device.
+struct Tensors {
+    std::vector<const Tensor*> t;
+    int type = DCR_NONE;
+    bool set(PyObject* list)
+    {
+        if (!PyList_Check(list) || PyList_GET_SIZE(list) == 0) return false;
+        const Py_ssize_t n = PyList_GET_SIZE(list);
+        t.reserve(n);
+        for (Py_ssize_t i = 0; i < n; ++i) {
+            PyObject* o = PyList_GET_ITEM(list, i);
+            if (!THPVariable_Check(o)) return false;
+            const Tensor& x = THPVariable_Unpack(o);
+            if (!x.is_cuda() || x.layout() != at::kStrided || !x.is_contiguous() || x.get_device() != c10::cuda::current_device()) return false;
+            const int c = code_of(x.scalar_type());
+            if (c == DCR_NONE || (i && c != type)) return false;
+            type = c;
+            t.push_back(&x);
+        }
+        return true;
+    }
+};
+
+// norm(list of gradients) -> norm
+PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Tensors g;
+    if (n != 1 || !g.set(a[0])) Py_RETURN_NONE;
+    std::vector<dcr_grad> table;
+    table.reserve(g.t.size());
+    for (const Tensor* x : g.t) table.push_back({x->data_ptr(), uint64_t(x->numel())});
+    const Tensor& like = *g.t[0];
+    Tensor work = make({int64_t(DCR_NORM_WORKSPACE)}, at::kByte, like), out = make({}, at::kFloat, like);
+    const int rc = dcr_grad_norm(table.data(), uint32_t(table.size()), g.type, work.data_ptr(), out.data_ptr<float>(), stream_of(like));
+    if (rc != DCR_OK) return PyLong_FromLong(rc);
+    return wrap(std::move(out));
+    END_HANDLE_TH_ERRORS
+}
+
+// adamw(weights, grads, states (all of one kind), bits, copies or None, norm or None, step, lr, beta1, beta2, eps, weight_decay,
+// max_norm, grad_scale, seed) -> DCR_OK
+PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Tensors w, g, c;
+    if (n != 15 || !w.set(a[0]) || !g.set(a[1]) || g.t.size() != w.t.size() || !PyList_Check(a[2]) ||
+        size_t(PyList_GET_SIZE(a[2])) != w.t.size() || (a[4] != Py_None && (!c.set(a[4]) || c.t.size() != w.t.size())))
+        Py_RETURN_NONE;
+    const Tensor& like = *w.t[0];
+    uint64_t bits, step, seed;
+    dcr_adamw_opts o{};
+    void* np = nullptr;
+    if (!whole(a[3], 32, &bits) || (bits != 8 && bits != 32) || (a[5] != Py_None && !flat(a[5], like, at::kFloat, 1, &np)) || !whole(a[6], ~0ull, &step) ||
+        !number(a[7], &o.lr) || !number(a[8], &o.beta1) || !number(a[9], &o.beta2) || !number(a[10], &o.eps) || !number(a[11], &o.weight_decay) ||
+        !number(a[12], &o.max_norm) || !number(a[13], &o.grad_scale) || !whole(a[14], 0xFFFFFFFFull, &seed))
+        Py_RETURN_NONE;
+    o.step = step, o.norm = static_cast<const float*>(np), o.seed = uint32_t(seed), o.state_bits = uint32_t(bits);
+    std::vector<dcr_adamw_tensor> table;
+    table.reserve(w.t.size());
+    PyTypeObject* kind = Py_TYPE(PyList_GET_ITEM(a[2], 0));
+    const Py_ssize_t parts = bits == 8 ? 4 : 2;
+    for (size_t i = 0; i < w.t.size(); ++i) {
+        PyObject* s = PyList_GET_ITEM(a[2], i);
+        const int64_t size = w.t[i]->numel();
+        if (Py_TYPE(s) != kind || !PyTuple_Check(s) || PyTuple_GET_SIZE(s) != parts || g.t[i]->numel() != size ||
+            (a[4] != Py_None && c.t[i]->numel() != size))
+            Py_RETURN_NONE;
+        dcr_adamw_tensor t{};
+        void *m, *v, *ms = nullptr, *vs = nullptr;
+        if (bits == 32) {
+            if (!flat(PyTuple_GET_ITEM(s, 0), like, at::kFloat, size, &m) || !flat(PyTuple_GET_ITEM(s, 1), like, at::kFloat, size, &v)) Py_RETURN_NONE;
+        } else {
+            const int64_t blocks = (size + DCR_ADAMW_BLOCK - 1) / DCR_ADAMW_BLOCK;
+            auto codes = [&](PyObject* x, void** p) { return flat(x, like, at::kByte, size, p) || flat(x, like, at::kFloat8_e4m3fn, size, p); };
+            if (!codes(PyTuple_GET_ITEM(s, 0), &m) || !codes(PyTuple_GET_ITEM(s, 2), &v) ||
+                !flat(PyTuple_GET_ITEM(s, 1), like, at::kFloat, blocks, &ms) || !flat(PyTuple_GET_ITEM(s, 3), like, at::kFloat, blocks, &vs))
+                Py_RETURN_NONE;
+        }
+        t.w = w.t[i]->data_ptr(), t.grad = g.t[i]->data_ptr(), t.m = m, t.v = v, t.m_scale = static_cast<float*>(ms);
+        t.v_scale = static_cast<float*>(vs), t.copy = a[4] == Py_None ? nullptr : c.t[i]->data_ptr(), t.n = uint64_t(size);
+        table.push_back(t);
+    }
+    return PyLong_FromLong(dcr_adamw(table.data(), uint32_t(table.size()), w.type, g.type, a[4] == Py_None ? int(DCR_NONE) : c.type, &o, stream_of(like)));
+    END_HANDLE_TH_ERRORS
+}
+
+#define CALL(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
-    {"quantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quantize)), METH_FASTCALL, nullptr},
-    {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear)), METH_FASTCALL, nullptr},
-    {"loss", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(loss)), METH_FASTCALL, nullptr},
-    {"logprobs", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(logprobs)), METH_FASTCALL, nullptr},
+    CALL(quantize), CALL(linear), CALL(loss),   CALL(logprobs), CALL(scores),       CALL(scores_grad), CALL(route),
+    CALL(route_grad), CALL(gather), CALL(combine), CALL(combine_grad), CALL(norm), CALL(adamw),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -88,6 +88,14 @@ __device__ __forceinline__ V sigmoid_of(V x)
     return (x < V(0) ? e : V(1)) / (V(1) + e);
 }
 
+// The same to two units more, for keys.
+__device__ __forceinline__ float key_sigmoid(float x)
+{
+    const float e = expf(-fabsf(x));
+    return __fdividef(x < 0.0f ? e : 1.0f, 1.0f + e);
+}
+__device__ __forceinline__ double key_sigmoid(double x) { return sigmoid_of(x); }
+
 // exp(x - m) where m is the largest; equal infinities are 1
 template <typename V>
 __device__ __forceinline__ V below(V x, V m)
@@ -95,26 +103,114 @@ __device__ __forceinline__ V below(V x, V m)
     return x == m ? V(1) : exp_of(x - m);
 }
 
-// What a token chose: lane j has its j-th expert (-1: none) and that one's logit.
+// What a token chose: lane j has its j-th expert (-1: none).
 struct Choice {
     int32_t expert;
-    float logit;
 };
 
-// The k best experts by keys of type V.  Returns whether keys of 32 bits left
-// an order open that the choice or its order depends on.
-template <int PER, typename V>
-__device__ __forceinline__ bool choose(const float (&x)[PER], const RouteArgs& A, Choice& out)
+// The bias of an expert.
+__device__ __forceinline__ float bias_of(const RouteArgs& A, int32_t e) { return A.bias ? A.bias[e] : 0.0f; }
+
+enum Open { kNone = 0, kOrder = 1, kGroups = 2 };
+
+// How far keys of 32 bits may be off: the error of a score in units of 2^-24
+// (the exponential's 4, a sum's and a quotient's 4; for softmax those of up to
+// 37 additions and of a difference of up to 60 from the maximum, too) for
+// both of two neighbours, and half a unit of s + bias.
+struct Slack {
+    float score;
+    __device__ __forceinline__ Slack(bool sigmoid, float most) : score(0x1p-24f * (sigmoid ? 20.0f : 256.0f) * most) {}
+    // a is the larger one; parts: scores that each is the sum of
+    __device__ __forceinline__ bool near(float a, float b, float parts) const
+    {
+        return a - b <= score * parts + 0x1p-23f * parts * (fabsf(a) + fabsf(b));
+    }
+};
+
+// A lane's consecutive values of a row, -inf behind its end; 16 bytes at a
+// time where the row lies so and they are all there.
+template <int PER, typename T>
+__device__ __forceinline__ void load_row(const T* row, uint32_t experts, float (&x)[PER], float empty = -INFINITY)
+{
+    const uint32_t first = threadIdx.x % 32 * PER;
+    if constexpr (PER * sizeof(T) >= 16) {
+        if (first + PER <= experts && (uintptr_t(row + first) & 15) == 0) {
+            constexpr int N = 16 / sizeof(T);
+            uint4 q[PER / N];
+#pragma unroll
+            for (int i = 0; i < PER / N; ++i) q[i] = reinterpret_cast<const uint4*>(row + first)[i];
+            const T* t = reinterpret_cast<const T*>(q);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) x[i] = to_f32(t[i]);
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) x[i] = first + i < experts ? to_f32(row[first + i]) : empty;
+}
+
+// The chosen experts, and those that are near to the last of them (bit i of
+// `rest` for the lane's i-th), a lane each, put in order by their scores in 64
+// bits: the first `count` are the choice.  -2 in all lanes where there are more
+// than lanes.
+template <int PER, typename T>
+__device__ __noinline__ int32_t settle(const T* row, const RouteArgs& A, int32_t e, uint32_t count, uint32_t rest)
+{
+    const uint32_t lane = threadIdx.x % 32, first = lane * PER;
+    uint32_t n = count;
+    for (int i = 0; i < PER; ++i) {
+        for (uint32_t who = __ballot_sync(~0u, rest >> i & 1); who; who &= who - 1) {
+            const int32_t v = __shfl_sync(~0u, int32_t(first) + i, __ffs(who) - 1);
+            if (lane == n) e = v;
+            ++n;
+        }
+    }
+    if (n > 32) return -2;
+    double m = 0.0, inv = 1.0, v = 0.0;
+    if (!A.sigmoid) {
+        float x[PER], top = -INFINITY;
+        load_row<PER, T>(row, A.experts, x);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) top = fmaxf(top, x[i]);
+        m = double(warp_max(top));
+        double s = 0.0;
+        for (int i = 0; i < PER; ++i) s += x[i] > -INFINITY ? below(double(x[i]), m) : 0.0;
+        inv = 1.0 / warp_sum(s);
+    }
+    if (lane < n) {
+        const double z = double(to_f32(row[e]));
+        v = (A.sigmoid ? sigmoid_of(z) : below(z, m) * inv) + double(bias_of(A, e));
+    }
+    uint32_t rank = 0;
+    for (uint32_t i = 0; i < n; ++i) {
+        const double w = __shfl_sync(~0u, v, i);
+        const int32_t f = __shfl_sync(~0u, e, i);
+        rank += w > v || (w == v && f < e);
+    }
+    int32_t out = -1;
+    for (uint32_t i = 0; i < n; ++i) {
+        const uint32_t r = __shfl_sync(~0u, rank, i);
+        const int32_t f = __shfl_sync(~0u, e, i);
+        if (r == lane && lane < count) out = f;
+    }
+    return out;
+}
+
+// The k best experts by keys of type V.  Returns whether keys of 32 bits left open what the choice
+// or its order depends on.
+template <int PER, typename T, typename V>
+__device__ __forceinline__ int choose(const float (&x)[PER], const float (&bias)[PER], const T* row, const RouteArgs& A, Choice& out)
 {
     using O = decltype(order_of(V()));
+    constexpr bool k32 = sizeof(V) == 4;
     const uint32_t lane = threadIdx.x % 32, first = lane * PER;
     O key[PER];
-    V most = V(1);     // the largest score
+    float most = 1.0f;     // the largest score
     if (A.by_logit) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) key[i] = order_of(V(x[i]));
     } else {
-        V m = V(0), total = V(1);
+        V m = V(0), inv = V(1);
         if (!A.sigmoid) {
             float top = -INFINITY;
 #pragma unroll
@@ -123,22 +219,18 @@ __device__ __forceinline__ bool choose(const float (&x)[PER], const RouteArgs& A
             V s = V(0);
 #pragma unroll
             for (int i = 0; i < PER; ++i) s += x[i] > -INFINITY ? below(V(x[i]), m) : V(0);
-            total = warp_sum(s);
-            most = V(1) / total;
+            inv = V(1) / warp_sum(s);
+            most = float(inv);
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            V v = A.sigmoid ? sigmoid_of(V(x[i])) : below(V(x[i]), m) / total;
-            if (A.bias && first + i < A.experts) v += V(A.bias[first + i]);
+            const V v = (A.sigmoid ? key_sigmoid(V(x[i])) : below(V(x[i]), m) * inv) + V(bias[i]);
             key[i] = x[i] > -INFINITY ? order_of(v) : O(0);
         }
     }
-    // The error of a 32-bit key in units of 2^-24: the exponential's 4, a sum's and a quotient's; for softmax those of up
-    // to 37 additions and of a difference of up to 60 from the maximum, too.  Beside it half a unit of s + bias.
-    const bool exact = sizeof(V) == 8 || A.by_logit;
-    const V slack = V(0x1p-24) * (A.sigmoid ? V(12) : V(256)) * most;
-    auto near = [&](V a, V b, V parts) { return !exact && a - b <= slack * parts + V(0x1p-23) * parts * (fabs(a) + fabs(b)); };
-    bool open = false;
+    const Slack slack(A.sigmoid, most);
+    const bool may = k32 && !A.by_logit;    // may leave something open
+    int open = kNone;
     if (A.groups > 1) {
         // lane g: the order of group g's score
         O score = 0;
@@ -181,7 +273,8 @@ __device__ __forceinline__ bool choose(const float (&x)[PER], const RouteArgs& A
             const O top = warp_max(score);
             if (top == 0) break;
             if (r == A.group_top) {
-                open |= near(value_of(last, V()), value_of(top, V()), V(2));
+                if constexpr (k32)
+                    if (may && slack.near(value_of(last, V()), value_of(top, V()), 2.0f)) open |= kGroups;
                 break;
             }
             const uint32_t who = __ffs(__ballot_sync(~0u, score == top)) - 1;
@@ -193,60 +286,61 @@ __device__ __forceinline__ bool choose(const float (&x)[PER], const RouteArgs& A
         for (int i = 0; i < PER; ++i)
             if (!(taken >> min((first + i) / A.group_size, 31u) & 1)) key[i] = 0;
     }
-    out = {-1, 0.0f};
-    O last = 0;
-    int32_t last_expert = -1;
-    float last_logit = 0.0f;
-    for (uint32_t r = 0; r < A.k; ++r) {
-        O best = 0;
-        int32_t at = 0;
-        float logit = 0.0f;
+    out.expert = -1;
+    O mine = 0;
+    uint32_t count = 0;
+    for (; count < A.k; ++count) {
+        O best = key[0];
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (key[i] > best) best = key[i], at = i, logit = x[i];
+        for (int i = 1; i < PER; ++i) best = max(best, key[i]);
         const O top = warp_max(best);
-        if (top == 0) {
-            last = 0;
-            break;
-        }
+        if (top == 0) break;
         const uint32_t who = __ffs(__ballot_sync(~0u, best == top)) - 1;    // lanes hold ascending experts: the lowest of equal ones
+        int32_t at = 0;
+#pragma unroll
+        for (int i = PER - 1; i > 0; --i)
+            if (key[i] == top) at = i;
+        if (key[0] == top) at = 0;
         const int32_t expert = __shfl_sync(~0u, int32_t(first) + at, who);
-        logit = __shfl_sync(~0u, logit, who);
-        // equal ones are so in any precision
-        if (r && near(value_of(last, V()), value_of(top, V()), V(1)))
-            open |= !(last_logit == logit && (!A.bias || A.bias[last_expert] == A.bias[expert]));
-        if (lane == r) out = {expert, logit};
+        if (lane == count) out.expert = expert, mine = top;
         if (lane == who) {
 #pragma unroll
             for (int i = 0; i < PER; ++i)
                 if (i == at) key[i] = 0;
         }
-        last = top, last_expert = expert, last_logit = logit;
     }
-    if (!exact && last != 0) {
-        // whatever was not chosen, against the last that was
-        const V worst = value_of(last, V());
-        bool tie = false;
+    if constexpr (k32) {
+        if (may && count) {
+            // neighbours in order, and what was not chosen against the last that was; equal ones are so in any precision
+            const uint32_t next = __shfl_down_sync(~0u, mine, 1), last = __shfl_sync(~0u, mine, count - 1);
+            const int32_t next_expert = __shfl_down_sync(~0u, out.expert, 1), last_expert = __shfl_sync(~0u, out.expert, count - 1);
+            auto same = [&](int32_t a, int32_t b) { return to_f32(row[a]) == to_f32(row[b]) && bias_of(A, a) == bias_of(A, b); };
+            bool tie = lane + 1 < count && slack.near(value_of(mine, 0.0f), value_of(next, 0.0f), 1.0f) && !same(out.expert, next_expert);
+            uint32_t rest = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (key[i] != 0 && near(worst, value_of(key[i], V()), V(1)))
-                tie |= !(last_logit == x[i] && (!A.bias || A.bias[last_expert] == A.bias[first + i]));
-        open |= __any_sync(~0u, tie);
+            for (int i = 0; i < PER; ++i) {
+                if (key[i] != 0 && slack.near(value_of(last, 0.0f), value_of(key[i], 0.0f), 1.0f)) {
+                    rest |= 1u << i;
+                    tie |= !same(last_expert, first + i);
+                }
+            }
+            if (__any_sync(~0u, tie)) {
+                if (open == kNone) out.expert = settle<PER, T>(row, A, out.expert, count, rest);
+                if (open == kNone && __any_sync(~0u, out.expert == -2)) open = kOrder;
+            }
+        }
     }
     return open;
 }
 
-template <int PER, typename T>
-__device__ __forceinline__ void load_row(const T* row, uint32_t experts, float (&x)[PER])
-{
-    const uint32_t first = threadIdx.x % 32 * PER;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) x[i] = first + i < experts ? to_f32(row[first + i]) : -INFINITY;
-}
+struct Slot {
+    int32_t expert;
+    float logit;
+};
 
 // Weights of the chosen experts from their logits, before the scale; for a
 // softmax that is not renormalised m and total are the row's.
-__device__ __forceinline__ float weight_of(const Choice& c, bool sigmoid, bool renormalise, float m, float total)
+__device__ __forceinline__ float weight_of(const Slot& c, bool sigmoid, bool renormalise, float m, float total)
 {
     const bool on = c.expert >= 0;
     if (!renormalise) return !on ? 0.0f : sigmoid ? sigmoid_of(c.logit) : below(c.logit, m) / total;
@@ -272,28 +366,32 @@ __device__ __forceinline__ void softmax_of(const float (&x)[PER], float& m, floa
 }
 
 // Decided again in 64 bits; apart, so that its registers do not weigh on the others.
-template <int PER>
-__device__ __noinline__ void choose_again(const float* x, const RouteArgs& A, Choice* c)
+template <int PER, typename T>
+__device__ __noinline__ int32_t choose_again(const T* row, const RouteArgs& A)
 {
-    float v[PER];
+    float x[PER], bias[PER];
+    load_row<PER, T>(row, A.experts, x);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] = x[i];
+    for (int i = 0; i < PER; ++i) bias[i] = A.bias && threadIdx.x % 32 * PER + i < A.experts ? A.bias[threadIdx.x % 32 * PER + i] : 0.0f;
     Choice out;
-    choose<PER, double>(v, A, out);
-    *c = out;
+    choose<PER, T, double>(x, bias, row, A, out);
+    return out.expert;
 }
 
-// A token by a warp; its experts are counted in `counts`.
+// A token by a warp, whose row x holds; its experts are counted in `counts`.
 template <int PER, typename T>
-__device__ __forceinline__ Choice route_token(const RouteArgs& A, uint64_t token, uint32_t* counts)
+__device__ __forceinline__ int32_t route_token(const RouteArgs& A, uint64_t token, const float (&x)[PER], const float (&bias)[PER], uint32_t* counts)
 {
     const uint32_t lane = threadIdx.x % 32;
-    Choice c = {-1, 0.0f};
+    const T* row = static_cast<const T*>(A.logits) + token * A.row_stride;
+    Slot c = {-1, 0.0f};
     float w = 0.0f;
     if (!A.mask || A.mask[token]) {
-        float x[PER], m = 0.0f, total = 1.0f;
-        load_row<PER, T>(static_cast<const T*>(A.logits) + token * A.row_stride, A.experts, x);
-        if (choose<PER, float>(x, A, c)) choose_again<PER>(x, A, &c);
+        Choice out;
+        if (choose<PER, T, float>(x, bias, row, A, out) != kNone) out.expert = choose_again<PER, T>(row, A);
+        c.expert = out.expert;
+        if (c.expert >= 0) c.logit = to_f32(row[c.expert]);
+        float m = 0.0f, total = 1.0f;
         if (!A.sigmoid && !A.renormalise) softmax_of(x, m, total);
         w = weight_of(c, A.sigmoid, A.renormalise, m, total) * A.scale;
     }
@@ -302,7 +400,27 @@ __device__ __forceinline__ Choice route_token(const RouteArgs& A, uint64_t token
         A.weights[token * A.k + lane] = c.expert < 0 ? 0.0f : w;
         if (c.expert >= 0) atomicAdd(&counts[c.expert], 1u);
     }
-    return c;
+    return c.expert;
+}
+
+// Tokens begin, begin + step, ... of a warp; a row is loaded while the one
+// before it is decided.
+template <int PER, typename T, typename F>
+__device__ __forceinline__ void route_tokens(const RouteArgs& A, uint64_t begin, uint64_t end, uint32_t step, uint32_t* counts, F each)
+{
+    float bias[PER], next[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) bias[i] = 0.0f;
+    if (A.bias) load_row<PER, float>(A.bias, A.experts, bias, 0.0f);
+    const T* rows = static_cast<const T*>(A.logits);
+    if (begin < end) load_row<PER, T>(rows + begin * A.row_stride, A.experts, next);
+    for (uint64_t t = begin; t < end; t += step) {
+        float x[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) x[i] = next[i];
+        if (t + step < end) load_row<PER, T>(rows + (t + step) * A.row_stride, A.experts, next);
+        each(t, route_token<PER, T>(A, t, x, bias, counts));
+    }
 }
 
 // Exclusive sums of v[0..n) in place, by a whole block; returns the total.
@@ -359,19 +477,20 @@ __device__ __forceinline__ void place(const RouteArgs& A, const int32_t* chosen,
 }
 
 constexpr int kThreads = 256;
+constexpr int kRouteThreads = 512;
 constexpr uint32_t kMaxParts = DCR_ROUTE_PARTS;
 
 template <int PER, typename T>
-__global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs A)
+__global__ void __launch_bounds__(kRouteThreads, PER <= 8 ? 2 : 1) route_kernel(const RouteArgs A)
 {
     __shared__ uint32_t counts[DCR_MAX_EXPERTS];
     launch_dependents();
-    for (uint32_t e = threadIdx.x; e < A.experts; e += kThreads) counts[e] = 0;
+    for (uint32_t e = threadIdx.x; e < A.experts; e += kRouteThreads) counts[e] = 0;
     __syncthreads();
     const uint64_t begin = uint64_t(blockIdx.x) * A.per_part, end = min(begin + A.per_part, A.tokens);
-    for (uint64_t t = begin + threadIdx.x / 32; t < end; t += kThreads / 32) route_token<PER, T>(A, t, counts);
+    route_tokens<PER, T>(A, begin + threadIdx.x / 32, end, kRouteThreads / 32, counts, [](uint64_t, int32_t) {});
     __syncthreads();
-    for (uint32_t e = threadIdx.x; e < A.experts; e += kThreads) A.counts[uint64_t(blockIdx.x) * A.experts + e] = counts[e];
+    for (uint32_t e = threadIdx.x; e < A.experts; e += kRouteThreads) A.counts[uint64_t(blockIdx.x) * A.experts + e] = counts[e];
 }
 
 // A warp an expert: the parts' counts become what lies before each part.
@@ -381,16 +500,19 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const RouteArgs A)
     grid_wait();
     const uint32_t e = blockIdx.x * (kThreads / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
     if (e >= A.experts) return;
-    uint32_t base = 0;
-    for (uint32_t p = 0; p < A.parts; p += 32) {
-        const uint32_t mine = p + lane < A.parts ? A.counts[uint64_t(p + lane) * A.experts + e] : 0;
-        uint32_t s = mine;
+    constexpr int kRounds = (kMaxParts + 31) / 32;
+    uint32_t v[kRounds], base = 0;      // all loads before the first sum
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) v[r] = r * 32 + lane < A.parts ? A.counts[uint64_t(r * 32 + lane) * A.experts + e] : 0;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        uint32_t s = v[r];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t u = __shfl_up_sync(~0u, s, o);
             if (lane >= uint32_t(o)) s += u;
         }
-        if (p + lane < A.parts) A.counts[uint64_t(p + lane) * A.experts + e] = base + s - mine;
+        if (r * 32 + lane < A.parts) A.counts[uint64_t(r * 32 + lane) * A.experts + e] = base + s - v[r];
         base += __shfl_sync(~0u, s, 31);
     }
     if (lane == 0) A.counts[uint64_t(A.parts) * A.experts + e] = base;
@@ -416,28 +538,29 @@ __global__ void __launch_bounds__(kThreads) place_kernel(const RouteArgs A)
     place<kThreads>(A, A.chosen + begin, begin, end, next);
 }
 
-// All of it for a batch of few slots.
-constexpr int kOneThreads = 512;
+// All of it for a batch of few slots; as many threads as have the registers.
 constexpr uint32_t kOneSlots = 1024;
+template <int PER>
+constexpr int kOneThreads = PER <= 4 ? 1024 : 512;
 
 template <int PER, typename T>
-__global__ void __launch_bounds__(kOneThreads) route_one_kernel(const RouteArgs A)
+__global__ void __launch_bounds__(kOneThreads<PER>) route_one_kernel(const RouteArgs A)
 {
+    constexpr int TH = kOneThreads<PER>;
     __shared__ uint32_t next[DCR_MAX_EXPERTS];
     __shared__ int32_t chosen[kOneSlots];
-    for (uint32_t e = threadIdx.x; e < A.experts; e += kOneThreads) next[e] = 0;
+    for (uint32_t e = threadIdx.x; e < A.experts; e += TH) next[e] = 0;
     __syncthreads();
-    for (uint64_t t = threadIdx.x / 32; t < A.tokens; t += kOneThreads / 32) {
-        const Choice c = route_token<PER, T>(A, t, next);
-        if (threadIdx.x % 32 < A.k) chosen[t * A.k + threadIdx.x % 32] = c.expert;
-    }
+    route_tokens<PER, T>(A, threadIdx.x / 32, A.tokens, TH / 32, next, [&](uint64_t t, int32_t expert) {
+        if (threadIdx.x % 32 < A.k) chosen[t * A.k + threadIdx.x % 32] = expert;
+    });
     __syncthreads();
-    const uint32_t total = scan<kOneThreads>(next, A.experts), slots = uint32_t(A.tokens) * A.k;
-    for (uint32_t e = threadIdx.x; e < A.experts; e += kOneThreads) A.offsets[e] = int32_t(next[e]);
+    const uint32_t total = scan<TH>(next, A.experts), slots = uint32_t(A.tokens) * A.k;
+    for (uint32_t e = threadIdx.x; e < A.experts; e += TH) A.offsets[e] = int32_t(next[e]);
     if (threadIdx.x == 0) A.offsets[A.experts] = int32_t(total);
-    for (uint32_t r = total + threadIdx.x; r < slots; r += kOneThreads) A.order[r] = -1;
+    for (uint32_t r = total + threadIdx.x; r < slots; r += TH) A.order[r] = -1;
     __syncthreads();
-    place<kOneThreads>(A, chosen, 0, slots, next);
+    place<TH>(A, chosen, 0, slots, next);
 }
 
 struct RouteGradArgs {
@@ -462,7 +585,7 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(const RouteGradArg
     float* row = rows[threadIdx.x / 32];
     for (uint64_t t = uint64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; t < A.tokens; t += uint64_t(gridDim.x) * (kThreads / 32)) {
         const T* x = static_cast<const T*>(A.logits) + t * A.row_stride;
-        Choice c = {-1, 0.0f};
+        Slot c = {-1, 0.0f};
         float d = 0.0f;
         if (lane < A.k) {
             c.expert = A.chosen[t * A.k + lane];
@@ -522,19 +645,20 @@ int route_launch(RouteArgs A, uint32_t dtype, cudaStream_t s)
 {
     cudaError_t e = cudaSuccess;
     if (A.tokens * A.k <= kOneSlots) {
-        const LaunchAttrs at(1, kOneThreads, 0, 1, false, s);
         with_dtype(dtype, [&](auto t) {
             return with_per(A.experts, [&](auto per) {
-                e = cudaLaunchKernelEx(&at.cfg, route_one_kernel<decltype(per)::value, decltype(t)>, A);
+                constexpr int PER = decltype(per)::value;
+                const LaunchAttrs at(1, kOneThreads<PER>, 0, 1, false, s);
+                e = cudaLaunchKernelEx(&at.cfg, route_one_kernel<PER, decltype(t)>, A);
                 return 0;
             });
         });
         return e == cudaSuccess ? DCR_OK : cuda_error(e, "route launch");
     }
     // a warp's tokens come one after another: parts as small as fill two blocks an SM
-    A.per_part = uint32_t(std::max<uint64_t>((A.tokens + kMaxParts - 1) / kMaxParts, kThreads / 32));
+    A.per_part = uint32_t(std::max<uint64_t>((A.tokens + kMaxParts - 1) / kMaxParts, kRouteThreads / 32));
     A.parts = uint32_t((A.tokens + A.per_part - 1) / A.per_part);
-    const LaunchAttrs at(A.parts, kThreads, 0, 1, false, s);
+    const LaunchAttrs at(A.parts, kRouteThreads, 0, 1, false, s);
     with_dtype(dtype, [&](auto t) {
         return with_per(A.experts, [&](auto per) {
             e = cudaLaunchKernelEx(&at.cfg, route_kernel<decltype(per)::value, decltype(t)>, A);

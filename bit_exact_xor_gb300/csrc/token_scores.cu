@@ -60,50 +60,61 @@ struct Sums {
     float s, t;
 };
 
-template <bool PLAIN, int N>
+// CLAMP: where a value is -inf, or left out as if it were.
+template <bool PLAIN, bool CLAMP, int N>
 __device__ __forceinline__ void add_values(Sums& a, const float (&v)[N], const Exponent& e)
 {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
+        float d = PLAIN ? fmaf(v[i], e.lo, fmaf(v[i], e.sc, -e.msc)) : fmaf(v[i] - e.m, e.lo, (v[i] - e.m) * e.sc);
         // -200: exp of it is 0, and so is its product with it, which with -inf would not be a number
-        const float d = max_nan(PLAIN ? fmaf(v[i], e.lo, fmaf(v[i], e.sc, -e.msc)) : fmaf(v[i] - e.m, e.lo, (v[i] - e.m) * e.sc), -200.0f);
+        if (CLAMP) d = max_nan(d, -200.0f);
         const float p = exp2_fast(d);
         a.s += p;
         a.t = fmaf(p, d, a.t);
     }
 }
 
-// count: null, or receives how many values are equal to m, which are left out.
-template <typename T, int NV>
-__device__ __forceinline__ Sums chunk_sums(const uint4 (&q)[NV], float m, const ScoreArgs& A, float* count)
+template <typename T, bool PLAIN, bool CLAMP, int NV>
+__device__ __forceinline__ Sums add_words(const uint4 (&q)[NV], const Exponent& e)
 {
     Sums a = {0.0f, 0.0f};
-    if (fabsf(m) == INFINITY) {
-        bool nan = false;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) nan |= word_nan<T>(q[i]);
-        if (nan) a.s = a.t = NAN;
-        return a;
-    }
-    const Exponent e(m, A.sc_dn, A.sc_lo);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         float v[Word<T>::kN];
         Word<T>::values(q[i], v);
-        if (count) {
-#pragma unroll
-            for (int j = 0; j < Word<T>::kN; ++j) {
-                if (v[j] == m) *count += 1.0f;
-                v[j] = v[j] == m ? -INFINITY : v[j];
-            }
-        }
-        if (e.plain) add_values<true>(a, v, e);
-        else add_values<false>(a, v, e);
+        add_values<PLAIN, CLAMP>(a, v, e);
     }
-    // what every exponent has too much
+    return a;
+}
+
+// What every exponent has too much is taken out of the sums.
+__device__ __forceinline__ void correct(Sums& a, const Exponent& e)
+{
     const float x = e.term_excess(), f = exp2f(-x);
     a.t = fmaf(-x, a.s, a.t) * f;
     a.s *= f;
+}
+
+// The same over the values below m, and how many are equal to it (m is finite or +inf).
+template <typename T, int NV>
+__device__ __forceinline__ Sums chunk_sums_below(const uint4 (&q)[NV], float m, const ScoreArgs& A, float& count)
+{
+    const Exponent e(m, A.sc_dn, A.sc_lo);
+    Sums a = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float v[Word<T>::kN];
+        Word<T>::values(q[i], v);
+#pragma unroll
+        for (int j = 0; j < Word<T>::kN; ++j) {
+            if (v[j] == m) count += 1.0f;
+            v[j] = v[j] == m ? -INFINITY : v[j];
+        }
+        if (e.plain) add_values<true, true>(a, v, e);
+        else add_values<false, true>(a, v, e);
+    }
+    correct(a, e);
     return a;
 }
 
@@ -137,6 +148,13 @@ __device__ __forceinline__ float value_of(uint32_t o)
 }
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t index) { return uint64_t(order_of(x)) << 32 | uint32_t(~index); }
 
+__device__ __forceinline__ uint4 load_word(const void* p)
+{
+    uint4 q;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "l"(p));
+    return q;
+}
+
 // This block's words of a row.
 template <typename T>
 struct Share {
@@ -149,7 +167,13 @@ struct Share {
     }
     __device__ __forceinline__ void load(uint32_t c, uint4 (&q)[kWords]) const
     {
-        const uint32_t k = first + c * kWords * step;
+        const uint32_t k = first + c * kWords * step, block = k - threadIdx.x;
+        if (block >= in.lo && block + (kWords - 1) * step + blockDim.x <= in.hi) {   // nothing of the block's chunk is cut
+            const T* p = in.base + uint64_t(k) * Word<T>::kN;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) q[i] = load_word(p + uint64_t(i * step) * Word<T>::kN);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < kWords; ++i) q[i] = in.load_whole(k + i * step);
 #pragma unroll
@@ -178,14 +202,41 @@ struct Share {
     }
 };
 
+// The sums over a chunk whose largest value is no larger than m, in rows that
+// hold -inf, NaN or an infinite m, or lie far from 0.  Apart, with the chunk
+// read again, so that the common case has its registers.
+template <typename T>
+__device__ __noinline__ Sums rare_sums(const T* x, uint32_t vocab, uint32_t rank, uint32_t blocks, uint32_t c, float m, float sc, float lo)
+{
+    const Share<T> S(x, vocab, rank, blocks);
+    Sums a = {0.0f, 0.0f};
+    const Exponent e(m, sc, lo);
+    bool nan = false;
+    for (int i = 0; i < kWords; ++i) {
+        const uint4 q = S.in.load(S.first + (c * kWords + i) * S.step);
+        float v[Word<T>::kN];
+        Word<T>::values(q, v);
+        nan |= word_nan<T>(q);
+        if (e.plain) add_values<true, true>(a, v, e);
+        else add_values<false, true>(a, v, e);
+    }
+    if (fabsf(m) == INFINITY) {
+        a.s = a.t = nan ? NAN : 0.0f;
+        return a;
+    }
+    correct(a, e);
+    return a;
+}
+
 template <int TH>
 struct TopMemory {
     float chunk_max[kBuckets][TH];
     uint64_t list[kList];
+    uint16_t bucket[kBuckets * TH];   // those that hold a value of the list: index in chunk_max
     uint64_t best[DCR_MAX_TOP];    // this block's, the largest first; 0: none
     uint64_t part[TH / 32];
     uint32_t bound[TH / 32];
-    uint32_t count, scan[TH / 32];
+    uint32_t count, buckets, scan[TH / 32];
 };
 
 // The n largest of list[0..count) to best.
@@ -195,7 +246,30 @@ __device__ __forceinline__ void sort_list(TopMemory<TH>& M, uint32_t count, uint
     for (uint32_t i = threadIdx.x; i < count; i += TH) {
         const uint64_t mine = M.list[i];
         uint32_t above = 0;
+#pragma unroll 8
         for (uint32_t j = 0; j < count; ++j) above += M.list[j] > mine;
+        if (above < n && mine != 0) M.best[above] = mine;
+    }
+}
+
+// The same of `lists` sorted lists of n, one after another: in each other
+// list it is searched how many are larger.
+template <int TH>
+__device__ __forceinline__ void merge_lists(TopMemory<TH>& M, uint32_t lists, uint32_t n)
+{
+    for (uint32_t i = threadIdx.x; i < lists * n; i += TH) {
+        const uint64_t mine = M.list[i];
+        uint32_t above = i % n;
+        for (uint32_t l = 0; l < lists; ++l) {
+            if (l == i / n) continue;
+            uint32_t lo = 0, hi = n;        // the first that is not larger
+            while (lo < hi) {
+                const uint32_t mid = (lo + hi) / 2;
+                if (M.list[l * n + mid] > mine) lo = mid + 1;
+                else hi = mid;
+            }
+            above += lo;
+        }
         if (above < n && mine != 0) M.best[above] = mine;
     }
 }
@@ -214,23 +288,32 @@ __device__ void find_top(TopMemory<TH>& M, const Share<T>& S, float mine, uint32
         if (lane == __ffs(who) - 1) left = 0;
     }
     if (lane == 0) M.bound[warp] = most;
-    if (threadIdx.x == 0) M.count = 0;
+    if (threadIdx.x == 0) M.count = M.buckets = 0;
     if (threadIdx.x < n) M.best[threadIdx.x] = 0;
     __syncthreads();
     uint32_t bound = M.bound[0];
     for (uint32_t i = 1; i < W; ++i) bound = min(bound, M.bound[i]);
+    // values of at least this order to the list.  The buckets that hold some are listed first, so that their words are shared
+    // out among all threads.
     auto collect = [&](uint32_t least) {
         for (uint32_t b = 0; b < min(S.chunks, kBuckets); ++b)
-            if (order_of(M.chunk_max[b][threadIdx.x]) >= least)
-                for (uint32_t c = b; c < S.chunks; c += kBuckets)
-                    S.each_of_chunk(c, [&](float v, uint32_t at) {
-                        if (order_of(v) >= least) {
-                            const uint32_t p = atomicAdd(&M.count, 1u);   // where a value stands in the list does not matter
-                            if (p < kList) M.list[p] = key_of(v, at);
-                        }
-                    });
+            if (order_of(M.chunk_max[b][threadIdx.x]) >= least) M.bucket[atomicAdd(&M.buckets, 1u)] = uint16_t(b * TH + threadIdx.x);
+        __syncthreads();
+        const uint32_t words = M.buckets * kWords;
+        for (uint32_t i = threadIdx.x; i < words; i += TH) {
+            const uint32_t from = M.bucket[i / kWords], thread = from % TH;
+            for (uint32_t c = from / TH; c < S.chunks; c += kBuckets) {
+                const uint32_t k = S.first - threadIdx.x + thread + (c * kWords + i % kWords) * S.step;
+                S.each(S.in.load(k), k, [&](float v, uint32_t at) {
+                    if (order_of(v) >= least) {
+                        const uint32_t p = atomicAdd(&M.count, 1u);   // where a value stands in the list does not matter
+                        if (p < kList) M.list[p] = key_of(v, at);
+                    }
+                });
+            }
+        }
     };
-    if (bound != 0) collect(bound);
+    collect(bound);
     __syncthreads();
     uint32_t count = M.count;
     if (count >= n && count <= kList) {
@@ -242,7 +325,7 @@ __device__ void find_top(TopMemory<TH>& M, const Share<T>& S, float mine, uint32
     if (count > kList) {
         // more than the list holds: those above the bound, then the first that are equal to it
         __syncthreads();
-        if (threadIdx.x == 0) M.count = 0;
+        if (threadIdx.x == 0) M.count = M.buckets = 0;
         __syncthreads();
         collect(bound + 1);
         __syncthreads();
@@ -324,7 +407,7 @@ __device__ __forceinline__ V remote(const V* p, uint32_t rank)
 __device__ __forceinline__ void cluster_barrier() { asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory"); }
 
 template <typename T, int TH, bool TOP>
-__global__ void __launch_bounds__(TH, 1024 / TH) scores_kernel(ScoreArgs A, uint32_t cluster)
+__global__ void __launch_bounds__(TH, 768 / TH) scores_kernel(ScoreArgs A, uint32_t cluster)
 {
     constexpr uint32_t W = TH / 32;
     __shared__ float4 parts[W];
@@ -372,7 +455,11 @@ __global__ void __launch_bounds__(TH, 1024 / TH) scores_kernel(ScoreArgs A, uint
             }
             top = {0.0f, 0.0f}, m = cm, at = c;
         }
-        const Sums a = chunk_sums<T, kWords>(q, m, A, nullptr);
+        const Exponent e(m, A.sc_dn, A.sc_lo);
+        Sums a = add_words<T, true, false>(q, e);
+        // not a number where a value is -inf or none itself
+        if (!(fabsf(a.t) < INFINITY) || !e.plain) a = rare_sums<T>(x, vocab, rank, cluster, c, m, A.sc_dn, A.sc_lo);
+        else correct(a, e);
         if (higher) top = a;
         else rest.s += a.s, rest.t += a.t;
     }
@@ -389,7 +476,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) scores_kernel(ScoreArgs A, uint
         // the chunk of the maximum again, without what is equal to it
         uint4 q[kWords];
         S.load(at, q);
-        top = chunk_sums<T, kWords>(q, m, A, &p.count);
+        top = chunk_sums_below<T, kWords>(q, m, A, p.count);
         p.s = rest.s + top.s, p.t = rest.t + top.t;
     }
     all.add(p, A.sc);
@@ -421,7 +508,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) scores_kernel(ScoreArgs A, uint
                 const uint32_t n = cluster * A.top;
                 for (uint32_t i = threadIdx.x; i < n; i += TH) top_memory.list[i] = remote(&top_memory.best[i % A.top], i / A.top);
                 __syncthreads();     // also: this block's own part of best is read
-                sort_list(top_memory, n, A.top);
+                merge_lists(top_memory, cluster, A.top);
                 __syncthreads();
             }
         }
@@ -535,16 +622,26 @@ int scores_launch(const ScoreArgs& A, uint32_t cluster, cudaStream_t s)
     return e == cudaSuccess ? DCR_OK : cuda_error(e, "token scores launch");
 }
 
-// Few long rows are shared by the blocks of a cluster, as long as each has a
-// chunk of its own.
+// Blocks of 128 or 256 threads, and one to eight of them for a row, whichever
+// the model of a launch finds fastest: rounds of as many blocks as fit at once
+// (768 threads an SM), each the time of its chunks, which is DRAM's for what
+// the SMs then have in flight (15 MB when full) or a load's latency, and the
+// steps at its end, which take longer where blocks have to meet.  (1021 rows
+// of 32771 f32 values: blocks of 256 leave a second round half empty.)
 template <typename T>
 int scores_launch(const ScoreArgs& A, cudaStream_t s)
 {
     const uint64_t words = (A.vocab * sizeof(T) + 15) / 16 + 1;
-    if (words <= 1024) return scores_launch<T, 128>(A, 1, s);
-    uint32_t cluster = 1;
-    while (cluster < kMaxBlocks && A.rows * cluster < 2 * 152 && words / cluster > 256 * kWords) cluster *= 2;
-    return scores_launch<T, 256>(A, cluster, s);
+    uint32_t threads = 128, cluster = 1;
+    double best = 1e300;
+    for (uint32_t th = 128; th <= 256; th *= 2)
+        for (uint32_t c = 1; c <= uint32_t(kMaxBlocks) && (c == 1 || words >= uint64_t(c) * th); c *= 2) {
+            const double slots = 152.0 * 768 / th, blocks = double(A.rows) * c, rounds = std::ceil(blocks / slots);
+            const double chunks = std::ceil(double(words) / (c * th * kWords));
+            const double us = rounds * (chunks * std::max(1.0, 2.4 * std::min(1.0, blocks / slots)) + 4.0 + (c > 1 ? 2.0 : 0.0));
+            if (us < best) best = us, threads = th, cluster = c;
+        }
+    return threads == 128 ? scores_launch<T, 128>(A, cluster, s) : scores_launch<T, 256>(A, cluster, s);
 }
 
 template <typename T, int TH, int NV>

@@ -8,7 +8,7 @@ from typing import NamedTuple
 import torch
 
 from . import OK, check
-from .ops import DTYPES, MAX_EXPERTS, SIGMOID, SOFTMAX, _elsewhere, _flat, _lib, _matrix, _raw_stream, _refuse
+from .ops import DTYPES, MAX_EXPERTS, SIGMOID, SOFTMAX, _elsewhere, _fast, _flat, _lib, _matrix, _raw_stream, _refuse, _result_of
 
 MAX_CHOSEN, MAX_GROUPS, ROUTE_PARTS = 32, 32, 304
 SCORINGS = {"softmax": SOFTMAX, "sigmoid": SIGMOID}
@@ -70,6 +70,11 @@ def route_experts(logits, k, scoring="softmax", bias=None, groups=1, group_top=N
     experts sum highest; renormalise: the chosen scores are divided by their
     sum; scale multiplies the weights; mask: bool or uint8 [tokens], False for
     tokens that go nowhere."""
+    if stream is None:
+        r = _fast.route(logits, k, SCORINGS.get(scoring), bias, groups, groups if group_top is None else group_top, group_by, renormalise,
+                        scale, mask)
+        if r is not None:
+            return Route(*_result_of(r))
     tokens, experts, stride, t = _matrix(logits, "logits")
     dev = logits.device
     if stream is not None or dev.index != torch.cuda.current_device():
@@ -108,6 +113,10 @@ def route_experts_grad(logits, route, grad_weights, scoring="softmax", renormali
     whose derivative by route.weights is grad_weights (float32 [tokens, k]).
     scoring, renormalise and scale are those of route_experts; out: a matrix to
     write to."""
+    if stream is None and out is None:
+        r = _fast.route_grad(logits, route.experts, grad_weights, SCORINGS.get(scoring), renormalise, scale)
+        if r is not None:
+            return _result_of(r)
     tokens, experts, stride, t = _matrix(logits, "logits")
     dev = logits.device
     if stream is not None or dev.index != torch.cuda.current_device():
@@ -141,6 +150,10 @@ def experts_gather(x, route, weighted=False, dtype=None, out=None, stream=None):
     [tokens * k, cols] in `dtype` (default: x's) or into `out`, times
     route.weights if weighted.  Rows behind the last expert's are left as they
     are."""
+    if stream is None:
+        r = _fast.gather(x, route.positions, route.weights if weighted else None, DTYPES.get(x.dtype if dtype is None else dtype), out)
+        if r is not None:
+            return _result_of(r)
     tokens, cols, stride, t = _matrix(x, "x")
     dev = x.device
     if stream is not None or dev.index != torch.cuda.current_device():
@@ -160,6 +173,10 @@ def experts_combine(y, route, weighted=True, dtype=None, out=None, stream=None):
     """dcr_experts_combine: for each token the sum of its rows of y [tokens * k,
     cols], times route.weights if weighted, [tokens, cols] in `dtype` (default:
     y's) or into `out`.  With weighted=False it is experts_gather's gradient."""
+    if stream is None:
+        r = _fast.combine(y, route.positions, route.weights if weighted else None, DTYPES.get(y.dtype if dtype is None else dtype), out)
+        if r is not None:
+            return _result_of(r)
     rows, cols, stride, t = _matrix(y, "y")
     dev = y.device
     if stream is not None or dev.index != torch.cuda.current_device():
@@ -182,6 +199,10 @@ def experts_combine_grad(y, route, grad, out=None, stream=None):
     of its output, grad [tokens, cols], those by y (in y's type; into `out`;
     rows behind the last expert's are left as they are) and by route.weights
     (float32 [tokens, k])."""
+    if stream is None:
+        r = _fast.combine_grad(y, route.positions, route.weights, grad, out)
+        if r is not None:
+            return _result_of(r)
     rows, cols, stride, t = _matrix(y, "y")
     dev = y.device
     if stream is not None or dev.index != torch.cuda.current_device():

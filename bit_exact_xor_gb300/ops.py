@@ -82,7 +82,8 @@ def _refuse(what):
 class _NoBinding:
     """In the compiled binding's place: takes no call, so that each goes on to
     the code below and through ctypes to the same kernels."""
-    quantize = linear = loss = logprobs = staticmethod(lambda *args: None)
+    quantize = linear = loss = logprobs = scores = scores_grad = route = route_grad = staticmethod(lambda *args: None)
+    gather = combine = combine_grad = norm = adamw = staticmethod(lambda *args: None)
 
 
 def _binding():

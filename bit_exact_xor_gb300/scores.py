@@ -7,7 +7,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import OK, check
-from .ops import _elsewhere, _flat, _lib, _matrix, _raw_stream, _refuse
+from .ops import _elsewhere, _fast, _flat, _lib, _matrix, _raw_stream, _refuse, _result_of
 
 MAX_TOP = 64
 _f32 = torch.float32
@@ -43,6 +43,10 @@ def token_scores(logits, tokens, top=0, temperature=1.0, stream=None):
     and tokens int64 [rows]: a TokenScores under softmax(logits / temperature).
     A row whose token lies outside [0, vocab) is left out (zeros, alternatives
     -1)."""
+    if stream is None:
+        r = _fast.scores(logits, tokens, top, temperature)
+        if r is not None:
+            return TokenScores(*_result_of(r))
     rows, vocab, stride, t = _matrix(logits, "logits")
     dev = logits.device
     if stream is not None or dev.index != torch.cuda.current_device():
@@ -69,6 +73,10 @@ def token_scores_grad(logits, tokens, stats, grad_logp=None, grad_entropy=None, 
     grad_entropy (float32 [rows], either may be None).  stats and temperature
     are that call's; out: a matrix to write to (logits itself, to save the
     memory)."""
+    if stream is None and out is None:
+        r = _fast.scores_grad(logits, tokens, stats, grad_logp, grad_entropy, temperature)
+        if r is not None:
+            return _result_of(r)
     rows, vocab, stride, t = _matrix(logits, "logits")
     dev = logits.device
     if stream is not None or dev.index != torch.cuda.current_device():
