@@ -377,7 +377,7 @@ __device__ __forceinline__ uint32_t tensor_of(const TABLE& T, uint32_t c)
 }
 
 template <int WB, int GB, int BITS, int N>
-__global__ void __launch_bounds__(kThreads, BITS == 8 ? 3 : 2) adamw_kernel(const __grid_constant__ Table<N> T, const AdamwArgs A)
+__global__ void __launch_bounds__(kThreads, BITS == 8 ? 4 : 2) adamw_kernel(const __grid_constant__ Table<N> T, const AdamwArgs A)
 {
     const Common C(A);
     if (C.skip) return;

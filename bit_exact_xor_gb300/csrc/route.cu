@@ -1,16 +1,20 @@
 // Routing of tokens to experts, and its gradient (include/dcr_ops.h).
 //
-// A warp takes a token: each lane holds PER consecutive experts, and k rounds
-// of a maximum over the warp find the chosen ones in order.  Where scores are
-// compared (with a bias, or for groups), 32 bits do not tell near ones apart:
-// it is noted whether two neighbours in that order, or the last chosen
-// and one that is not, lie nearer than the error of 32-bit scores allows, which happens to about one token in a
-// thousand, and such a token is decided again with scores in 64 bits.
+// A warp takes a token, each lane PER consecutive experts.  The k-th largest
+// of the lanes' maxima is a bound that at least k keys reach, and few more: the
+// keys that reach it go to a lane each, which counts how many are above its
+// own.  Where scores are compared (with a bias, or for groups), 32 bits do not
+// tell near ones apart: the bound is lowered by what such keys may be off, and
+// a token of which two neighbours among the first k, or the last of them and a
+// later one, are nearer than that is put in order by scores in 64 bits, a lane
+// an expert (settle; about one token in a thousand), and so are groups
+// (settle_groups).  Where more keys reach the bound than a warp has lanes, a
+// token is decided anew in 64 bits, one expert after another.
 //
-// The experts' order is a counting sort that keeps the tokens' order: blocks
-// count what their tokens chose (route_kernel), a warp an expert adds up the
-// blocks' counts (scan_kernel), and the same blocks place their slots
-// (place_kernel).  A small batch takes one block and one launch.
+// The experts' order is a counting sort that keeps the tokens' order: parts of
+// the batch, one a block, count what their tokens chose (route_kernel); then
+// each block adds up the counts of the parts before its own and places its
+// slots (place_kernel).  A small batch takes one block and one launch.
 #include <algorithm>
 #include <cmath>
 
@@ -28,9 +32,9 @@ struct RouteArgs {
     int32_t* offsets;
     int32_t* order;
     int32_t* positions;
-    uint32_t* counts;       // [parts][experts], then a total for each expert
+    uint32_t* counts;       // [parts][stride]
     uint64_t tokens, row_stride;
-    uint32_t experts, parts, per_part;
+    uint32_t experts, stride, parts, per_part;    // stride: of counts, a multiple of 4
     uint32_t k, groups, group_top, group_by, group_size;
     bool sigmoid, renormalise, by_logit;
     float scale;
@@ -103,15 +107,8 @@ __device__ __forceinline__ V below(V x, V m)
     return x == m ? V(1) : exp_of(x - m);
 }
 
-// What a token chose: lane j has its j-th expert (-1: none).
-struct Choice {
-    int32_t expert;
-};
-
 // The bias of an expert.
 __device__ __forceinline__ float bias_of(const RouteArgs& A, int32_t e) { return A.bias ? A.bias[e] : 0.0f; }
-
-enum Open { kNone = 0, kOrder = 1, kGroups = 2 };
 
 // How far keys of 32 bits may be off: the error of a score in units of 2^-24
 // (the exponential's 4, a sum's and a quotient's 4; for softmax those of up to
@@ -149,63 +146,98 @@ __device__ __forceinline__ void load_row(const T* row, uint32_t experts, float (
     for (int i = 0; i < PER; ++i) x[i] = first + i < experts ? to_f32(row[first + i]) : empty;
 }
 
-// The chosen experts, and those that are near to the last of them (bit i of
-// `rest` for the lane's i-th), a lane each, put in order by their scores in 64
-// bits: the first `count` are the choice.  -2 in all lanes where there are more
-// than lanes.
+// A softmax's maximum and 1 / sum in 64 bits, by the whole warp; nothing for sigmoid.
+struct Softmax64 {
+    double m, inv;
+};
 template <int PER, typename T>
-__device__ __noinline__ int32_t settle(const T* row, const RouteArgs& A, int32_t e, uint32_t count, uint32_t rest)
+__device__ __forceinline__ Softmax64 softmax_64(const T* row, const RouteArgs& A)
 {
-    const uint32_t lane = threadIdx.x % 32, first = lane * PER;
-    uint32_t n = count;
-    for (int i = 0; i < PER; ++i) {
-        for (uint32_t who = __ballot_sync(~0u, rest >> i & 1); who; who &= who - 1) {
-            const int32_t v = __shfl_sync(~0u, int32_t(first) + i, __ffs(who) - 1);
-            if (lane == n) e = v;
-            ++n;
-        }
-    }
-    if (n > 32) return -2;
-    double m = 0.0, inv = 1.0, v = 0.0;
-    if (!A.sigmoid) {
-        float x[PER], top = -INFINITY;
-        load_row<PER, T>(row, A.experts, x);
+    Softmax64 f = {0.0, 1.0};
+    if (A.sigmoid) return f;
+    float x[PER], top = -INFINITY;
+    load_row<PER, T>(row, A.experts, x);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) top = fmaxf(top, x[i]);
-        m = double(warp_max(top));
-        double s = 0.0;
-        for (int i = 0; i < PER; ++i) s += x[i] > -INFINITY ? below(double(x[i]), m) : 0.0;
-        inv = 1.0 / warp_sum(s);
-    }
-    if (lane < n) {
-        const double z = double(to_f32(row[e]));
-        v = (A.sigmoid ? sigmoid_of(z) : below(z, m) * inv) + double(bias_of(A, e));
-    }
+    for (int i = 0; i < PER; ++i) top = fmaxf(top, x[i]);
+    f.m = double(warp_max(top));
+    double s = 0.0;
+    for (int i = 0; i < PER; ++i) s += x[i] > -INFINITY ? below(double(x[i]), f.m) : 0.0;
+    f.inv = 1.0 / warp_sum(s);
+    return f;
+}
+// The order of an expert's key in 64 bits.
+template <typename T>
+__device__ __forceinline__ uint64_t key_64(const T* row, const RouteArgs& A, const Softmax64& f, int32_t e)
+{
+    const double x = double(to_f32(row[e]));
+    if (!(x > -double(INFINITY))) return 0;
+    return order_of((A.sigmoid ? sigmoid_of(x) : below(x, f.m) * f.inv) + double(bias_of(A, e)));
+}
+
+// Lanes 0 to n - 1 hold the first `count` experts in the order of 32 bits and
+// those behind them that are near to the last: put in order by their scores
+// in 64 bits.  The first `count` are the choice.
+template <int PER, typename T>
+__device__ __noinline__ int32_t settle(const T* row, const RouteArgs& A, int32_t e, uint32_t count, uint32_t n)
+{
+    const uint32_t lane = threadIdx.x % 32;
+    const Softmax64 f = softmax_64<PER>(row, A);
+    const uint64_t v = lane < n ? key_64(row, A, f, e) : 0;
     uint32_t rank = 0;
     for (uint32_t i = 0; i < n; ++i) {
-        const double w = __shfl_sync(~0u, v, i);
-        const int32_t f = __shfl_sync(~0u, e, i);
-        rank += w > v || (w == v && f < e);
+        const uint64_t w = __shfl_sync(~0u, static_cast<unsigned long long>(v), i);
+        const int32_t other = __shfl_sync(~0u, e, i);
+        rank += w > v || (w == v && other < e);
     }
     int32_t out = -1;
     for (uint32_t i = 0; i < n; ++i) {
         const uint32_t r = __shfl_sync(~0u, rank, i);
-        const int32_t f = __shfl_sync(~0u, e, i);
-        if (r == lane && lane < count) out = f;
+        const int32_t other = __shfl_sync(~0u, e, i);
+        if (r == lane && lane < count) out = other;
     }
     return out;
 }
 
-// The k best experts by keys of type V.  Returns whether keys of 32 bits left open what the choice
-// or its order depends on.
-template <int PER, typename T, typename V>
-__device__ __forceinline__ int choose(const float (&x)[PER], const float (&bias)[PER], const T* row, const RouteArgs& A, Choice& out)
+// Of the groups `open`, those of the largest scores in 64 bits join the groups
+// `taken` until there are group_top.
+template <int PER, typename T>
+__device__ __noinline__ uint32_t settle_groups(const T* row, const RouteArgs& A, uint32_t taken, uint32_t open)
 {
-    using O = decltype(order_of(V()));
+    const uint32_t lane = threadIdx.x % 32;
+    const Softmax64 f = softmax_64<PER>(row, A);
+    uint64_t score = 0;
+    for (uint32_t rest = open; rest; rest &= rest - 1) {
+        const uint32_t g = __ffs(rest) - 1;
+        uint64_t a = 0, b = 0;
+        for (uint32_t i = lane; i < A.group_size; i += 32) {
+            const uint64_t v = key_64(row, A, f, int32_t(g * A.group_size + i));
+            b = max(b, min(a, v));
+            a = max(a, v);
+        }
+        const uint64_t top = warp_max(a);
+        const uint32_t who = __ffs(__ballot_sync(~0u, a == top)) - 1;
+        const uint64_t next = warp_max(lane == who ? b : a);
+        if (lane == g) score = next == 0 || A.group_by == 1 ? top : order_of(value_of(top, 0.0) + value_of(next, 0.0));
+    }
+    while (__popc(taken) < int(A.group_top)) {
+        const uint64_t top = warp_max(score);
+        if (top == 0) break;
+        const uint32_t who = __ffs(__ballot_sync(~0u, score == top)) - 1;
+        taken |= 1u << who;
+        if (lane == who) score = 0;
+    }
+    return taken;
+}
+
+// The orders of all experts' keys, of type V; 0 for those that cannot be
+// chosen, and for those of groups that are not taken.  most: the largest
+// score.
+template <int PER, typename T, typename V, typename O>
+__device__ __forceinline__ void keys_of(const T* row, const float (&x)[PER], const float (&bias)[PER], const RouteArgs& A, O (&key)[PER], float& most)
+{
     constexpr bool k32 = sizeof(V) == 4;
     const uint32_t lane = threadIdx.x % 32, first = lane * PER;
-    O key[PER];
-    float most = 1.0f;     // the largest score
+    most = 1.0f;
     if (A.by_logit) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) key[i] = order_of(V(x[i]));
@@ -228,9 +260,6 @@ __device__ __forceinline__ int choose(const float (&x)[PER], const float (&bias)
             key[i] = x[i] > -INFINITY ? order_of(v) : O(0);
         }
     }
-    const Slack slack(A.sigmoid, most);
-    const bool may = k32 && !A.by_logit;    // may leave something open
-    int open = kNone;
     if (A.groups > 1) {
         // lane g: the order of group g's score
         O score = 0;
@@ -267,14 +296,24 @@ __device__ __forceinline__ int choose(const float (&x)[PER], const float (&bias)
                 if (lane == g) score = join(top, next);
             }
         }
+        const O group = score;
         uint32_t taken = 0;
         O last = 0;
         for (uint32_t r = 0; r <= A.group_top; ++r) {
             const O top = warp_max(score);
             if (top == 0) break;
             if (r == A.group_top) {
-                if constexpr (k32)
-                    if (may && slack.near(value_of(last, V()), value_of(top, V()), 2.0f)) open |= kGroups;
+                if constexpr (k32) {
+                    const Slack slack(A.sigmoid, most);
+                    const float in = value_of(last, 0.0f), out = value_of(top, 0.0f), mine = value_of(group, 0.0f);
+                    if (!A.by_logit && slack.near(in, out, 2.0f)) {
+                        // groups that may change places
+                        const bool taken_one = taken >> lane & 1;
+                        const bool close = group != 0 && (taken_one ? slack.near(mine, out, 2.0f) : slack.near(in, mine, 2.0f));
+                        const uint32_t all = __ballot_sync(~0u, close);
+                        taken = settle_groups<PER>(row, A, taken & ~all, all);
+                    }
+                }
                 break;
             }
             const uint32_t who = __ffs(__ballot_sync(~0u, score == top)) - 1;
@@ -286,51 +325,99 @@ __device__ __forceinline__ int choose(const float (&x)[PER], const float (&bias)
         for (int i = 0; i < PER; ++i)
             if (!(taken >> min((first + i) / A.group_size, 31u) & 1)) key[i] = 0;
     }
-    out.expert = -1;
-    O mine = 0;
-    uint32_t count = 0;
-    for (; count < A.k; ++count) {
-        O best = key[0];
+}
+
+// The k best experts by keys of 64 bits, one after another: lane j's is the
+// j-th (-1: none).  Apart, so that its registers do not weigh on the others.
+template <int PER, typename T>
+__device__ __noinline__ int32_t choose_again(const T* row, const RouteArgs& A)
+{
+    const uint32_t lane = threadIdx.x % 32, first = lane * PER;
+    float x[PER], bias[PER], most;
+    uint64_t key[PER];
+    load_row<PER, T>(row, A.experts, x);
 #pragma unroll
-        for (int i = 1; i < PER; ++i) best = max(best, key[i]);
-        const O top = warp_max(best);
-        if (top == 0) break;
-        const uint32_t who = __ffs(__ballot_sync(~0u, best == top)) - 1;    // lanes hold ascending experts: the lowest of equal ones
+    for (int i = 0; i < PER; ++i) bias[i] = first + i < A.experts ? bias_of(A, first + i) : 0.0f;
+    keys_of<PER, T, double>(row, x, bias, A, key, most);
+    int32_t mine = -1;
+    for (uint32_t r = 0; r < A.k; ++r) {
+        uint64_t best = 0;
         int32_t at = 0;
 #pragma unroll
-        for (int i = PER - 1; i > 0; --i)
-            if (key[i] == top) at = i;
-        if (key[0] == top) at = 0;
+        for (int i = 0; i < PER; ++i)
+            if (key[i] > best) best = key[i], at = i;
+        const uint64_t top = warp_max(best);
+        if (top == 0) break;
+        const uint32_t who = __ffs(__ballot_sync(~0u, best == top)) - 1;    // lanes hold ascending experts: the lowest of equal ones
         const int32_t expert = __shfl_sync(~0u, int32_t(first) + at, who);
-        if (lane == count) out.expert = expert, mine = top;
+        if (lane == r) mine = expert;
         if (lane == who) {
 #pragma unroll
             for (int i = 0; i < PER; ++i)
                 if (i == at) key[i] = 0;
         }
     }
-    if constexpr (k32) {
-        if (may && count) {
-            // neighbours in order, and what was not chosen against the last that was; equal ones are so in any precision
-            const uint32_t next = __shfl_down_sync(~0u, mine, 1), last = __shfl_sync(~0u, mine, count - 1);
-            const int32_t next_expert = __shfl_down_sync(~0u, out.expert, 1), last_expert = __shfl_sync(~0u, out.expert, count - 1);
-            auto same = [&](int32_t a, int32_t b) { return to_f32(row[a]) == to_f32(row[b]) && bias_of(A, a) == bias_of(A, b); };
-            bool tie = lane + 1 < count && slack.near(value_of(mine, 0.0f), value_of(next, 0.0f), 1.0f) && !same(out.expert, next_expert);
-            uint32_t rest = 0;
+    return mine;
+}
+
+// The k best experts: lane j's is the j-th (-1: none).  list: 32 entries of
+// the warp's own.
+template <int PER, typename T>
+__device__ __forceinline__ int32_t choose(const float (&x)[PER], const float (&bias)[PER], const T* row, const RouteArgs& A, uint64_t* list)
+{
+    const uint32_t lane = threadIdx.x % 32, first = lane * PER;
+    uint32_t key[PER];
+    float most;
+    keys_of<PER, T, float>(row, x, bias, A, key, most);
+    uint32_t best = key[0], bound = 1;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                if (key[i] != 0 && slack.near(value_of(last, 0.0f), value_of(key[i], 0.0f), 1.0f)) {
-                    rest |= 1u << i;
-                    tie |= !same(last_expert, first + i);
-                }
-            }
-            if (__any_sync(~0u, tie)) {
-                if (open == kNone) out.expert = settle<PER, T>(row, A, out.expert, count, rest);
-                if (open == kNone && __any_sync(~0u, out.expert == -2)) open = kOrder;
-            }
+    for (int i = 1; i < PER; ++i) best = max(best, key[i]);
+    for (uint32_t r = 0; r < A.k; ++r) {
+        const uint32_t top = warp_max(best);
+        if (top == 0) {     // fewer lanes than k: all that can be chosen
+            bound = 1;
+            break;
         }
+        const uint32_t who = __ffs(__ballot_sync(~0u, best == top)) - 1;
+        if (lane == who) best = 0;
+        bound = top;
     }
-    return open;
+    const Slack slack(A.sigmoid, most);
+    if (!A.by_logit && bound > 1) {
+        const float b = value_of(bound, 0.0f);
+        bound = max(order_of(b - slack.score - 0x1p-21f * fabsf(b)), 1u);   // (infinite - infinite: all)
+    }
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const bool in = key[i] >= bound;
+        const uint32_t all = __ballot_sync(~0u, in), at = n + __popc(all & ((1u << lane) - 1));
+        if (in && at < 32) list[at] = uint64_t(key[i]) << 32 | (0xFFFFFFFFu - (first + i));    // the lower expert above
+        n += __popc(all);
+    }
+    if (n > 32) return choose_again<PER, T>(row, A);
+    __syncwarp();
+    uint64_t mine = lane < n ? list[lane] : 0;
+    uint32_t rank = 0;
+#pragma unroll 4
+    for (uint32_t i = 0; i < n; ++i) rank += list[i] > mine;
+    __syncwarp();
+    if (lane < n) list[rank] = mine;
+    __syncwarp();
+    mine = lane < n ? list[lane] : 0;
+    __syncwarp();
+    const uint32_t count = min(n, A.k);
+    const int32_t expert = lane < n ? int32_t(0xFFFFFFFFu - uint32_t(mine)) : -1;
+    if (!A.by_logit && n > 1) {
+        // each of the first `count` against the next one, those behind them against the last; equal ones are so in any precision
+        const uint32_t other = lane < count ? lane + 1 : count - 1;
+        const float v = value_of(uint32_t(mine >> 32), 0.0f), u = __shfl_sync(~0u, v, other & 31);
+        const int32_t e = __shfl_sync(~0u, expert, other & 31);
+        const bool close = lane < n && other < n && slack.near(fmaxf(u, v), fminf(u, v), 1.0f);
+        const bool tie = close && !(to_f32(row[e]) == to_f32(row[expert]) && bias_of(A, e) == bias_of(A, expert));
+        if (__any_sync(~0u, tie)) return settle<PER, T>(row, A, expert, count, count + __popc(__ballot_sync(~0u, close && lane >= count)));
+    }
+    return lane < count ? expert : -1;
 }
 
 struct Slot {
@@ -365,31 +452,16 @@ __device__ __forceinline__ void softmax_of(const float (&x)[PER], float& m, floa
     total = warp_sum(total);
 }
 
-// Decided again in 64 bits; apart, so that its registers do not weigh on the others.
-template <int PER, typename T>
-__device__ __noinline__ int32_t choose_again(const T* row, const RouteArgs& A)
-{
-    float x[PER], bias[PER];
-    load_row<PER, T>(row, A.experts, x);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) bias[i] = A.bias && threadIdx.x % 32 * PER + i < A.experts ? A.bias[threadIdx.x % 32 * PER + i] : 0.0f;
-    Choice out;
-    choose<PER, T, double>(x, bias, row, A, out);
-    return out.expert;
-}
-
 // A token by a warp, whose row x holds; its experts are counted in `counts`.
 template <int PER, typename T>
-__device__ __forceinline__ int32_t route_token(const RouteArgs& A, uint64_t token, const float (&x)[PER], const float (&bias)[PER], uint32_t* counts)
+__device__ __forceinline__ int32_t route_token(const RouteArgs& A, uint64_t token, const float (&x)[PER], const float (&bias)[PER], uint64_t* list, uint32_t* counts)
 {
     const uint32_t lane = threadIdx.x % 32;
     const T* row = static_cast<const T*>(A.logits) + token * A.row_stride;
     Slot c = {-1, 0.0f};
     float w = 0.0f;
     if (!A.mask || A.mask[token]) {
-        Choice out;
-        if (choose<PER, T, float>(x, bias, row, A, out) != kNone) out.expert = choose_again<PER, T>(row, A);
-        c.expert = out.expert;
+        c.expert = choose<PER, T>(x, bias, row, A, list);
         if (c.expert >= 0) c.logit = to_f32(row[c.expert]);
         float m = 0.0f, total = 1.0f;
         if (!A.sigmoid && !A.renormalise) softmax_of(x, m, total);
@@ -406,7 +478,7 @@ __device__ __forceinline__ int32_t route_token(const RouteArgs& A, uint64_t toke
 // Tokens begin, begin + step, ... of a warp; a row is loaded while the one
 // before it is decided.
 template <int PER, typename T, typename F>
-__device__ __forceinline__ void route_tokens(const RouteArgs& A, uint64_t begin, uint64_t end, uint32_t step, uint32_t* counts, F each)
+__device__ __forceinline__ void route_tokens(const RouteArgs& A, uint64_t begin, uint64_t end, uint32_t step, uint64_t (*lists)[32], uint32_t* counts, F each)
 {
     float bias[PER], next[PER];
 #pragma unroll
@@ -419,7 +491,7 @@ __device__ __forceinline__ void route_tokens(const RouteArgs& A, uint64_t begin,
 #pragma unroll
         for (int i = 0; i < PER; ++i) x[i] = next[i];
         if (t + step < end) load_row<PER, T>(rows + (t + step) * A.row_stride, A.experts, next);
-        each(t, route_token<PER, T>(A, t, x, bias, counts));
+        each(t, route_token<PER, T>(A, t, x, bias, lists[threadIdx.x / 32], counts));
     }
 }
 
@@ -452,106 +524,140 @@ __device__ __forceinline__ uint32_t scan(uint32_t* v, uint32_t n)
     return base;
 }
 
-// Slots begin to end into their rows, in their order; next[e]: the next row of expert e.
+// Slots begin to end into their rows, in their order; next[e]: the next row of
+// expert e.  before: [TH / 32][experts]: what the warps of a round hold of each
+// expert, then what lies before each warp's.
 template <int TH>
-__device__ __forceinline__ void place(const RouteArgs& A, const int32_t* chosen, uint64_t begin, uint64_t end, uint32_t* next)
+__device__ __forceinline__ void place(const RouteArgs& A, const int32_t* chosen, uint64_t begin, uint64_t end, uint32_t* next, uint16_t* before)
 {
-    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32, n = A.experts;
     for (uint64_t at = begin; at < end; at += TH) {
+        const uint32_t warps = uint32_t(min((end - at + 31) / 32, uint64_t(TH / 32)));
+        for (uint32_t i = threadIdx.x; i < warps * n; i += TH) before[i] = 0;
+        __syncthreads();
         const uint64_t slot = at + threadIdx.x;
         const int32_t e = slot < end ? chosen[slot - begin] : -1;
-        const uint32_t same = __match_any_sync(~0u, e), before = __popc(same & ((1u << lane) - 1));
-        for (uint32_t w = 0; w < TH / 32 && at + w * 32 < end; ++w) {
-            if (w == warp) {
-                const uint32_t row = e >= 0 ? next[e] + before : 0;
-                __syncwarp();
-                if (e >= 0) {
-                    if (before == 0) next[e] = row + __popc(same);
-                    A.order[row] = int32_t(slot);
+        const uint32_t same = __match_any_sync(~0u, e), first = __popc(same & ((1u << lane) - 1));
+        if (e >= 0 && first == 0) before[warp * n + e] = uint16_t(__popc(same));
+        __syncthreads();
+        uint32_t sum[(DCR_MAX_EXPERTS + TH - 1) / TH];
+#pragma unroll
+        for (int j = 0; j < int(DCR_MAX_EXPERTS + TH - 1) / TH; ++j) {
+            const uint32_t x = threadIdx.x + j * TH;
+            sum[j] = 0;
+            if (x < n) {
+                for (uint32_t w0 = 0; w0 < warps; w0 += 8) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (uint32_t w = 0; w < 8; ++w) v[w] = w0 + w < warps ? before[(w0 + w) * n + x] : 0;
+#pragma unroll
+                    for (uint32_t w = 0; w < 8; ++w) {
+                        if (w0 + w < warps) before[(w0 + w) * n + x] = uint16_t(sum[j]);
+                        sum[j] += v[w];
+                    }
                 }
-                if (slot < end) A.positions[slot] = e >= 0 ? int32_t(row) : -1;
             }
-            __syncthreads();
         }
+        __syncthreads();
+        if (e >= 0) {
+            const uint32_t row = next[e] + before[warp * n + e] + first;
+            A.order[row] = int32_t(slot);
+            A.positions[slot] = int32_t(row);
+        } else if (slot < end) {
+            A.positions[slot] = -1;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < int(DCR_MAX_EXPERTS + TH - 1) / TH; ++j)
+            if (threadIdx.x + j * TH < n) next[threadIdx.x + j * TH] += sum[j];
+        __syncthreads();
     }
 }
 
 constexpr int kThreads = 256;
-constexpr int kRouteThreads = 512;
 constexpr uint32_t kMaxParts = DCR_ROUTE_PARTS;
+// Threads of a block: as many as have the registers that lanes with PER experts take.
+template <int PER>
+constexpr int kRouteThreads = PER <= 4 ? 1024 : PER == 8 ? 768 : 512;
 
 template <int PER, typename T>
-__global__ void __launch_bounds__(kRouteThreads, PER <= 8 ? 2 : 1) route_kernel(const RouteArgs A)
+__global__ void __launch_bounds__(kRouteThreads<PER>) route_kernel(const RouteArgs A)
 {
-    __shared__ uint32_t counts[DCR_MAX_EXPERTS];
+    constexpr int TH = kRouteThreads<PER>;
+    __shared__ uint32_t counts[PER * 32];
+    __shared__ uint64_t lists[TH / 32][32];
     launch_dependents();
-    for (uint32_t e = threadIdx.x; e < A.experts; e += kRouteThreads) counts[e] = 0;
+    for (uint32_t e = threadIdx.x; e < A.stride; e += TH) counts[e] = 0;
     __syncthreads();
     const uint64_t begin = uint64_t(blockIdx.x) * A.per_part, end = min(begin + A.per_part, A.tokens);
-    route_tokens<PER, T>(A, begin + threadIdx.x / 32, end, kRouteThreads / 32, counts, [](uint64_t, int32_t) {});
+    route_tokens<PER, T>(A, begin + threadIdx.x / 32, end, TH / 32, lists, counts, [](uint64_t, int32_t) {});
     __syncthreads();
-    for (uint32_t e = threadIdx.x; e < A.experts; e += kRouteThreads) A.counts[uint64_t(blockIdx.x) * A.experts + e] = counts[e];
+    for (uint32_t e = threadIdx.x; e < A.stride; e += TH) A.counts[uint64_t(blockIdx.x) * A.stride + e] = counts[e];
 }
 
-// A warp an expert: the parts' counts become what lies before each part.
-__global__ void __launch_bounds__(kThreads) scan_kernel(const RouteArgs A)
+template <int TH>
+__global__ void __launch_bounds__(TH) place_kernel(const RouteArgs A)
 {
-    launch_dependents();
+    extern __shared__ uint16_t before[];
+    __shared__ uint32_t next[DCR_MAX_EXPERTS], mine[DCR_MAX_EXPERTS];   // all parts' counts, then rows; those of the parts before
+    for (uint32_t e = threadIdx.x; e < A.stride; e += TH) next[e] = mine[e] = 0;
+    __syncthreads();
     grid_wait();
-    const uint32_t e = blockIdx.x * (kThreads / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (e >= A.experts) return;
-    constexpr int kRounds = (kMaxParts + 31) / 32;
-    uint32_t v[kRounds], base = 0;      // all loads before the first sum
+    // a warp takes the same 128 experts, 4 a lane, of every so many parts
+    constexpr uint32_t kAtOnce = 10;
+    const uint32_t quads = A.stride / 4, wide = (quads + 31) / 32;
+    const uint32_t per = wide <= 1 ? 1 : wide <= 2 ? 2 : wide <= 4 ? 4 : 8, quad = threadIdx.x / 32 % per * 32 + threadIdx.x % 32, step = TH / 32 / per;
+    if (quad < quads) {
+        uint4 all = make_uint4(0, 0, 0, 0), ours = all;
+        for (uint32_t first = threadIdx.x / 32 / per; first < A.parts; first += step * kAtOnce) {
+            uint4 v[kAtOnce];
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) v[r] = r * 32 + lane < A.parts ? A.counts[uint64_t(r * 32 + lane) * A.experts + e] : 0;
+            for (uint32_t i = 0; i < kAtOnce; ++i) {
+                const uint32_t p = first + i * step;
+                v[i] = p < A.parts ? reinterpret_cast<const uint4*>(A.counts)[uint64_t(p) * quads + quad] : make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-        uint32_t s = v[r];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t u = __shfl_up_sync(~0u, s, o);
-            if (lane >= uint32_t(o)) s += u;
+            for (uint32_t i = 0; i < kAtOnce; ++i) {
+                all.x += v[i].x, all.y += v[i].y, all.z += v[i].z, all.w += v[i].w;
+                if (first + i * step < blockIdx.x) ours.x += v[i].x, ours.y += v[i].y, ours.z += v[i].z, ours.w += v[i].w;
+            }
         }
-        if (r * 32 + lane < A.parts) A.counts[uint64_t(r * 32 + lane) * A.experts + e] = base + s - v[r];
-        base += __shfl_sync(~0u, s, 31);
+        const uint32_t a[4] = {all.x, all.y, all.z, all.w}, o[4] = {ours.x, ours.y, ours.z, ours.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (a[i]) atomicAdd(&next[quad * 4 + i], a[i]);     // whole numbers: in any order
+            if (o[i]) atomicAdd(&mine[quad * 4 + i], o[i]);
+        }
     }
-    if (lane == 0) A.counts[uint64_t(A.parts) * A.experts + e] = base;
-}
-
-__global__ void __launch_bounds__(kThreads) place_kernel(const RouteArgs A)
-{
-    __shared__ uint32_t next[DCR_MAX_EXPERTS];
-    grid_wait();
-    for (uint32_t e = threadIdx.x; e < A.experts; e += kThreads) next[e] = A.counts[uint64_t(A.parts) * A.experts + e];
     __syncthreads();
-    const uint32_t total = scan<kThreads>(next, A.experts);
+    const uint32_t total = scan<TH>(next, A.experts);
     const uint64_t slots = A.tokens * A.k;
     if (blockIdx.x == 0) {
-        for (uint32_t e = threadIdx.x; e < A.experts; e += kThreads) A.offsets[e] = int32_t(next[e]);
+        for (uint32_t e = threadIdx.x; e < A.experts; e += TH) A.offsets[e] = int32_t(next[e]);
         if (threadIdx.x == 0) A.offsets[A.experts] = int32_t(total);
         __syncthreads();
     }
-    for (uint64_t r = total + uint64_t(blockIdx.x) * kThreads + threadIdx.x; r < slots; r += uint64_t(gridDim.x) * kThreads) A.order[r] = -1;
-    for (uint32_t e = threadIdx.x; e < A.experts; e += kThreads) next[e] += A.counts[uint64_t(blockIdx.x) * A.experts + e];
+    for (uint64_t r = total + uint64_t(blockIdx.x) * TH + threadIdx.x; r < slots; r += uint64_t(gridDim.x) * TH) A.order[r] = -1;
+    for (uint32_t e = threadIdx.x; e < A.experts; e += TH) next[e] += mine[e];
     __syncthreads();
     const uint64_t begin = min(uint64_t(blockIdx.x) * A.per_part * A.k, slots), end = min(begin + uint64_t(A.per_part) * A.k, slots);
-    place<kThreads>(A, A.chosen + begin, begin, end, next);
+    place<TH>(A, A.chosen + begin, begin, end, next, before);
 }
 
-// All of it for a batch of few slots; as many threads as have the registers.
+// All of it for a batch of few slots.
 constexpr uint32_t kOneSlots = 1024;
-template <int PER>
-constexpr int kOneThreads = PER <= 4 ? 1024 : 512;
 
 template <int PER, typename T>
-__global__ void __launch_bounds__(kOneThreads<PER>) route_one_kernel(const RouteArgs A)
+__global__ void __launch_bounds__(kRouteThreads<PER>) route_one_kernel(const RouteArgs A)
 {
-    constexpr int TH = kOneThreads<PER>;
-    __shared__ uint32_t next[DCR_MAX_EXPERTS];
+    constexpr int TH = kRouteThreads<PER>;
+    extern __shared__ uint16_t before[];
+    __shared__ uint32_t next[PER * 32];
     __shared__ int32_t chosen[kOneSlots];
+    __shared__ uint64_t lists[TH / 32][32];
     for (uint32_t e = threadIdx.x; e < A.experts; e += TH) next[e] = 0;
     __syncthreads();
-    route_tokens<PER, T>(A, threadIdx.x / 32, A.tokens, TH / 32, next, [&](uint64_t t, int32_t expert) {
+    route_tokens<PER, T>(A, threadIdx.x / 32, A.tokens, TH / 32, lists, next, [&](uint64_t t, int32_t expert) {
         if (threadIdx.x % 32 < A.k) chosen[t * A.k + threadIdx.x % 32] = expert;
     });
     __syncthreads();
@@ -560,7 +666,7 @@ __global__ void __launch_bounds__(kOneThreads<PER>) route_one_kernel(const Route
     if (threadIdx.x == 0) A.offsets[A.experts] = int32_t(total);
     for (uint32_t r = total + threadIdx.x; r < slots; r += TH) A.order[r] = -1;
     __syncthreads();
-    place<TH>(A, chosen, 0, slots, next);
+    place<TH>(A, chosen, 0, slots, next, before);
 }
 
 struct RouteGradArgs {
@@ -641,34 +747,29 @@ int with_per(uint32_t experts, F f)
     return f(std::integral_constant<int, 32>());
 }
 
+// Shared memory that place() takes: 32 KB at most.
+size_t place_bytes(int threads, uint32_t experts) { return size_t(threads / 32) * experts * sizeof(uint16_t); }
+
 int route_launch(RouteArgs A, uint32_t dtype, cudaStream_t s)
 {
+    const bool one = A.tokens * A.k <= kOneSlots;
     cudaError_t e = cudaSuccess;
-    if (A.tokens * A.k <= kOneSlots) {
-        with_dtype(dtype, [&](auto t) {
-            return with_per(A.experts, [&](auto per) {
-                constexpr int PER = decltype(per)::value;
-                const LaunchAttrs at(1, kOneThreads<PER>, 0, 1, false, s);
-                e = cudaLaunchKernelEx(&at.cfg, route_one_kernel<PER, decltype(t)>, A);
-                return 0;
-            });
-        });
-        return e == cudaSuccess ? DCR_OK : cuda_error(e, "route launch");
-    }
-    // a warp's tokens come one after another: parts as small as fill two blocks an SM
-    A.per_part = uint32_t(std::max<uint64_t>((A.tokens + kMaxParts - 1) / kMaxParts, kRouteThreads / 32));
+    // a part an SM, but no fewer tokens than warps
+    A.per_part = uint32_t(std::max<uint64_t>((A.tokens + kMaxParts - 1) / kMaxParts, 16));
     A.parts = uint32_t((A.tokens + A.per_part - 1) / A.per_part);
-    const LaunchAttrs at(A.parts, kRouteThreads, 0, 1, false, s);
     with_dtype(dtype, [&](auto t) {
         return with_per(A.experts, [&](auto per) {
-            e = cudaLaunchKernelEx(&at.cfg, route_kernel<decltype(per)::value, decltype(t)>, A);
+            constexpr int PER = decltype(per)::value, TH = kRouteThreads<PER>;
+            const LaunchAttrs at(one ? 1 : A.parts, TH, one ? place_bytes(TH, A.experts) : 0, 1, false, s);
+            e = one ? cudaLaunchKernelEx(&at.cfg, route_one_kernel<PER, decltype(t)>, A) : cudaLaunchKernelEx(&at.cfg, route_kernel<PER, decltype(t)>, A);
             return 0;
         });
     });
     if (e != cudaSuccess) return cuda_error(e, "route launch");
-    const LaunchAttrs at2((A.experts + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0, 1, true, s), at3(A.parts, kThreads, 0, 1, true, s);
-    e = cudaLaunchKernelEx(&at2.cfg, scan_kernel, A);
-    if (e == cudaSuccess) e = cudaLaunchKernelEx(&at3.cfg, place_kernel, A);
+    if (one) return DCR_OK;
+    const int th = A.experts <= 512 ? 1024 : 512;
+    const LaunchAttrs at(A.parts, th, place_bytes(th, A.experts), 1, true, s);
+    e = th == 1024 ? cudaLaunchKernelEx(&at.cfg, place_kernel<1024>, A) : cudaLaunchKernelEx(&at.cfg, place_kernel<512>, A);
     return e == cudaSuccess ? DCR_OK : cuda_error(e, "route launch");
 }
 
@@ -705,11 +806,12 @@ extern "C" int dcr_route(const void* logits, uint32_t dtype, uint64_t tokens, ui
     if (!offsets || (tokens && (!logits || !chosen || !weights || !order || !positions || !workspace)))
         return set_error(DCR_ERR_INVALID, "dcr_route: NULL argument");
     if (uintptr_t(logits) % dtype_size(dtype) || uintptr_t(bias) % 4 || uintptr_t(chosen) % 4 || uintptr_t(weights) % 4 ||
-        uintptr_t(offsets) % 4 || uintptr_t(order) % 4 || uintptr_t(positions) % 4 || uintptr_t(workspace) % 4)
+        uintptr_t(offsets) % 4 || uintptr_t(order) % 4 || uintptr_t(positions) % 4 || uintptr_t(workspace) % 16)
         return set_error(DCR_ERR_INVALID, "dcr_route: misaligned buffer");
     RouteArgs A{};
     A.logits = logits, A.bias = bias, A.mask = mask, A.chosen = chosen, A.weights = weights, A.offsets = offsets, A.order = order;
     A.positions = positions, A.counts = static_cast<uint32_t*>(workspace), A.tokens = tokens, A.row_stride = row_stride, A.experts = experts;
+    A.stride = (experts + 3) / 4 * 4;
     A.k = o.k, A.groups = o.groups, A.group_top = o.group_top, A.group_by = o.group_by, A.group_size = experts / o.groups;
     A.sigmoid = o.scoring == DCR_SIGMOID, A.renormalise = o.renormalise != 0, A.scale = o.scale;
     // one group's scores decide in the same order as the logits

@@ -10,7 +10,7 @@ import torch
 from . import OK, check
 from .ops import DTYPES, MAX_EXPERTS, SIGMOID, SOFTMAX, _elsewhere, _fast, _flat, _lib, _matrix, _raw_stream, _refuse, _result_of
 
-MAX_CHOSEN, MAX_GROUPS, ROUTE_PARTS = 32, 32, 304
+MAX_CHOSEN, MAX_GROUPS, ROUTE_PARTS = 32, 32, 152
 SCORINGS = {"softmax": SOFTMAX, "sigmoid": SIGMOID}
 _f32, _i32 = torch.float32, torch.int32
 
@@ -93,7 +93,7 @@ def route_experts(logits, k, scoring="softmax", bias=None, groups=1, group_top=N
     r = Route(torch.empty((tokens, k), dtype=_i32, device=dev), torch.empty((tokens, k), dtype=_f32, device=dev),
               torch.empty(experts + 1, dtype=_i32, device=dev), torch.empty(tokens * k, dtype=_i32, device=dev),
               torch.empty((tokens, k), dtype=_i32, device=dev))
-    work = torch.empty((ROUTE_PARTS + 1) * experts, dtype=_i32, device=dev)
+    work = torch.empty(ROUTE_PARTS * ((experts + 3) // 4 * 4), dtype=_i32, device=dev)
     rc = _library().dcr_route(logits.data_ptr(), t, tokens, experts, stride, pb, pm, ctypes.byref(o), r.experts.data_ptr(),
                               r.weights.data_ptr(), r.offsets.data_ptr(), r.order.data_ptr(), r.positions.data_ptr(), work.data_ptr(),
                               _raw_stream(dev.index))

@@ -186,13 +186,13 @@ int dcr_token_scores_grad(const void* logits, uint32_t dtype, uint64_t rows, uin
  * of expert e are offsets[e] to offsets[e + 1], as dcr_nvfp4_matmul takes
  * them, ordered by token; positions: the row of a slot; order [tokens * k]: the slot
  * (token * k + place) of a row, -1 behind the last.
- * workspace: device, 4-byte aligned, DCR_ROUTE_WORKSPACE(experts) bytes.
+ * workspace: device, 16-byte aligned, DCR_ROUTE_WORKSPACE(experts) bytes.
  * tokens * k < 2^31. */
 enum { DCR_SOFTMAX = 0, DCR_SIGMOID = 1 };
 #define DCR_MAX_CHOSEN 32u
 #define DCR_MAX_GROUPS 32u
-#define DCR_ROUTE_PARTS 304u
-#define DCR_ROUTE_WORKSPACE(experts) (4ull * (DCR_ROUTE_PARTS + 1) * (experts))
+#define DCR_ROUTE_PARTS 152u
+#define DCR_ROUTE_WORKSPACE(experts) (16ull * DCR_ROUTE_PARTS * (((experts) + 3) / 4))
 typedef struct {
     uint32_t scoring, k, groups, group_top, group_by, renormalise;
     float scale;

@@ -193,4 +193,4 @@ def test_header_constants():
     for module, names in ((scores, ["MAX_TOP"]), (experts, ["MAX_CHOSEN", "MAX_GROUPS", "ROUTE_PARTS"]), (adamw, ["ADAMW_BLOCK", "NORM_WORKSPACE"])):
         for n in names:
             assert int(re.search(r"DCR_%s (\d+)u" % n, src).group(1)) == getattr(module, n)
-    assert "#define DCR_ROUTE_WORKSPACE(experts) (4ull * (DCR_ROUTE_PARTS + 1) * (experts))" in src
+    assert "#define DCR_ROUTE_WORKSPACE(experts) (16ull * DCR_ROUTE_PARTS * (((experts) + 3) / 4))" in src
