@@ -531,11 +531,20 @@ struct Range {
     bool operator<(const Range& o) const { return lo < o.lo; }
 };
 
-bool overlapping(std::vector<Range>& r)
+// kinds: the ranges of all weights, of all gradients and so on, each of which
+// a program mostly has in the order of their addresses.
+bool overlapping(std::vector<Range> (&kinds)[7])
 {
-    std::sort(r.begin(), r.end());
+    for (auto& k : kinds)
+        if (!std::is_sorted(k.begin(), k.end())) std::sort(k.begin(), k.end());
+    for (size_t step = 1; step < 7; step *= 2)
+        for (size_t i = 0; i + step < 7; i += 2 * step) {
+            std::vector<Range> both(kinds[i].size() + kinds[i + step].size());
+            std::merge(kinds[i].begin(), kinds[i].end(), kinds[i + step].begin(), kinds[i + step].end(), both.begin());
+            kinds[i].swap(both);
+        }
     uintptr_t read = 0, written = 0;
-    for (const Range& x : r) {
+    for (const Range& x : kinds[0]) {
         if (x.lo < written || (x.out && x.lo < read)) return true;
         uintptr_t& end = x.out ? written : read;
         end = std::max(end, x.hi);
@@ -606,9 +615,9 @@ extern "C" int dcr_adamw(const dcr_adamw_tensor* tensors, uint32_t count, uint32
         return set_error(DCR_ERR_INVALID, "dcr_adamw: misaligned buffer");
     try {
         std::vector<dcr_adamw_tensor> t;
-        std::vector<Range> used;
+        std::vector<Range> used[7];
         t.reserve(count);
-        used.reserve(7 * size_t(count));
+        for (auto& u : used) u.reserve(count);
         uint64_t chunks = 0;
         for (uint32_t i = 0; i < count; ++i) {
             dcr_adamw_tensor x = tensors[i];
@@ -621,16 +630,16 @@ extern "C" int dcr_adamw(const dcr_adamw_tensor* tensors, uint32_t count, uint32
             if (uintptr_t(x.w) % dtype_size(w_dtype) || uintptr_t(x.grad) % dtype_size(grad_dtype) || uintptr_t(x.copy) % cb ||
                 uintptr_t(x.m) % sb || uintptr_t(x.v) % sb || (sb == 1 && (uintptr_t(x.m_scale) % 4 || uintptr_t(x.v_scale) % 4)))
                 return set_error(DCR_ERR_INVALID, "dcr_adamw: tensor %u is misaligned", i);
-            auto use = [&](const void* p, uint64_t bytes, bool out) { used.push_back(Range{uintptr_t(p), uintptr_t(p) + bytes, out}); };
-            use(x.w, x.n * dtype_size(w_dtype), true);
-            use(x.grad, x.n * dtype_size(grad_dtype), false);
-            use(x.m, x.n * sb, true);
-            use(x.v, x.n * sb, true);
-            if (copy_dtype != DCR_NONE) use(x.copy, x.n * cb, true);
+            auto use = [&](int kind, const void* p, uint64_t bytes, bool out) { used[kind].push_back(Range{uintptr_t(p), uintptr_t(p) + bytes, out}); };
+            use(0, x.w, x.n * dtype_size(w_dtype), true);
+            use(1, x.grad, x.n * dtype_size(grad_dtype), false);
+            use(2, x.m, x.n * sb, true);
+            use(3, x.v, x.n * sb, true);
+            if (copy_dtype != DCR_NONE) use(4, x.copy, x.n * cb, true);
             if (sb == 1) {
                 const uint64_t blocks = (x.n + kBlock - 1) / kBlock;
-                use(x.m_scale, blocks * 4, true);
-                use(x.v_scale, blocks * 4, true);
+                use(5, x.m_scale, blocks * 4, true);
+                use(6, x.v_scale, blocks * 4, true);
             }
             chunks += (x.n + kRound - 1) / kRound;
             t.push_back(x);

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const ExchangeArgs A, 
 }
 
 template <typename TI, typename TO, bool VEC>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const ExchangeArgs A, uint32_t team, uint32_t pieces, uint32_t piece)
+__global__ void __launch_bounds__(kThreads, 8) combine_kernel(const ExchangeArgs A, uint32_t team, uint32_t pieces, uint32_t piece)
 {
     const Place P(A, team, pieces, piece);
     if (P.token >= A.tokens) return;

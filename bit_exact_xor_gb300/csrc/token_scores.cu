@@ -41,9 +41,9 @@ struct ScoreArgs {
     float sc_dn, sc_lo;   // the same rounded down, and the (positive) rest
 };
 
-constexpr int kWords = 8;          // words of a chunk
+constexpr int kWords = 6;          // words of a chunk
 constexpr uint32_t kBuckets = 16;  // chunk maxima that a thread keeps
-constexpr uint32_t kList = 1024;   // values that are sorted
+constexpr uint32_t kList = 512;    // values that are sorted
 constexpr int kMaxBlocks = 8;      // of a cluster
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -60,32 +60,57 @@ struct Sums {
     float s, t;
 };
 
-// CLAMP: where a value is -inf, or left out as if it were.
-template <bool PLAIN, bool CLAMP, int N>
+// Two multiply-adds, or sums, in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 r;
+    asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7}; fma.rn.f32x2 z, x, y, z; mov.b64 {%0, %1}, z; }"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{ .reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// The sums of a chunk without -inf and not far from 0.
+template <typename T>
+__device__ __forceinline__ Sums plain_sums(const uint4 (&q)[kWords], const Exponent& e)
+{
+    float2 s = both(0.0f), t = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+        float v[Word<T>::kN];
+        Word<T>::values(q[i], v);
+#pragma unroll
+        for (int j = 0; j < Word<T>::kN; j += 2) {
+            const float2 x = make_float2(v[j], v[j + 1]), d = fma2(x, both(e.lo), fma2(x, both(e.sc), both(-e.msc)));
+            const float2 p = make_float2(exp2_fast(d.x), exp2_fast(d.y));
+            s = add2(s, p);
+            t = fma2(p, d, t);
+        }
+    }
+    return {s.x + s.y, t.x + t.y};
+}
+
+// The same, where a value may be -inf, or left out as if it were, one by one.
+template <bool PLAIN, int N>
 __device__ __forceinline__ void add_values(Sums& a, const float (&v)[N], const Exponent& e)
 {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        float d = PLAIN ? fmaf(v[i], e.lo, fmaf(v[i], e.sc, -e.msc)) : fmaf(v[i] - e.m, e.lo, (v[i] - e.m) * e.sc);
+        const float x = PLAIN ? fmaf(v[i], e.lo, fmaf(v[i], e.sc, -e.msc)) : fmaf(v[i] - e.m, e.lo, (v[i] - e.m) * e.sc);
         // -200: exp of it is 0, and so is its product with it, which with -inf would not be a number
-        if (CLAMP) d = max_nan(d, -200.0f);
-        const float p = exp2_fast(d);
+        const float d = max_nan(x, -200.0f), p = exp2_fast(d);
         a.s += p;
         a.t = fmaf(p, d, a.t);
     }
-}
-
-template <typename T, bool PLAIN, bool CLAMP, int NV>
-__device__ __forceinline__ Sums add_words(const uint4 (&q)[NV], const Exponent& e)
-{
-    Sums a = {0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        float v[Word<T>::kN];
-        Word<T>::values(q[i], v);
-        add_values<PLAIN, CLAMP>(a, v, e);
-    }
-    return a;
 }
 
 // What every exponent has too much is taken out of the sums.
@@ -111,8 +136,8 @@ __device__ __forceinline__ Sums chunk_sums_below(const uint4 (&q)[NV], float m, 
             if (v[j] == m) count += 1.0f;
             v[j] = v[j] == m ? -INFINITY : v[j];
         }
-        if (e.plain) add_values<true, true>(a, v, e);
-        else add_values<false, true>(a, v, e);
+        if (e.plain) add_values<true>(a, v, e);
+        else add_values<false>(a, v, e);
     }
     correct(a, e);
     return a;
@@ -217,8 +242,8 @@ __device__ __noinline__ Sums rare_sums(const T* x, uint32_t vocab, uint32_t rank
         float v[Word<T>::kN];
         Word<T>::values(q, v);
         nan |= word_nan<T>(q);
-        if (e.plain) add_values<true, true>(a, v, e);
-        else add_values<false, true>(a, v, e);
+        if (e.plain) add_values<true>(a, v, e);
+        else add_values<false>(a, v, e);
     }
     if (fabsf(m) == INFINITY) {
         a.s = a.t = nan ? NAN : 0.0f;
@@ -237,6 +262,7 @@ struct TopMemory {
     uint64_t part[TH / 32];
     uint32_t bound[TH / 32];
     uint32_t count, buckets, scan[TH / 32];
+    uint64_t lists[kMaxBlocks * DCR_MAX_TOP];   // in the cluster's first block: all blocks' best
 };
 
 // The n largest of list[0..count) to best.
@@ -258,14 +284,14 @@ template <int TH>
 __device__ __forceinline__ void merge_lists(TopMemory<TH>& M, uint32_t lists, uint32_t n)
 {
     for (uint32_t i = threadIdx.x; i < lists * n; i += TH) {
-        const uint64_t mine = M.list[i];
+        const uint64_t mine = M.lists[i];
         uint32_t above = i % n;
         for (uint32_t l = 0; l < lists; ++l) {
             if (l == i / n) continue;
             uint32_t lo = 0, hi = n;        // the first that is not larger
             while (lo < hi) {
                 const uint32_t mid = (lo + hi) / 2;
-                if (M.list[l * n + mid] > mine) lo = mid + 1;
+                if (M.lists[l * n + mid] > mine) lo = mid + 1;
                 else hi = mid;
             }
             above += lo;
@@ -274,67 +300,85 @@ __device__ __forceinline__ void merge_lists(TopMemory<TH>& M, uint32_t lists, ui
     }
 }
 
-// The n largest of the block's share to best, sorted.  mine: the thread's maximum.
-template <typename T, int TH>
-__device__ void find_top(TopMemory<TH>& M, const Share<T>& S, float mine, uint32_t n)
+// Before a barrier: a warp's part of the bound, which at least ceil(n / W) of
+// its lanes' maxima reach.
+template <int TH>
+__device__ __forceinline__ void start_top(TopMemory<TH>& M, float mine, uint32_t n)
 {
-    constexpr uint32_t W = TH / 32;
-    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    // the bound: in each warp at least ceil(n / W) lanes' maxima reach it
+    const uint32_t lane = threadIdx.x % 32;
     uint32_t left = order_of(mine), most = 0;
-    for (uint32_t i = 0; i < (n + W - 1) / W; ++i) {
+    for (uint32_t i = 0; i < (n + TH / 32 - 1) / (TH / 32); ++i) {
         most = __reduce_max_sync(~0u, left);
         const uint32_t who = __ballot_sync(~0u, left == most);
         if (lane == __ffs(who) - 1) left = 0;
     }
-    if (lane == 0) M.bound[warp] = most;
+    if (lane == 0) M.bound[threadIdx.x / 32] = most;
     if (threadIdx.x == 0) M.count = M.buckets = 0;
     if (threadIdx.x < n) M.best[threadIdx.x] = 0;
-    __syncthreads();
+}
+
+template <int TH>
+__device__ __forceinline__ uint32_t bound_of(const TopMemory<TH>& M)
+{
     uint32_t bound = M.bound[0];
-    for (uint32_t i = 1; i < W; ++i) bound = min(bound, M.bound[i]);
-    // values of at least this order to the list.  The buckets that hold some are listed first, so that their words are shared
-    // out among all threads.
-    auto collect = [&](uint32_t least) {
-        for (uint32_t b = 0; b < min(S.chunks, kBuckets); ++b)
-            if (order_of(M.chunk_max[b][threadIdx.x]) >= least) M.bucket[atomicAdd(&M.buckets, 1u)] = uint16_t(b * TH + threadIdx.x);
-        __syncthreads();
-        const uint32_t words = M.buckets * kWords;
-        for (uint32_t i = threadIdx.x; i < words; i += TH) {
-            const uint32_t from = M.bucket[i / kWords], thread = from % TH;
-            for (uint32_t c = from / TH; c < S.chunks; c += kBuckets) {
-                const uint32_t k = S.first - threadIdx.x + thread + (c * kWords + i % kWords) * S.step;
-                S.each(S.in.load(k), k, [&](float v, uint32_t at) {
-                    if (order_of(v) >= least) {
-                        const uint32_t p = atomicAdd(&M.count, 1u);   // where a value stands in the list does not matter
-                        if (p < kList) M.list[p] = key_of(v, at);
-                    }
-                });
-            }
+#pragma unroll
+    for (uint32_t i = 1; i < TH / 32; ++i) bound = min(bound, M.bound[i]);
+    return bound;
+}
+
+// The buckets that hold a value of at least this order, so that their words
+// can be shared out among all threads.
+template <typename T, int TH>
+__device__ __forceinline__ void list_buckets(TopMemory<TH>& M, const Share<T>& S, uint32_t least)
+{
+    for (uint32_t b = 0; b < min(S.chunks, kBuckets); ++b)
+        if (order_of(M.chunk_max[b][threadIdx.x]) >= least) M.bucket[atomicAdd(&M.buckets, 1u)] = uint16_t(b * TH + threadIdx.x);
+}
+
+// The values of at least this order of the buckets listed, to the list; where
+// a value stands there does not matter.
+template <typename T, int TH>
+__device__ __forceinline__ void list_values(TopMemory<TH>& M, const Share<T>& S, uint32_t least)
+{
+    const uint32_t words = M.buckets * kWords;
+    for (uint32_t i = threadIdx.x; i < words; i += TH) {
+        const uint32_t from = M.bucket[i / kWords];
+        for (uint32_t c = from / TH; c < S.chunks; c += kBuckets) {
+            const uint32_t k = S.first - threadIdx.x + from % TH + (c * kWords + i % kWords) * S.step;
+            S.each(S.in.load(k), k, [&](float v, uint32_t at) {
+                if (order_of(v) >= least) {
+                    const uint32_t p = atomicAdd(&M.count, 1u);
+                    if (p < kList) M.list[p] = key_of(v, at);
+                }
+            });
         }
-    };
-    collect(bound);
-    __syncthreads();
-    uint32_t count = M.count;
-    if (count >= n && count <= kList) {
-        sort_list(M, count, n);
-        __syncthreads();
-        return;
     }
-    bool done = false;
+}
+
+// The n largest of the block's share to best, sorted, where the list does not
+// hold all that reach the bound, or fewer than n do.
+template <typename T, int TH>
+__device__ __noinline__ void search_top(TopMemory<TH>& M, const T* x, uint32_t vocab, uint32_t rank, uint32_t blocks, uint32_t n)
+{
+    constexpr uint32_t W = TH / 32;
+    const Share<T> S(x, vocab, rank, blocks);
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32, bound = bound_of(M);
+    uint32_t count = M.count;
+    __syncthreads();
     if (count > kList) {
         // more than the list holds: those above the bound, then the first that are equal to it
-        __syncthreads();
         if (threadIdx.x == 0) M.count = M.buckets = 0;
         __syncthreads();
-        collect(bound + 1);
+        list_buckets(M, S, bound + 1);
+        __syncthreads();
+        list_values(M, S, bound + 1);
         __syncthreads();
         count = M.count;
         if (count <= kList - DCR_MAX_TOP) {
             uint32_t need = count < n ? n - count : 0, at = count;
             for (uint32_t k = S.first; need && k - threadIdx.x < S.in.words; k += S.step) {
                 // all threads go through words of one stride at a time, in the order of the indexes
-                uint4 q = S.in.load(k);
+                const uint4 q = S.in.load(k);
                 uint32_t equal = 0;
                 S.each(q, k, [&](float v, uint32_t) { equal += order_of(v) == bound; });
                 uint32_t before = equal;
@@ -360,12 +404,13 @@ __device__ void find_top(TopMemory<TH>& M, const Share<T>& S, float mine, uint32
             }
             __syncthreads();
             sort_list(M, at, n);
-            done = true;
+            __syncthreads();
+            return;
         }
     }
-    // fewer than n numbers in the share, or more than the list holds in another way: the largest, n times
+    // the largest, n times
     uint64_t last = ~0ull;
-    for (uint32_t i = 0; i < n && !done; ++i) {
+    for (uint32_t i = 0; i < n; ++i) {
         uint64_t best = 0;
         for (uint32_t c = 0; c < S.chunks; ++c)
             S.each_of_chunk(c, [&](float v, uint32_t at) {
@@ -385,33 +430,26 @@ __device__ void find_top(TopMemory<TH>& M, const Share<T>& S, float mine, uint32
     __syncthreads();
 }
 
-// A value of another block's shared memory.
-template <typename V>
-__device__ __forceinline__ V remote(const V* p, uint32_t rank)
+// A word, or four, into the shared memory of the cluster's first block.
+__device__ __forceinline__ void to_first(const void* p, uint64_t v)
 {
-    static_assert(sizeof(V) == 4 || sizeof(V) == 8, "one word");
-    uint32_t at = uint32_t(__cvta_generic_to_shared(p));
-    asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(rank));
-    if constexpr (sizeof(V) == 4) {
-        uint32_t r;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
-        V v;
-        memcpy(&v, &r, 4);
-        return v;
-    } else {
-        uint64_t r;
-        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(r) : "r"(at) : "memory");
-        return V(r);
-    }
+    asm volatile("{ .reg .b32 a; mapa.shared::cluster.u32 a, %0, 0; st.shared::cluster.u64 [a], %1; }" ::"r"(uint32_t(__cvta_generic_to_shared(p))), "l"(v)
+                 : "memory");
 }
-__device__ __forceinline__ void cluster_barrier() { asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ void to_first(const void* p, const Part& v)
+{
+    asm volatile("{ .reg .b32 a; mapa.shared::cluster.u32 a, %0, 0; st.shared::cluster.v4.f32 [a], {%1, %2, %3, %4}; }" ::"r"(
+                     uint32_t(__cvta_generic_to_shared(p))),
+                 "f"(v.m), "f"(v.count), "f"(v.s), "f"(v.t)
+                 : "memory");
+}
 
 template <typename T, int TH, bool TOP>
-__global__ void __launch_bounds__(TH, 768 / TH) scores_kernel(ScoreArgs A, uint32_t cluster)
+__global__ void __launch_bounds__(TH, 1024 / TH) scores_kernel(ScoreArgs A, uint32_t cluster)
 {
     constexpr uint32_t W = TH / 32;
-    __shared__ float4 parts[W];
-    __shared__ float4 whole;
+    __shared__ float warp_max_of[W];
+    __shared__ float4 parts[W], blocks[kMaxBlocks];
     __shared__ TopMemory<TOP ? TH : 32> top_memory;
     const uint32_t rank = cluster > 1 ? blockIdx.x % cluster : 0, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const uint64_t row = blockIdx.x / cluster;
@@ -429,7 +467,9 @@ __global__ void __launch_bounds__(TH, 768 / TH) scores_kernel(ScoreArgs A, uint3
         }
         return;
     }
-    const float xy = to_f32(x[token]);
+    // another block's shared memory may be written once that block is known to run: all say so here, and wait for it at the
+    // end of their work
+    if (cluster > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     const Share<T> S(x, vocab, rank, cluster);
     // top: the sums over the chunk that the maximum m comes from (`at`); rest: those over the others
     float m = -INFINITY;
@@ -456,21 +496,26 @@ __global__ void __launch_bounds__(TH, 768 / TH) scores_kernel(ScoreArgs A, uint3
             top = {0.0f, 0.0f}, m = cm, at = c;
         }
         const Exponent e(m, A.sc_dn, A.sc_lo);
-        Sums a = add_words<T, true, false>(q, e);
+        Sums a = plain_sums<T>(q, e);
         // not a number where a value is -inf or none itself
         if (!(fabsf(a.t) < INFINITY) || !e.plain) a = rare_sums<T>(x, vocab, rank, cluster, c, m, A.sc_dn, A.sc_lo);
         else correct(a, e);
         if (higher) top = a;
         else rest.s += a.s, rest.t += a.t;
     }
+    const float xy = to_f32(x[token]);      // there by the time that the sums are
     // the row's maximum in this block, and which threads have it
-    float bm = m;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, o));
-    if (lane == 0) parts[warp].x = bm;
+    float bm = value_of(__reduce_max_sync(~0u, order_of(m)));
+    if (lane == 0) warp_max_of[warp] = bm;
+    if constexpr (TOP) start_top(top_memory, m, A.top);
     __syncthreads();
 #pragma unroll
-    for (uint32_t i = 0; i < W; ++i) bm = fmaxf(bm, parts[i].x);
+    for (uint32_t i = 0; i < W; ++i) bm = fmaxf(bm, warp_max_of[i]);
+    uint32_t bound = 0;
+    if constexpr (TOP) {
+        bound = bound_of(top_memory);
+        list_buckets(top_memory, S, bound);
+    }
     Part p = {m, 0.0f, rest.s + top.s, rest.t + top.t}, all = {bm, 0.0f, 0.0f, 0.0f};
     if (m == bm && m != -INFINITY) {
         // the chunk of the maximum again, without what is equal to it
@@ -486,33 +531,38 @@ __global__ void __launch_bounds__(TH, 768 / TH) scores_kernel(ScoreArgs A, uint3
         all.s += __shfl_xor_sync(~0u, all.s, o);
         all.t += __shfl_xor_sync(~0u, all.t, o);
     }
-    __syncthreads();
     if (lane == 0) parts[warp] = make_float4(bm, all.count, all.s, all.t);
-    if constexpr (TOP) find_top<T, TH>(top_memory, S, m, A.top);
-    else __syncthreads();
+    __syncthreads();
+    if constexpr (TOP) {
+        list_values(top_memory, S, bound);
+        __syncthreads();
+        const uint32_t count = top_memory.count;
+        if (count >= A.top && count <= kList) {
+            sort_list(top_memory, count, A.top);
+            __syncthreads();
+        } else {
+            search_top<T, TH>(top_memory, x, vocab, rank, cluster, A.top);
+        }
+    }
     all = {bm, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (uint32_t i = 0; i < W; ++i) all.count += parts[i].y, all.s += parts[i].z, all.t += parts[i].w;
     if (cluster > 1) {
-        if (threadIdx.x == 0) whole = make_float4(all.m, all.count, all.s, all.t);
-        cluster_barrier();      // every block of the cluster runs, and has written what the first one reads
+        asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        if (threadIdx.x == 0) to_first(&blocks[rank], all);
+        if constexpr (TOP) {
+            if (threadIdx.x < A.top) to_first(&top_memory.lists[rank * A.top + threadIdx.x], top_memory.best[threadIdx.x]);
+        }
+        asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
         if (rank == 0) {
-            Part b[kMaxBlocks];
-            for (uint32_t i = 0; i < cluster; ++i) {
-                b[i] = {remote(&whole.x, i), remote(&whole.y, i), remote(&whole.z, i), remote(&whole.w, i)};
-                bm = fmaxf(bm, b[i].m);
-            }
+            for (uint32_t i = 0; i < cluster; ++i) bm = fmaxf(bm, blocks[i].x);
             all = {bm, 0.0f, 0.0f, 0.0f};
-            for (uint32_t i = 0; i < cluster; ++i) all.add(b[i], A.sc);
+            for (uint32_t i = 0; i < cluster; ++i) all.add({blocks[i].x, blocks[i].y, blocks[i].z, blocks[i].w}, A.sc);
             if constexpr (TOP) {
-                const uint32_t n = cluster * A.top;
-                for (uint32_t i = threadIdx.x; i < n; i += TH) top_memory.list[i] = remote(&top_memory.best[i % A.top], i / A.top);
-                __syncthreads();     // also: this block's own part of best is read
-                merge_lists(top_memory, cluster, A.top);
+                merge_lists(top_memory, cluster, A.top);     // all have read best
                 __syncthreads();
             }
         }
-        cluster_barrier();      // what the first block reads stays until it has
     }
     if (rank != 0) return;
     const float r = bm == INFINITY && all.s == all.s ? 0.0f : all.s + (all.count - 1.0f);
@@ -624,8 +674,8 @@ int scores_launch(const ScoreArgs& A, uint32_t cluster, cudaStream_t s)
 
 // Blocks of 128 or 256 threads, and one to eight of them for a row, whichever
 // the model of a launch finds fastest: rounds of as many blocks as fit at once
-// (768 threads an SM), each the time of its chunks, which is DRAM's for what
-// the SMs then have in flight (15 MB when full) or a load's latency, and the
+// (1024 threads an SM), each the time of its chunks, which is DRAM's for what
+// the SMs then have in flight (16 MB when full) or a load's latency, and the
 // steps at its end, which take longer where blocks have to meet.  (1021 rows
 // of 32771 f32 values: blocks of 256 leave a second round half empty.)
 template <typename T>
@@ -636,9 +686,9 @@ int scores_launch(const ScoreArgs& A, cudaStream_t s)
     double best = 1e300;
     for (uint32_t th = 128; th <= 256; th *= 2)
         for (uint32_t c = 1; c <= uint32_t(kMaxBlocks) && (c == 1 || words >= uint64_t(c) * th); c *= 2) {
-            const double slots = 152.0 * 768 / th, blocks = double(A.rows) * c, rounds = std::ceil(blocks / slots);
+            const double slots = 152.0 * 1024 / th, blocks = double(A.rows) * c, rounds = std::ceil(blocks / slots);
             const double chunks = std::ceil(double(words) / (c * th * kWords));
-            const double us = rounds * (chunks * std::max(1.0, 2.4 * std::min(1.0, blocks / slots)) + 4.0 + (c > 1 ? 2.0 : 0.0));
+            const double us = rounds * (chunks * std::max(1.0, 0.39 * kWords * std::min(1.0, blocks / slots)) + 4.0 + (c > 1 ? 2.0 : 0.0));
             if (us < best) best = us, threads = th, cluster = c;
         }
     return threads == 128 ? scores_launch<T, 128>(A, cluster, s) : scores_launch<T, 256>(A, cluster, s);

@@ -271,3 +271,21 @@ def test_streams_and_graphs():
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert torch.equal(back, dcr.token_scores_grad(into, tokens, want.stats, one, one))
     assert torch.equal(dcr.token_scores_grad(z, tokens, exp.stats, one, one), grad)
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(2, 140001, "bf16"), (40, 70001, "f32"), (150, 33001, "f32")])
+def test_clusters_that_come_and_go(rows, vocab, dtype):
+    # rows of several blocks, most of them left out and gone at once, on two streams: each block's part reaches the first one
+    z, tokens = _rows(rows, vocab, dtype, 2)
+    every = dcr.token_scores(z.cuda(), tokens.cuda(), top=20)
+    some = torch.where(torch.arange(rows) % 3 == 1, torch.full_like(tokens, -1), tokens).cuda()
+    dev = z.cuda()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [dcr.token_scores(dev, some, top=20, stream=streams[i % 2]) for i in range(6)]
+    torch.cuda.synchronize()
+    keep = (some >= 0).nonzero()[:, 0]
+    for g in got:
+        assert all(torch.equal(a[keep], b[keep]) for a, b in zip(g, every))
+    exp = torch.sort(z.float(), dim=1, descending=True, stable=True)[1][:, :20]
+    assert torch.equal(every.top_tokens.cpu(), exp)

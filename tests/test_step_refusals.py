@@ -194,3 +194,12 @@ def test_header_constants():
         for n in names:
             assert int(re.search(r"DCR_%s (\d+)u" % n, src).group(1)) == getattr(module, n)
     assert "#define DCR_ROUTE_WORKSPACE(experts) (16ull * DCR_ROUTE_PARTS * (((experts) + 3) / 4))" in src
+
+
+def test_no_block_reaches_into_another_before_the_cluster_runs():
+    # every write to another block's shared memory comes behind a wait of the cluster's barrier, and another one follows it
+    src = open(os.path.join(os.path.dirname(ops.__file__), "csrc", "token_scores.cu")).read()
+    body = re.sub(r"//[^\n]*", "", src).split("scores_kernel(ScoreArgs A, uint32_t cluster)", 1)[1]
+    first, last = body.index("to_first("), body.rindex("to_first(")
+    assert body.index("barrier.cluster.arrive.relaxed") < body.index("barrier.cluster.wait.acquire") < first
+    assert "barrier.cluster.arrive.release;\\nbarrier.cluster.wait.acquire" in body[last:]
