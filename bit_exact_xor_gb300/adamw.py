@@ -137,6 +137,8 @@ def adamw_step(weights, grads, states, step, lr, betas=(0.9, 0.999), eps=1e-8, w
     from grad_norm) and max_norm gradients are scaled down to that norm, and a
     norm that is not finite leaves the whole step out.  seed: for the rounding
     of 8-bit moments."""
+    if max_norm is not None and not max_norm > 0:
+        _refuse("max_norm must be positive")
     kind = type(states[0]) if states.__class__ is list and states else None
     if stream is None and (kind is AdamState32 or kind is AdamState8):
         r = _fast.adamw(weights, grads, states, 32 if kind is AdamState32 else 8, copies, norm, step, lr, betas[0], betas[1], eps, weight_decay,

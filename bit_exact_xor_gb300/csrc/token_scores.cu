@@ -685,7 +685,7 @@ int scores_launch(const ScoreArgs& A, cudaStream_t s)
     uint32_t threads = 128, cluster = 1;
     double best = 1e300;
     for (uint32_t th = 128; th <= 256; th *= 2)
-        for (uint32_t c = 1; c <= uint32_t(kMaxBlocks) && (c == 1 || words >= uint64_t(c) * th); c *= 2) {
+        for (uint32_t c = 1; c <= uint32_t(kMaxBlocks) && (c == 1 || (words >= uint64_t(c) * th && A.rows < 1u << 20)); c *= 2) {
             const double slots = 152.0 * 1024 / th, blocks = double(A.rows) * c, rounds = std::ceil(blocks / slots);
             const double chunks = std::ceil(double(words) / (c * th * kWords));
             const double us = rounds * (chunks * std::max(1.0, 0.39 * kWords * std::min(1.0, blocks / slots)) + 4.0 + (c > 1 ? 2.0 : 0.0));

@@ -182,7 +182,8 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
     for call in (lambda: dcr.token_scores(x, t), lambda: dcr.token_scores_grad(x, t, x), lambda: dcr.route_experts(x, 2),
                  lambda: dcr.route_experts_grad(x, r, x), lambda: dcr.experts_gather(x, r), lambda: dcr.experts_combine(x, r),
                  lambda: dcr.experts_combine_grad(x, r, x), lambda: dcr.grad_norm([x]), lambda: dcr.grad_norm([]), lambda: dcr.adamw_states([x], 16),
-                 lambda: dcr.adamw_step([x], [x], [dcr.AdamState32(x, x)], 1, 1e-3), lambda: dcr.adamw_step([], [], [], 1, 1e-3)):
+                 lambda: dcr.adamw_step([x], [x], [dcr.AdamState32(x, x)], 1, 1e-3),
+                 lambda: dcr.adamw_step([x], [x], [dcr.AdamState32(x, x)], 1, 1e-3, norm=x, max_norm=0.0), lambda: dcr.adamw_step([], [], [], 1, 1e-3)):
         with pytest.raises(dcr.DcrError) as e:
             call()
         assert e.value.code == dcr.ERR_INVALID
