@@ -92,10 +92,13 @@ __device__ __forceinline__ V sigmoid_of(V x)
     return (x < V(0) ? e : V(1)) / (V(1) + e);
 }
 
-// The same to two units more, for keys.
+// The same for keys, off by at most 7 units of 2^-24: e = exp(-|x|) is off by 4
+// and 1.5 |x| units of itself (the approximation's 2 and a rounded product),
+// which s (1 - s) turns into one at most; the sum's 1, the quotient's 4.
 __device__ __forceinline__ float key_sigmoid(float x)
 {
-    const float e = expf(-fabsf(x));
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fabsf(x) * -1.44269504f));
     return __fdividef(x < 0.0f ? e : 1.0f, 1.0f + e);
 }
 __device__ __forceinline__ double key_sigmoid(double x) { return sigmoid_of(x); }
@@ -111,9 +114,9 @@ __device__ __forceinline__ V below(V x, V m)
 __device__ __forceinline__ float bias_of(const RouteArgs& A, int32_t e) { return A.bias ? A.bias[e] : 0.0f; }
 
 // How far keys of 32 bits may be off: the error of a score in units of 2^-24
-// (the exponential's 4, a sum's and a quotient's 4; for softmax those of up to
-// 37 additions and of a difference of up to 60 from the maximum, too) for
-// both of two neighbours, and half a unit of s + bias.
+// (key_sigmoid's 7, taken as 10; for softmax the exponential's 4, a product's 1,
+// those of up to 37 additions and of a difference of up to 60 from the maximum)
+// for both of two neighbours, and half a unit of s + bias.
 struct Slack {
     float score;
     __device__ __forceinline__ Slack(bool sigmoid, float most) : score(0x1p-24f * (sigmoid ? 20.0f : 256.0f) * most) {}
@@ -230,10 +233,10 @@ __device__ __noinline__ uint32_t settle_groups(const T* row, const RouteArgs& A,
 }
 
 // The orders of all experts' keys, of type V; 0 for those that cannot be
-// chosen, and for those of groups that are not taken.  most: the largest
-// score.
+// chosen, and for those of groups that are not taken.  bias: of PER * 32
+// experts, in shared memory; most: the largest score.
 template <int PER, typename T, typename V, typename O>
-__device__ __forceinline__ void keys_of(const T* row, const float (&x)[PER], const float (&bias)[PER], const RouteArgs& A, O (&key)[PER], float& most)
+__device__ __forceinline__ void keys_of(const T* row, const float (&x)[PER], const float* bias, const RouteArgs& A, O (&key)[PER], float& most)
 {
     constexpr bool k32 = sizeof(V) == 4;
     const uint32_t lane = threadIdx.x % 32, first = lane * PER;
@@ -256,7 +259,7 @@ __device__ __forceinline__ void keys_of(const T* row, const float (&x)[PER], con
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const V v = (A.sigmoid ? key_sigmoid(V(x[i])) : below(V(x[i]), m) * inv) + V(bias[i]);
+            const V v = (A.sigmoid ? key_sigmoid(V(x[i])) : below(V(x[i]), m) * inv) + V(bias[first + i]);
             key[i] = x[i] > -INFINITY ? order_of(v) : O(0);
         }
     }
@@ -330,14 +333,12 @@ __device__ __forceinline__ void keys_of(const T* row, const float (&x)[PER], con
 // The k best experts by keys of 64 bits, one after another: lane j's is the
 // j-th (-1: none).  Apart, so that its registers do not weigh on the others.
 template <int PER, typename T>
-__device__ __noinline__ int32_t choose_again(const T* row, const RouteArgs& A)
+__device__ __noinline__ int32_t choose_again(const T* row, const float* bias, const RouteArgs& A)
 {
     const uint32_t lane = threadIdx.x % 32, first = lane * PER;
-    float x[PER], bias[PER], most;
+    float x[PER], most;
     uint64_t key[PER];
     load_row<PER, T>(row, A.experts, x);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) bias[i] = first + i < A.experts ? bias_of(A, first + i) : 0.0f;
     keys_of<PER, T, double>(row, x, bias, A, key, most);
     int32_t mine = -1;
     for (uint32_t r = 0; r < A.k; ++r) {
@@ -363,7 +364,7 @@ __device__ __noinline__ int32_t choose_again(const T* row, const RouteArgs& A)
 // The k best experts: lane j's is the j-th (-1: none).  list: 32 entries of
 // the warp's own.
 template <int PER, typename T>
-__device__ __forceinline__ int32_t choose(const float (&x)[PER], const float (&bias)[PER], const T* row, const RouteArgs& A, uint64_t* list)
+__device__ __forceinline__ int32_t choose(const float (&x)[PER], const float* bias, const T* row, const RouteArgs& A, uint64_t* list)
 {
     const uint32_t lane = threadIdx.x % 32, first = lane * PER;
     uint32_t key[PER];
@@ -395,7 +396,7 @@ __device__ __forceinline__ int32_t choose(const float (&x)[PER], const float (&b
         if (in && at < 32) list[at] = uint64_t(key[i]) << 32 | (0xFFFFFFFFu - (first + i));    // the lower expert above
         n += __popc(all);
     }
-    if (n > 32) return choose_again<PER, T>(row, A);
+    if (n > 32) return choose_again<PER, T>(row, bias, A);
     __syncwarp();
     uint64_t mine = lane < n ? list[lane] : 0;
     uint32_t rank = 0;
@@ -452,19 +453,35 @@ __device__ __forceinline__ void softmax_of(const float (&x)[PER], float& m, floa
     total = warp_sum(total);
 }
 
-// A token by a warp, whose row x holds; its experts are counted in `counts`.
-template <int PER, typename T>
-__device__ __forceinline__ int32_t route_token(const RouteArgs& A, uint64_t token, const float (&x)[PER], const float (&bias)[PER], uint64_t* list, uint32_t* counts)
+// What the warps of a block that route tokens share.
+template <int PER, int TH>
+struct RouteMemory {
+    float bias[PER * 32];
+    uint64_t lists[TH / 32][32];
+    __device__ __forceinline__ void fill(const RouteArgs& A)
+    {
+        for (uint32_t e = threadIdx.x; e < PER * 32; e += TH) bias[e] = e < A.experts ? bias_of(A, e) : 0.0f;
+    }
+};
+
+// A token by a warp; its experts are counted in `counts`.  Returns lane j's.
+template <int PER, typename T, int TH>
+__device__ __forceinline__ int32_t route_token(const RouteArgs& A, uint64_t token, RouteMemory<PER, TH>& M, uint32_t* counts)
 {
     const uint32_t lane = threadIdx.x % 32;
     const T* row = static_cast<const T*>(A.logits) + token * A.row_stride;
     Slot c = {-1, 0.0f};
     float w = 0.0f;
+    float x[PER];
+    load_row<PER, T>(row, A.experts, x);
     if (!A.mask || A.mask[token]) {
-        c.expert = choose<PER, T>(x, bias, row, A, list);
+        c.expert = choose<PER, T>(x, M.bias, row, A, M.lists[threadIdx.x / 32]);
         if (c.expert >= 0) c.logit = to_f32(row[c.expert]);
         float m = 0.0f, total = 1.0f;
-        if (!A.sigmoid && !A.renormalise) softmax_of(x, m, total);
+        if (!A.sigmoid && !A.renormalise) {
+            load_row<PER, T>(row, A.experts, x);    // again: kept, it would take registers from the choice
+            softmax_of(x, m, total);
+        }
         w = weight_of(c, A.sigmoid, A.renormalise, m, total) * A.scale;
     }
     if (lane < A.k) {
@@ -473,26 +490,6 @@ __device__ __forceinline__ int32_t route_token(const RouteArgs& A, uint64_t toke
         if (c.expert >= 0) atomicAdd(&counts[c.expert], 1u);
     }
     return c.expert;
-}
-
-// Tokens begin, begin + step, ... of a warp; a row is loaded while the one
-// before it is decided.
-template <int PER, typename T, typename F>
-__device__ __forceinline__ void route_tokens(const RouteArgs& A, uint64_t begin, uint64_t end, uint32_t step, uint64_t (*lists)[32], uint32_t* counts, F each)
-{
-    float bias[PER], next[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) bias[i] = 0.0f;
-    if (A.bias) load_row<PER, float>(A.bias, A.experts, bias, 0.0f);
-    const T* rows = static_cast<const T*>(A.logits);
-    if (begin < end) load_row<PER, T>(rows + begin * A.row_stride, A.experts, next);
-    for (uint64_t t = begin; t < end; t += step) {
-        float x[PER];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) x[i] = next[i];
-        if (t + step < end) load_row<PER, T>(rows + (t + step) * A.row_stride, A.experts, next);
-        each(t, route_token<PER, T>(A, t, x, bias, lists[threadIdx.x / 32], counts));
-    }
 }
 
 // Exclusive sums of v[0..n) in place, by a whole block; returns the total.
@@ -578,19 +575,20 @@ constexpr int kThreads = 256;
 constexpr uint32_t kMaxParts = DCR_ROUTE_PARTS;
 // Threads of a block: as many as have the registers that lanes with PER experts take.
 template <int PER>
-constexpr int kRouteThreads = PER <= 4 ? 1024 : PER == 8 ? 768 : 512;
+constexpr int kRouteThreads = PER <= 8 ? 1024 : 512;
 
 template <int PER, typename T>
 __global__ void __launch_bounds__(kRouteThreads<PER>) route_kernel(const RouteArgs A)
 {
     constexpr int TH = kRouteThreads<PER>;
     __shared__ uint32_t counts[PER * 32];
-    __shared__ uint64_t lists[TH / 32][32];
+    __shared__ RouteMemory<PER, TH> memory;
     launch_dependents();
+    memory.fill(A);
     for (uint32_t e = threadIdx.x; e < A.stride; e += TH) counts[e] = 0;
     __syncthreads();
     const uint64_t begin = uint64_t(blockIdx.x) * A.per_part, end = min(begin + A.per_part, A.tokens);
-    route_tokens<PER, T>(A, begin + threadIdx.x / 32, end, TH / 32, lists, counts, [](uint64_t, int32_t) {});
+    for (uint64_t t = begin + threadIdx.x / 32; t < end; t += TH / 32) route_token<PER, T, TH>(A, t, memory, counts);
     __syncthreads();
     for (uint32_t e = threadIdx.x; e < A.stride; e += TH) A.counts[uint64_t(blockIdx.x) * A.stride + e] = counts[e];
 }
@@ -654,12 +652,14 @@ __global__ void __launch_bounds__(kRouteThreads<PER>) route_one_kernel(const Rou
     extern __shared__ uint16_t before[];
     __shared__ uint32_t next[PER * 32];
     __shared__ int32_t chosen[kOneSlots];
-    __shared__ uint64_t lists[TH / 32][32];
+    __shared__ RouteMemory<PER, TH> memory;
+    memory.fill(A);
     for (uint32_t e = threadIdx.x; e < A.experts; e += TH) next[e] = 0;
     __syncthreads();
-    route_tokens<PER, T>(A, threadIdx.x / 32, A.tokens, TH / 32, lists, next, [&](uint64_t t, int32_t expert) {
+    for (uint64_t t = threadIdx.x / 32; t < A.tokens; t += TH / 32) {
+        const int32_t expert = route_token<PER, T, TH>(A, t, memory, next);
         if (threadIdx.x % 32 < A.k) chosen[t * A.k + threadIdx.x % 32] = expert;
-    });
+    }
     __syncthreads();
     const uint32_t total = scan<TH>(next, A.experts), slots = uint32_t(A.tokens) * A.k;
     for (uint32_t e = threadIdx.x; e < A.experts; e += TH) A.offsets[e] = int32_t(next[e]);
