@@ -5,7 +5,13 @@
 // launch), so that a call copies nothing to the device and can be captured.  A
 // block takes a chunk of one tensor, a warp 256 consecutive values of it at a
 // time: the block of values that shares a scale of an 8-bit moment, 8 a lane.
-// All loads of those come before the arithmetic.
+// The loads of a warp's next values come before the arithmetic on these.
+//
+// Moments in 32 bits are bound by DRAM: 185 million values in 196 tensors (16-bit
+// gradients and copies) in 968 us, 6.7 TB/s of what it moves, and their norm in
+// 78 (4.8 TB/s).  Moments in 8 bits are bound by instruction issue, 80
+// instructions a value, of which a correctly rounded root and quotient are a
+// third: 218 million values in 589 us, 5.0 TB/s (685 without the loads ahead).
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -376,6 +382,8 @@ __device__ __forceinline__ uint32_t tensor_of(const TABLE& T, uint32_t c)
     return lo;
 }
 
+// 8 bits: 64 registers, for four blocks an SM (80 and three: 596 us; two rounds unrolled, without moves between
+// them: 671).
 template <int WB, int GB, int BITS, int N>
 __global__ void __launch_bounds__(kThreads, BITS == 8 ? 4 : 2) adamw_kernel(const __grid_constant__ Table<N> T, const AdamwArgs A)
 {

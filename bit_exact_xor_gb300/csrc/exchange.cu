@@ -3,7 +3,10 @@
 //
 // A team of threads takes a token, 8 columns a thread at a time: a token's row
 // is read once and written to its k rows, or its k rows are read and summed in
-// registers.  Everything is bound by these rows' bytes.
+// registers.  Everything is bound by these rows' bytes: 65520 rows of 6144
+// values, an eighth of them without a token, gathered in 120 us (bf16, 6.6
+// TB/s), summed in 216 (f32, 7.0 TB/s) or about 140 (bf16), the gradients of the
+// sum in 450 (f32, 6.5 TB/s).
 #include <algorithm>
 
 #include "ops_internal.h"
@@ -98,6 +101,8 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const ExchangeArgs A, 
     }
 }
 
+// As many threads as an SM holds: rows at unrelated places want many loads under way (65520 rows of bf16 values: 156 us with
+// 1536 threads an SM; 8 rows on their way a thread and fewer threads: 203; 32 bytes of a row a thread: 170).
 template <typename TI, typename TO, bool VEC>
 __global__ void __launch_bounds__(kThreads, 8) combine_kernel(const ExchangeArgs A, uint32_t team, uint32_t pieces, uint32_t piece)
 {

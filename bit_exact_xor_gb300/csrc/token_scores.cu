@@ -2,7 +2,7 @@
 // of each row of logits, and the gradient of the first two
 // (include/dcr_ops.h).
 //
-// One pass: each thread reads its words of the row in chunks of 8 and keeps a
+// One pass: each thread reads its words of the row in chunks of 6 and keeps a
 // running maximum m, the sum of exp((x - m) / T) and the sum of that times the
 // exponent; maxima and sums meet once, at the end.  The chunk that holds a
 // thread's maximum is summed apart, so that the threads whose maximum is the
@@ -17,6 +17,12 @@
 // above the bound are taken, and the first of the equal ones in the order of
 // their indexes; where that does not fit either, the largest is searched
 // `top` times.
+//
+// Long batches are bound by instruction issue, 8 to 9 a value, and by the steps
+// at a row's end: 4096 rows of 128256 bf16 values in 183 us (5.7 TB/s), with
+// 20 alternatives in 228; 4096 of 32768 f32 values in 88 (6.1 TB/s) and their
+// gradient in 168 (6.4 TB/s).  Few rows are bound by latency: 8 rows of 128256
+// in 9.0 us, with 20 alternatives in 13.4.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -444,6 +450,8 @@ __device__ __forceinline__ void to_first(const void* p, const Part& v)
                  : "memory");
 }
 
+// 64 registers a thread: 80 leave a quarter of the threads out (4096 rows of
+// 128256 values, 20 alternatives: 251 us), and chunks of 8 words do not fit (349).
 template <typename T, int TH, bool TOP>
 __global__ void __launch_bounds__(TH, 1024 / TH) scores_kernel(ScoreArgs A, uint32_t cluster)
 {
