@@ -598,6 +598,9 @@ __global__ void __launch_bounds__(kRouteThreads<PER>) route_kernel(const RouteAr
     for (uint32_t e = threadIdx.x; e < A.stride; e += TH) A.counts[uint64_t(blockIdx.x) * A.stride + e] = counts[e];
 }
 
+// Shared memory that place() takes: 32 KB at most.
+size_t place_bytes(int threads, uint32_t experts) { return size_t(threads / 32) * experts * sizeof(uint16_t); }
+
 template <int TH>
 __global__ void __launch_bounds__(TH) place_kernel(const RouteArgs A)
 {
@@ -650,14 +653,22 @@ __global__ void __launch_bounds__(TH) place_kernel(const RouteArgs A)
 // All of it for a batch of few slots.
 constexpr uint32_t kOneSlots = 1024;
 
+// What routing and then placing take of the shared memory, one after the other.
+template <int PER>
+size_t one_bytes(uint32_t experts)
+{
+    return std::max(sizeof(RouteMemory<PER, kRouteThreads<PER>>), place_bytes(kRouteThreads<PER>, experts));
+}
+
 template <int PER, typename T>
 __global__ void __launch_bounds__(kRouteThreads<PER>) route_one_kernel(const RouteArgs A)
 {
     constexpr int TH = kRouteThreads<PER>;
-    extern __shared__ uint16_t before[];
+    extern __shared__ __align__(16) uint8_t shared[];
     __shared__ uint32_t next[PER * 32];
     __shared__ int32_t chosen[kOneSlots];
-    __shared__ RouteMemory<PER, TH> memory;
+    RouteMemory<PER, TH>& memory = *reinterpret_cast<RouteMemory<PER, TH>*>(shared);
+    uint16_t* before = reinterpret_cast<uint16_t*>(shared);
     memory.fill(A);
     for (uint32_t e = threadIdx.x; e < A.experts; e += TH) next[e] = 0;
     __syncthreads();
@@ -752,9 +763,6 @@ int with_per(uint32_t experts, F f)
     return f(std::integral_constant<int, 32>());
 }
 
-// Shared memory that place() takes: 32 KB at most.
-size_t place_bytes(int threads, uint32_t experts) { return size_t(threads / 32) * experts * sizeof(uint16_t); }
-
 int route_launch(RouteArgs A, uint32_t dtype, cudaStream_t s)
 {
     const bool one = A.tokens * A.k <= kOneSlots;
@@ -765,7 +773,7 @@ int route_launch(RouteArgs A, uint32_t dtype, cudaStream_t s)
     with_dtype(dtype, [&](auto t) {
         return with_per(A.experts, [&](auto per) {
             constexpr int PER = decltype(per)::value, TH = kRouteThreads<PER>;
-            const LaunchAttrs at(one ? 1 : A.parts, TH, one ? place_bytes(TH, A.experts) : 0, 1, false, s);
+            const LaunchAttrs at(one ? 1 : A.parts, TH, one ? one_bytes<PER>(A.experts) : 0, 1, false, s);
             e = one ? cudaLaunchKernelEx(&at.cfg, route_one_kernel<PER, decltype(t)>, A) : cudaLaunchKernelEx(&at.cfg, route_kernel<PER, decltype(t)>, A);
             return 0;
         });

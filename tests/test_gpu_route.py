@@ -48,6 +48,17 @@ def test_choice_and_order(tokens, experts, k, dtype, scoring):
             _check(z, k, got, scoring, b, renormalise=renormalise, scale=scale)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("experts", [1, 31, 33, 64, 127, 129, 256, 257, 511, 513, 777, 1023, 1024])
+def test_few_and_many_tokens_over_any_number_of_experts(experts, dtype):
+    # a batch in one launch, and just more than that
+    k = min(experts, 8)
+    bias = torch.randn(experts, generator=torch.Generator().manual_seed(2)) * 0.05
+    for tokens in (1, 1024 // k, 1024 // k + 1):
+        z = _router(tokens, experts, dtype, experts)
+        _check(z, k, dcr.route_experts(z.cuda(), k, bias=bias.cuda()), bias=bias)
+
+
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("group_by", [1, 2])
 @pytest.mark.parametrize("tokens,experts,groups,group_top,k", [
