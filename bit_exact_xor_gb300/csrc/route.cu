@@ -329,9 +329,12 @@ __device__ __forceinline__ void keys_of(const T* row, const float (&x)[PER], con
             if (lane == who) score = 0;
             last = top;
         }
+        uint32_t g = first / A.group_size, within = first - g * A.group_size;
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (!(taken >> min((first + i) / A.group_size, 31u) & 1)) key[i] = 0;
+        for (int i = 0; i < PER; ++i) {
+            if (g > 31 || !(taken >> g & 1)) key[i] = 0;
+            if (++within == A.group_size) ++g, within = 0;
+        }
     }
 }
 
