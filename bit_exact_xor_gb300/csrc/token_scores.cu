@@ -685,11 +685,13 @@ int scores_launch(const ScoreArgs& A, uint32_t cluster, cudaStream_t s)
 }
 
 // Blocks of 128 or 256 threads, and one to eight of them for a row, whichever
-// the model of a launch finds fastest: rounds of as many blocks as fit at once
-// (1024 threads an SM), each the time of its chunks, which is DRAM's for what
-// the SMs then have in flight (16 MB when full) or a load's latency, and the
-// steps at its end, which take longer where blocks have to meet.  (1021 rows
-// of 32771 f32 values: blocks of 256 leave a second round half empty.)
+// the model of a launch finds fastest: a block's chunks, each the time of
+// DRAM's for what the SMs then have in flight (16 MB when full, 1024 threads an
+// SM) or a load's latency, for as many blocks as come one after another on a
+// slot; and in each round the steps at a row's end, which take longer where
+// blocks have to meet.  (4096 rows of 128256 bf16 values, 20 alternatives: 208 us
+// with 128 threads, 214 with 256; 1021 of 32771 f32 values: 35 and 41; 8 rows
+// of 128256 in clusters of eight: 15.4 and 12.0.)
 template <typename T>
 int scores_launch(const ScoreArgs& A, cudaStream_t s)
 {
@@ -698,9 +700,8 @@ int scores_launch(const ScoreArgs& A, cudaStream_t s)
     double best = 1e300;
     for (uint32_t th = 128; th <= 256; th *= 2)
         for (uint32_t c = 1; c <= uint32_t(kMaxBlocks) && (c == 1 || (words >= uint64_t(c) * th && A.rows < 1u << 20)); c *= 2) {
-            const double slots = 152.0 * 1024 / th, blocks = double(A.rows) * c, rounds = std::ceil(blocks / slots);
-            const double chunks = std::ceil(double(words) / (c * th * kWords));
-            const double us = rounds * (chunks * std::max(1.0, 0.39 * kWords * std::min(1.0, blocks / slots)) + 4.0 + (c > 1 ? 2.0 : 0.0));
+            const double turns = double(A.rows) * c * th / (152.0 * 1024), chunks = std::ceil(double(words) / (c * th * kWords));
+            const double us = chunks * std::max(1.0, 0.39 * kWords * std::min(1.0, turns)) * std::max(1.0, turns) + std::ceil(turns) * (c > 1 ? 6.0 : 4.0);
             if (us < best) best = us, threads = th, cluster = c;
         }
     return threads == 128 ? scores_launch<T, 128>(A, cluster, s) : scores_launch<T, 256>(A, cluster, s);
