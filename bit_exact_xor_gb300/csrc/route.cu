@@ -16,9 +16,9 @@
 // each block adds up the counts of the parts before its own and places its
 // slots (place_kernel).  A small batch takes one block and one launch.
 //
-// Bound by instruction issue, about 1150 instructions a token of 256 experts in
-// groups with a bias (half of them the choice itself): 16381 tokens in 31 us,
-// 20 without either, of which placing takes 6; their gradient in 6.4 (its 34 MB
+// Bound by instruction issue, about 1120 instructions a token of 256 experts in
+// groups with a bias (680 without either): 16381 tokens in 29 us, 20 without
+// either, of which placing takes 6; their gradient in 6.4 (its 34 MB
 // are 5).  64 tokens over 64 experts take 8.6 us, most of it one token's chain.
 #include <algorithm>
 #include <cmath>

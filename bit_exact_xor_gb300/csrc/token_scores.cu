@@ -20,9 +20,9 @@
 //
 // Long batches are bound by instruction issue, 8 to 9 a value, and by the steps
 // at a row's end: 4096 rows of 128256 bf16 values in 171 us (6.1 TB/s), with
-// 20 alternatives in 214; 4096 of 32768 f32 values in 84 (6.4 TB/s) and their
+// 20 alternatives in 208; 4096 of 32768 f32 values in 84 (6.4 TB/s) and their
 // gradient in 168 (6.4 TB/s).  Few rows are bound by latency: 8 rows of 128256
-// in 7.7 us, with 20 alternatives in 12.1.
+// in 7.8 us, with 20 alternatives in 12.0.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
