@@ -19,8 +19,8 @@
 // `top` times.
 //
 // Long batches are bound by instruction issue, 8 to 9 a value, and by the steps
-// at a row's end: 4096 rows of 128256 bf16 values in 171 us (6.1 TB/s), with
-// 20 alternatives in 208; 4096 of 32768 f32 values in 84 (6.4 TB/s) and their
+// at a row's end: 4096 rows of 128256 bf16 values in 173 us (6.1 TB/s), with
+// 20 alternatives in 213; 4096 of 32768 f32 values in 84 (6.4 TB/s) and their
 // gradient in 168 (6.4 TB/s).  Few rows are bound by latency: 8 rows of 128256
 // in 7.8 us, with 20 alternatives in 12.0.
 #include <algorithm>
@@ -105,6 +105,31 @@ __device__ __forceinline__ Sums plain_sums(const uint4 (&q)[kWords], const Expon
         }
     }
     return {s.x + s.y, t.x + t.y};
+}
+
+// A word whose values below lowest() are that, -inf among them; NaN stays.
+template <typename T>
+__device__ __forceinline__ float lowest()
+{
+    return std::is_same<T, __half>::value ? -65504.0f : -1e30f;
+}
+__device__ __forceinline__ uint4 not_below(const uint4& q, float)
+{
+    return make_uint4(__float_as_uint(max_nan(__uint_as_float(q.x), -1e30f)), __float_as_uint(max_nan(__uint_as_float(q.y), -1e30f)),
+                      __float_as_uint(max_nan(__uint_as_float(q.z), -1e30f)), __float_as_uint(max_nan(__uint_as_float(q.w), -1e30f)));
+}
+template <typename T>
+__device__ __forceinline__ uint4 not_below(const uint4& q, T)
+{
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    const T l = from_f32<T>(lowest<T>());
+    T2 low;
+    low.x = l, low.y = l;
+    union { uint4 w; T2 t[4]; } u;
+    u.w = q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u.t[i] = __hmax2_nan(u.t[i], low);
+    return u.w;
 }
 
 // The same, where a value may be -inf, or left out as if it were, one by one.
@@ -237,7 +262,8 @@ struct Share {
 
 // The sums over a chunk whose largest value is no larger than m, in rows that
 // hold -inf, NaN or an infinite m, or lie far from 0.  Apart, with the chunk
-// read again, so that the common case has its registers.
+// read again, so that the common case has its registers (2048 rows of 128256
+// bf16 values: 90 us, 97 with every seventh value -inf, 242 far from 0).
 template <typename T>
 __device__ __noinline__ Sums rare_sums(const T* x, uint32_t vocab, uint32_t rank, uint32_t blocks, uint32_t c, float m, float sc, float lo)
 {
@@ -366,12 +392,11 @@ __device__ __forceinline__ void list_values(TopMemory<TH>& M, const Share<T>& S,
 // The n largest of the block's share to best, sorted, where the list does not
 // hold all that reach the bound, or fewer than n do.
 template <typename T, int TH>
-__device__ __noinline__ void search_top(TopMemory<TH>& M, const T* x, uint32_t vocab, uint32_t rank, uint32_t blocks, uint32_t n)
+__device__ __noinline__ void search_top(TopMemory<TH>& M, const T* x, uint32_t vocab, uint32_t rank, uint32_t blocks, uint32_t count, uint32_t n)
 {
     constexpr uint32_t W = TH / 32;
     const Share<T> S(x, vocab, rank, blocks);
     const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32, bound = bound_of(M);
-    uint32_t count = M.count;
     __syncthreads();
     if (count > kList) {
         // more than the list holds: those above the bound, then the first that are equal to it
@@ -379,10 +404,11 @@ __device__ __noinline__ void search_top(TopMemory<TH>& M, const T* x, uint32_t v
         __syncthreads();
         list_buckets(M, S, bound + 1);
         __syncthreads();
-        list_values(M, S, bound + 1);
+        const bool fits = M.buckets <= kList - DCR_MAX_TOP;
+        if (fits) list_values(M, S, bound + 1);
         __syncthreads();
         count = M.count;
-        if (count <= kList - DCR_MAX_TOP) {
+        if (fits && count <= kList - DCR_MAX_TOP) {
             uint32_t need = count < n ? n - count : 0, at = count;
             for (uint32_t k = S.first; need && k - threadIdx.x < S.in.words; k += S.step) {
                 // all threads go through words of one stride at a time, in the order of the indexes
@@ -485,6 +511,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) scores_kernel(ScoreArgs A, uint
     float m = -INFINITY;
     Sums rest = {0.0f, 0.0f}, top = {0.0f, 0.0f};
     uint32_t at = 0;
+    bool masked = false;
     for (uint32_t c = 0; c < S.chunks; ++c) {
         uint4 q[kWords];
         S.load(c, q);
@@ -507,10 +534,26 @@ __global__ void __launch_bounds__(TH, 1024 / TH) scores_kernel(ScoreArgs A, uint
             }
             top = {0.0f, 0.0f}, m = cm, at = c;
         }
+        if (m == -INFINITY) {
+            // nothing so far, unless a value is none
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) nan |= word_nan<T>(q[i]);
+            if (nan) rest.s = rest.t = NAN;
+            continue;
+        }
+        if (masked) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) q[i] = not_below(q[i], T());
+        }
         const Exponent e(m, A.sc_dn, A.sc_lo);
         Sums a = plain_sums<T>(q, e, left, S.step);
-        // not a number where a value is -inf or none itself
-        if (!(fabsf(a.t) < INFINITY) || !e.plain) a = rare_sums<T>(x, vocab, rank, cluster, c, m, A.sc_dn, A.sc_lo);
+        if (!(fabsf(a.t) < INFINITY) || !e.plain) {
+            // not a number where a value is -inf or none itself.  A row that holds one -inf holds more: from now on they are
+            // finite values so far below the maximum (which only grows) that their part is 0
+            a = rare_sums<T>(x, vocab, rank, cluster, c, m, A.sc_dn, A.sc_lo);
+            masked = e.plain && (m - lowest<T>()) * A.sc > 200.0f;
+        }
         else correct(a, e);
         if (higher) top = a;
         else rest.s += a.s, rest.t += a.t;
@@ -546,14 +589,16 @@ __global__ void __launch_bounds__(TH, 1024 / TH) scores_kernel(ScoreArgs A, uint
     if (lane == 0) parts[warp] = make_float4(bm, all.count, all.s, all.t);
     __syncthreads();
     if constexpr (TOP) {
-        list_values(top_memory, S, bound);
+        // each bucket listed holds a value at least: more than the list has room for need not be collected
+        const bool fits = top_memory.buckets <= kList;
+        if (fits) list_values(top_memory, S, bound);
         __syncthreads();
-        const uint32_t count = top_memory.count;
+        const uint32_t count = fits ? top_memory.count : kList + 1;
         if (count >= A.top && count <= kList) {
             sort_list(top_memory, count, A.top);
             __syncthreads();
         } else {
-            search_top<T, TH>(top_memory, x, vocab, rank, cluster, A.top);
+            search_top<T, TH>(top_memory, x, vocab, rank, cluster, count, A.top);
         }
     }
     all = {bm, 0.0f, 0.0f, 0.0f};
@@ -690,7 +735,7 @@ int scores_launch(const ScoreArgs& A, uint32_t cluster, cudaStream_t s)
 // SM) or a load's latency, for as many blocks as come one after another on a
 // slot; and in each round the steps at a row's end, which take longer where
 // blocks have to meet.  (4096 rows of 128256 bf16 values, 20 alternatives: 208 us
-// with 128 threads, 214 with 256; 1021 of 32771 f32 values: 35 and 41; 8 rows
+// with 128 threads, 214 with 256, before -inf was kept out of the slow sums; 1021 of 32771 f32 values: 35 and 41; 8 rows
 // of 128256 in clusters of eight: 15.4 and 12.0.)
 template <typename T>
 int scores_launch(const ScoreArgs& A, cudaStream_t s)
