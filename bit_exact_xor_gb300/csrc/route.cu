@@ -369,12 +369,40 @@ __device__ __noinline__ int32_t choose_again(const T* row, const float* bias, co
     return mine;
 }
 
-// The k best experts: lane j's is the j-th (-1: none).  list: 32 entries of
-// the warp's own.
-template <int PER, typename T>
-__device__ __forceinline__ int32_t choose(const float (&x)[PER], const float* bias, const T* row, const RouteArgs& A, uint64_t* list)
+// What the warps of a block that route tokens share.
+template <int PER, int TH>
+struct RouteMemory {
+    float bias[PER * 32];
+    uint64_t lists[TH / 32][32];
+    bool even;      // all biases are the same, and more than -inf
+    __device__ __forceinline__ void fill(const RouteArgs& A)
+    {
+        bool same = true;
+        const float first = bias_of(A, 0);
+        for (uint32_t e = threadIdx.x; e < PER * 32; e += TH) {
+            bias[e] = e < A.experts ? bias_of(A, e) : 0.0f;
+            same &= e >= A.experts || bias[e] == first;
+        }
+        same = __syncthreads_and(same && first > -INFINITY);
+        if (threadIdx.x == 0) even = same;
+    }
+};
+
+// The k best experts: lane j's is the j-th (-1: none).
+template <int PER, typename T, int TH>
+__device__ __forceinline__ int32_t choose(const float (&x)[PER], const T* row, const RouteArgs& A, RouteMemory<PER, TH>& M)
 {
     const uint32_t lane = threadIdx.x % 32, first = lane * PER;
+    const float* bias = M.bias;
+    uint64_t* list = M.lists[threadIdx.x / 32];
+    // a row without a difference (padding, say): the first k, without the comparisons in 64 bits that so many ties would take
+    const float one = __shfl_sync(~0u, x[0], 0);
+    if (__all_sync(~0u, x[0] == one || first >= A.experts) && M.even && one > -INFINITY) {
+        bool even = true;
+#pragma unroll
+        for (int i = 1; i < PER; ++i) even &= x[i] == one || first + i >= A.experts;
+        if (__all_sync(~0u, even)) return lane < A.k ? int32_t(lane) : -1;
+    }
     uint32_t key[PER];
     float most;
     keys_of<PER, T, float>(row, x, bias, A, key, most);
@@ -461,17 +489,6 @@ __device__ __forceinline__ void softmax_of(const float (&x)[PER], float& m, floa
     total = warp_sum(total);
 }
 
-// What the warps of a block that route tokens share.
-template <int PER, int TH>
-struct RouteMemory {
-    float bias[PER * 32];
-    uint64_t lists[TH / 32][32];
-    __device__ __forceinline__ void fill(const RouteArgs& A)
-    {
-        for (uint32_t e = threadIdx.x; e < PER * 32; e += TH) bias[e] = e < A.experts ? bias_of(A, e) : 0.0f;
-    }
-};
-
 // A token by a warp; its experts are counted in `counts`.  Returns lane j's.
 template <int PER, typename T, int TH>
 __device__ __forceinline__ int32_t route_token(const RouteArgs& A, uint64_t token, RouteMemory<PER, TH>& M, uint32_t* counts)
@@ -483,7 +500,7 @@ __device__ __forceinline__ int32_t route_token(const RouteArgs& A, uint64_t toke
     float x[PER];
     load_row<PER, T>(row, A.experts, x);
     if (!A.mask || A.mask[token]) {
-        c.expert = choose<PER, T>(x, M.bias, row, A, M.lists[threadIdx.x / 32]);
+        c.expert = choose<PER, T>(x, row, A, M);
         if (c.expert >= 0) c.logit = to_f32(row[c.expert]);
         float m = 0.0f, total = 1.0f;
         if (!A.sigmoid && !A.renormalise) {

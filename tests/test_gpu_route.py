@@ -217,3 +217,28 @@ def test_all_tokens_to_the_same_experts():
     z = torch.zeros(3000, 64)
     z[:, 5], z[:, 63] = 2.0, 1.0
     _check(z, 2, dcr.route_experts(z.cuda(), 2))
+
+
+@pytest.mark.parametrize("experts,groups", [(64, 1), (256, 8), (60, 6), (1000, 4)])
+def test_rows_without_a_difference(experts, groups):
+    # padding that nothing masks: all logits of a row are equal, beside rows that are not; with all sorts of biases
+    k, kw = 8, dict(groups=groups, group_top=max(2, groups // 2) if groups > 1 else 1)
+    z = _router(300, experts, "f32", 11)
+    z[::2] = 0.0
+    z[1::10] = 3.5
+    z[3::10] = -math.inf
+    z[5::10, -1] = 0.1
+    z[7::10] = float("nan")
+    zero = torch.zeros(experts)
+    some = zero.clone()
+    some[3], some[-1] = -math.inf, 0.25
+    for scoring in ("softmax", "sigmoid"):
+        for bias in (None, zero, zero + 0.5, some, zero - math.inf):
+            got = dcr.route_experts(z.cuda(), k, scoring=scoring, bias=None if bias is None else bias.cuda(), **kw)
+            chosen = R.choose(z, k, scoring, bias, groups, kw["group_top"], 2, None)
+            assert torch.equal(got.experts.cpu().long(), chosen)
+            offsets, order, positions = R.expert_order(chosen, experts)
+            assert torch.equal(got.offsets.cpu().long(), offsets) and torch.equal(got.order.cpu().long(), order)
+            w = R.weights(z.double(), chosen, scoring, True, 1.0)
+            # a few roundings: equal parts of 1, or the quotients of other tests
+            assert bool(((got.weights.cpu().double() - w).abs() <= w * 2.0 ** -16).all())
