@@ -615,10 +615,11 @@ extern "C" int dcr_adamw(const dcr_adamw_tensor* tensors, uint32_t count, uint32
     const dcr_adamw_opts& o = *opts;
     if (o.state_bits != 32 && o.state_bits != 8) return set_error(DCR_ERR_INVALID, "dcr_adamw: state_bits must be 32 or 8");
     if (!(o.beta1 >= 0.0 && o.beta1 < 1.0) || !(o.beta2 >= 0.0 && o.beta2 < 1.0)) return set_error(DCR_ERR_INVALID, "dcr_adamw: betas must lie in [0, 1)");
-    if (!std::isfinite(o.lr) || o.lr < 0.0 || !std::isfinite(o.weight_decay) || o.weight_decay < 0.0 || !std::isfinite(o.eps) || o.eps < 0.0)
+    auto finite = [](double v) { return std::isfinite(float(v)); };    // in the 32 bits that the kernel computes in
+    if (!finite(o.lr) || o.lr < 0.0 || !finite(o.weight_decay) || o.weight_decay < 0.0 || !finite(o.eps) || o.eps < 0.0)
         return set_error(DCR_ERR_INVALID, "dcr_adamw: lr, weight_decay and eps must be finite and not negative");
-    if (!std::isfinite(o.grad_scale)) return set_error(DCR_ERR_INVALID, "dcr_adamw: grad_scale must be finite");
-    if (!std::isfinite(o.max_norm) || o.max_norm < 0.0 || (o.max_norm > 0.0 && !o.norm))
+    if (!finite(o.grad_scale)) return set_error(DCR_ERR_INVALID, "dcr_adamw: grad_scale must be finite");
+    if (!finite(o.max_norm) || o.max_norm < 0.0 || (o.max_norm > 0.0 && !o.norm))
         return set_error(DCR_ERR_INVALID, "dcr_adamw: max_norm must be finite, not negative, and needs a norm");
     if (o.step == 0 && !o.device_step) return set_error(DCR_ERR_INVALID, "dcr_adamw: step counts from 1");
     if (uintptr_t(o.norm) % 4 || uintptr_t(o.device_lr) % 4 || uintptr_t(o.device_step) % 8)

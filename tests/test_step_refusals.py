@@ -154,7 +154,7 @@ nan, inf = float("nan"), float("inf")
 
 @pytest.mark.parametrize("kw,why", [
     (dict(w=3), "unknown dtype"), (dict(g=3), "unknown dtype"), (dict(c=4), "unknown dtype"), (dict(bits=16), "state_bits"), (dict(beta1=1.0), "betas"),
-    (dict(beta1=-0.1), "betas"), (dict(beta2=nan), "betas"), (dict(lr=nan), "lr"), (dict(lr=-1.0), "lr"), (dict(eps=inf), "eps"), (dict(weight_decay=-1.0), "weight_decay"),
+    (dict(beta1=-0.1), "betas"), (dict(beta2=nan), "betas"), (dict(lr=nan), "lr"), (dict(lr=-1.0), "lr"), (dict(eps=inf), "eps"), (dict(lr=1e39), "lr"), (dict(grad_scale=1e39), "grad_scale"), (dict(weight_decay=-1.0), "weight_decay"),
     (dict(grad_scale=inf), "grad_scale"), (dict(max_norm=1.0), "max_norm"), (dict(max_norm=nan, norm=P), "max_norm"), (dict(step=0), "step"),
     (dict(norm=P + 2), "misaligned"), (dict(device_step=P + 4), "misaligned"), (dict(device_lr=P + 2), "misaligned"),
     (dict(t=[dict(w=None)]), "NULL"), (dict(t=[dict(grad=None)]), "NULL"), (dict(t=[dict(m=None)]), "NULL"), (dict(t=[dict(v=None)]), "NULL"),
