@@ -28,9 +28,11 @@ struct ExchangeArgs {
 
 constexpr int kThreads = 256;
 
-// 8 values at p, of which the first n exist.
+// 8 values of a thread: consecutive ones in 16-byte words where all is laid
+// out so (VEC), else every `team`th, the first n of them, so that neighbouring
+// threads still read neighbouring values.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, uint32_t n, float (&v)[8])
+__device__ __forceinline__ void load8(const T* p, uint32_t team, uint32_t n, float (&v)[8])
 {
     if (VEC) {
         uint4 q[sizeof(T) / 2];
@@ -41,11 +43,11 @@ __device__ __forceinline__ void load8(const T* p, uint32_t n, float (&v)[8])
         for (int i = 0; i < 8; ++i) v[i] = to_f32(t[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = uint32_t(i) < n ? to_f32(p[i]) : 0.0f;
+        for (int i = 0; i < 8; ++i) v[i] = uint32_t(i) < n ? to_f32(p[i * team]) : 0.0f;
     }
 }
 template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* p, uint32_t n, const float (&v)[8])
+__device__ __forceinline__ void store8(T* p, uint32_t team, uint32_t n, const float (&v)[8])
 {
     if (VEC) {
         uint4 q[sizeof(T) / 2];
@@ -57,34 +59,38 @@ __device__ __forceinline__ void store8(T* p, uint32_t n, const float (&v)[8])
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (uint32_t(i) < n) p[i] = from_f32<T>(v[i]);
+            if (uint32_t(i) < n) p[i * team] = from_f32<T>(v[i]);
     }
 }
 
 // The token and the columns of a thread: blockIdx.x counts pieces of `piece`
 // columns within groups of tokens, one for each team.
+template <bool VEC>
 struct Place {
     uint64_t token, begin, end;
-    __device__ __forceinline__ Place(const ExchangeArgs& A, uint32_t team, uint32_t pieces, uint32_t piece)
+    uint32_t team;
+    __device__ __forceinline__ Place(const ExchangeArgs& A, uint32_t team_, uint32_t pieces, uint64_t piece) : team(team_)
     {
         token = uint64_t(blockIdx.x / pieces) * (kThreads / team) + threadIdx.x / team;
-        begin = uint64_t(blockIdx.x % pieces) * piece + threadIdx.x % team * 8;
+        begin = uint64_t(blockIdx.x % pieces) * piece + threadIdx.x % team * (VEC ? 8 : 1);
         end = min(uint64_t(blockIdx.x % pieces + 1) * piece, A.cols);
     }
+    // how many of the values from column c on exist
+    __device__ __forceinline__ uint32_t count(uint64_t c) const { return VEC ? 8 : uint32_t(min((end - c + team - 1) / team, uint64_t(8))); }
 };
 
 template <typename TI, typename TO, bool VEC>
 __global__ void __launch_bounds__(kThreads) gather_kernel(const ExchangeArgs A, uint32_t team, uint32_t pieces, uint32_t piece)
 {
-    const Place P(A, team, pieces, piece);
+    const Place<VEC> P(A, team, pieces, piece);
     if (P.token >= A.tokens) return;
     const int32_t* pos = A.positions + P.token * A.k;
     const float* w = A.weights ? A.weights + P.token * A.k : nullptr;
     const TI* x = static_cast<const TI*>(A.tokens_side) + P.token * A.token_stride;
     for (uint64_t c = P.begin; c < P.end; c += team * 8) {
-        const uint32_t n = uint32_t(min(P.end - c, uint64_t(8)));
+        const uint32_t n = P.count(c);
         float v[8];
-        load8<TI, VEC>(x + c, n, v);
+        load8<TI, VEC>(x + c, team, n, v);
         for (uint32_t j = 0; j < A.k; ++j) {
             const uint64_t row = uint64_t(int64_t(pos[j]));
             if (row >= A.rows) continue;
@@ -93,9 +99,9 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const ExchangeArgs A, 
                 float u[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) u[i] = v[i] * w[j];
-                store8<TO, VEC>(out, n, u);
+                store8<TO, VEC>(out, team, n, u);
             } else {
-                store8<TO, VEC>(out, n, v);
+                store8<TO, VEC>(out, team, n, v);
             }
         }
     }
@@ -106,36 +112,37 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const ExchangeArgs A, 
 template <typename TI, typename TO, bool VEC>
 __global__ void __launch_bounds__(kThreads, 8) combine_kernel(const ExchangeArgs A, uint32_t team, uint32_t pieces, uint32_t piece)
 {
-    const Place P(A, team, pieces, piece);
+    const Place<VEC> P(A, team, pieces, piece);
     if (P.token >= A.tokens) return;
     const int32_t* pos = A.positions + P.token * A.k;
     const float* w = A.weights ? A.weights + P.token * A.k : nullptr;
     TO* out = static_cast<TO*>(A.out) + P.token * A.out_stride;
     for (uint64_t c = P.begin; c < P.end; c += team * 8) {
-        const uint32_t n = uint32_t(min(P.end - c, uint64_t(8)));
+        const uint32_t n = P.count(c);
         float s[8] = {};
 #pragma unroll 4
         for (uint32_t j = 0; j < A.k; ++j) {
             const uint64_t row = uint64_t(int64_t(pos[j]));
             if (row >= A.rows) continue;
             float v[8];
-            load8<TI, VEC>(static_cast<const TI*>(A.rows_side) + row * A.row_stride + c, n, v);
+            load8<TI, VEC>(static_cast<const TI*>(A.rows_side) + row * A.row_stride + c, team, n, v);
             const float f = w ? w[j] : 1.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[i] = fmaf(f, v[i], s[i]);
         }
-        store8<TO, VEC>(out + c, n, s);
+        store8<TO, VEC>(out + c, team, n, s);
     }
 }
 
 constexpr int kAtOnce = 4;     // rows whose products with the gradient are summed at once
+constexpr uint64_t kFullWarps = 152 * 16;      // of combine_grad_kernel, which fill the SMs
 
 // TY: type of y and its gradient, TG: of the output's gradient.
 template <typename TY, typename TG, bool VEC>
 __global__ void __launch_bounds__(kThreads) combine_grad_kernel(const ExchangeArgs A, uint32_t team)
 {
     __shared__ float part[kThreads / 32][kAtOnce];
-    const Place P(A, team, 1, ~0u);
+    const Place<VEC> P(A, team, 1, A.cols);
     const bool on = P.token < A.tokens;
     const int32_t* pos = A.positions + P.token * A.k;
     const float* w = A.weights ? A.weights + P.token * A.k : nullptr;
@@ -150,12 +157,12 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(const ExchangeAr
             dot[i] = 0.0f;
         }
         for (uint64_t c = P.begin; on && c < A.cols; c += team * 8) {
-            const uint32_t n = uint32_t(min(A.cols - c, uint64_t(8)));
+            const uint32_t n = P.count(c);
             float v[8], y[kAtOnce][8];
-            load8<TG, VEC>(g + c, n, v);
+            load8<TG, VEC>(g + c, team, n, v);
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i)
-                if (A.grad_weights && row[i] < A.rows) load8<TY, VEC>(static_cast<const TY*>(A.rows_side) + row[i] * A.row_stride + c, n, y[i]);
+                if (A.grad_weights && row[i] < A.rows) load8<TY, VEC>(static_cast<const TY*>(A.rows_side) + row[i] * A.row_stride + c, team, n, y[i]);
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) {
                 if (row[i] >= A.rows) continue;
@@ -167,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(const ExchangeAr
                     float u[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) u[e] = v[e] * f[i];
-                    store8<TY, VEC>(static_cast<TY*>(A.out) + row[i] * A.out_stride + c, n, u);
+                    store8<TY, VEC>(static_cast<TY*>(A.out) + row[i] * A.out_stride + c, team, n, u);
                 }
             }
         }
@@ -310,7 +317,10 @@ extern "C" int dcr_experts_combine_grad(const void* y, uint32_t y_dtype, uint64_
     const uint32_t ys = dtype_size(y_dtype);
     const bool vec = cols % 8 == 0 && aligned(grad, grad_stride, dtype_size(dtype)) && (!grad_weights || aligned(y, y_stride, ys)) &&
                      (!grad_y || aligned(grad_y, grad_y_stride, ys));
-    const uint32_t team = team_of(cols);
+    // A warp a token needs no barriers (2432 tokens of 8 rows of 1024 bf16 values: 27 -> 17 us); a block shares one where
+    // tokens are few, or rows so long that their pieces are better read at once (8190 of 6144 f32 values: 469 -> 450).
+    const bool warps = tokens >= kFullWarps && cols * ys <= 16384;
+    const uint32_t team = std::min(team_of(cols), warps ? 32u : uint32_t(kThreads));
     return with_types(y_dtype, dtype, vec, [&](auto a, auto b, auto v) {
         const LaunchAttrs at((tokens + kThreads / team - 1) / (kThreads / team), kThreads, 0, 1, false, static_cast<cudaStream_t>(stream));
         const cudaError_t e = cudaLaunchKernelEx(&at.cfg, combine_grad_kernel<decltype(a), decltype(b), decltype(v)::value>, A, team);

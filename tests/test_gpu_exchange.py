@@ -81,6 +81,27 @@ def test_gradients_of_combine(tokens, experts, k, cols, dtype, grads):
     assert bool((by_w.cpu()[r.positions < 0] == 0).all())
 
 
+@pytest.mark.parametrize("dtype,cols", [("bf16", 8192), ("bf16", 1000), ("f32", 333), ("f16", 8), ("f32", 4100)])
+def test_gradients_of_combine_of_many_tokens(dtype, cols):
+    # enough tokens for a warp each: a thread adds up at most 8 products of every 256 columns, then threads in pairs
+    tokens, k = 2500, 2
+    r = _route(tokens, 7, k, cols, masked=0.2)
+    y, g = _randn(tokens * k, cols, dtype, 2), _randn(tokens, cols, dtype, 3)
+    total = int(r.offsets[-1])
+    slot = r.order[:total].long()
+    y[total:] = float("nan")
+    into = torch.full((tokens * k, cols), 7.0, dtype=DT[dtype], device="cuda")
+    by_y, by_w = dcr.experts_combine_grad(y.cuda(), _cuda(r), g.cuda(), out=into)
+    assert bool((by_y[total:] == 7).all())
+    assert torch.equal(by_y.cpu()[:total], (g[slot // k].float() * r.weights.reshape(-1)[slot][:, None]).to(DT[dtype]))
+    exp, size = (torch.zeros(tokens * k, dtype=torch.float64) for _ in range(2))
+    part = y[:total].double() * g[slot // k].double()
+    exp[slot], size[slot] = part.sum(1), part.abs().sum(1)
+    off = (by_w.cpu().double().reshape(-1) - exp).abs()
+    assert bool((off <= size * (8 * (cols // 256 + 1) + 8) * 2.0 ** -24).all())
+    assert bool((by_w.cpu()[r.positions < 0] == 0).all())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("cols", [16, 40, 1001])
 def test_strides(cols, dtype):
