@@ -736,11 +736,14 @@ int scores_launch(const ScoreArgs& A, uint32_t cluster, cudaStream_t s)
 // slot; and in each round the steps at a row's end, which take longer where
 // blocks have to meet.  (4096 rows of 128256 bf16 values, 20 alternatives: 208 us
 // with 128 threads, 214 with 256, before -inf was kept out of the slow sums; 1021 of 32771 f32 values: 35 and 41; 8 rows
-// of 128256 in clusters of eight: 15.4 and 12.0.)
+// of 128256 in clusters of eight: 15.4 and 12.0.)  A row of one chunk takes a
+// warp, as long as its 32 maxima give a bound (2154 rows of 60, 5
+// alternatives: 27 -> 15 us).
 template <typename T>
 int scores_launch(const ScoreArgs& A, cudaStream_t s)
 {
     const uint64_t words = (A.vocab * sizeof(T) + 15) / 16 + 1;
+    if (words <= 32 * kWords && A.top <= 32) return scores_launch<T, 32>(A, 1, s);
     uint32_t threads = 128, cluster = 1;
     double best = 1e300;
     for (uint32_t th = 128; th <= 256; th *= 2)

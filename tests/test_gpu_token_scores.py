@@ -105,7 +105,7 @@ def _hard_rows(vocab):
     return torch.stack(rows)
 
 
-@pytest.mark.parametrize("vocab,top", [(7000, 1), (7000, 20), (7000, 64), (40000, 20), (70, 64)])
+@pytest.mark.parametrize("vocab,top", [(7000, 1), (7000, 20), (7000, 64), (40000, 20), (70, 64), (70, 5), (700, 20), (700, 32), (764, 1), (764, 33)])
 @pytest.mark.parametrize("many", [False, True])
 def test_alternatives_of_hard_rows(vocab, top, many):
     z = _hard_rows(vocab)
