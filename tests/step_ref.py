@@ -101,8 +101,7 @@ def weights(x, chosen, scoring, renormalise, scale):
 def expert_order(chosen, experts):
     """offsets, order, positions of a counting sort that keeps the slots' order."""
     flat = chosen.reshape(-1).tolist()
-    order = [s for e in range(experts) for s in (i for i, c in enumerate(flat) if c == e)] if len(flat) * experts < 1 << 22 else [
-        s for _, s in sorted((c, i) for i, c in enumerate(flat) if c >= 0)]
+    order = [s for _, s in sorted((c, i) for i, c in enumerate(flat) if c >= 0)]
     offsets = [0] * (experts + 1)
     for c in flat:
         if c >= 0:
