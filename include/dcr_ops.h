@@ -145,11 +145,11 @@ int dcr_token_logprobs(const void* logits, uint32_t dtype, uint64_t rows, uint64
  *   entropy = log(1 + r) + D,
  * and the `top` likeliest tokens, the lowest index first among equal ones,
  * with their log-probabilities: top_logp and top_tokens [rows, top], top at
- * most DCR_MAX_TOP and vocab.  A NaN stands behind every number there.
- * stats [rows, 3] receives M, r and D, which dcr_token_scores_grad takes.
- * logp, entropy, stats and top_logp are held in 32 bits.  A row whose token lies outside
- * [0, vocab) is left out: its logits are not read, its outputs are 0 and its
- * alternatives' tokens -1.  logp, entropy and stats may each be NULL. */
+ * most DCR_MAX_TOP and vocab.  A NaN stands behind every number there.  stats
+ * [rows, 3] receives M, r and D, which dcr_token_scores_grad takes.  logp,
+ * entropy, stats and top_logp are held in 32 bits.  A row whose token lies
+ * outside [0, vocab) is left out: its logits are not read, its outputs are 0
+ * and its alternatives' tokens -1.  logp, entropy and stats may each be NULL. */
 #define DCR_MAX_TOP 64u
 int dcr_token_scores(const void* logits, uint32_t dtype, uint64_t rows, uint64_t vocab, uint64_t row_stride,
                      const int64_t* tokens, float temperature, uint32_t top, float* logp, float* entropy,
@@ -177,17 +177,16 @@ int dcr_token_scores_grad(const void* logits, uint32_t dtype, uint64_t rows, uin
  * groups (of experts / groups consecutive experts) whose group_by (1 or 2)
  * best sum highest.  Which experts are chosen is decided as with scores in 64
  * bits; without a bias, and with one group or group_by 1, by the logits
- * themselves.  Their weights are s without the bias,
- * divided by the sum over the chosen ones if renormalise is not 0, times
- * scale.  An expert whose logit or s + bias is -inf or NaN is never chosen;
- * a token that mask (bytes, nullable) has a 0 for chooses none.  Slots without
- * an expert hold expert -1, weight 0 and position -1.
- *   experts, weights, positions [tokens, k]; offsets [experts + 1]: the rows
- * of expert e are offsets[e] to offsets[e + 1], as dcr_nvfp4_matmul takes
- * them, ordered by token; positions: the row of a slot; order [tokens * k]: the slot
- * (token * k + place) of a row, -1 behind the last.
- * workspace: device, 16-byte aligned, DCR_ROUTE_WORKSPACE(experts) bytes.
- * tokens * k < 2^31. */
+ * themselves.  Their weights are s without the bias, divided by the sum over
+ * the chosen ones if renormalise is not 0, times scale.  An expert whose logit
+ * or s + bias is -inf or NaN is never chosen; a token that mask (bytes,
+ * nullable) has a 0 for chooses none.  Slots without an expert hold expert -1,
+ * weight 0 and position -1.
+ * experts, weights, positions [tokens, k]; offsets [experts + 1]: the rows of
+ * expert e are offsets[e] to offsets[e + 1], as dcr_nvfp4_matmul takes them,
+ * ordered by token; positions: the row of a slot; order [tokens * k]: the slot
+ * (token * k + place) of a row, -1 behind the last.  workspace: device,
+ * 16-byte aligned, DCR_ROUTE_WORKSPACE(experts) bytes.  tokens * k < 2^31. */
 enum { DCR_SOFTMAX = 0, DCR_SIGMOID = 1 };
 #define DCR_MAX_CHOSEN 32u
 #define DCR_MAX_GROUPS 32u
@@ -203,42 +202,44 @@ int dcr_route(const void* logits, uint32_t dtype, uint64_t tokens, uint32_t expe
 
 /* The gradient by the logits of a loss whose derivative by the weights is
  * grad_weights [tokens, k]; the choice itself and the bias carry none.  grad
- * [tokens, experts] (dtype, rows grad_stride elements apart); opts: scoring, k, renormalise
- * and scale are used. */
+ * [tokens, experts] (dtype, rows grad_stride elements apart); opts: scoring,
+ * k, renormalise and scale are used. */
 int dcr_route_grad(const void* logits, uint32_t dtype, uint64_t tokens, uint32_t experts, uint64_t row_stride,
                    const int32_t* chosen, const float* grad_weights, const dcr_route_opts* opts, void* grad,
                    uint64_t grad_stride, void* stream);
 
-/* Rows into the experts' order: out[positions[t, j]] = x[t], times
- * weights[t, j] if weights is not NULL, rounded once.  x [tokens, cols] (x_dtype, rows x_stride
- * elements apart), out (dtype, rows out_stride apart) of `rows` rows; positions [tokens, k] as from
- * dcr_route; one that lies outside [0, rows) is passed over, and rows of out that none
- * names are left as they are. */
+/* Rows into the experts' order: out[positions[t, j]] = x[t], times weights[t,
+ * j] if weights is not NULL, rounded once.  x [tokens, cols] (x_dtype, rows
+ * x_stride elements apart), out (dtype, rows out_stride apart) of `rows` rows;
+ * positions [tokens, k] as from dcr_route; one that lies outside [0, rows) is
+ * passed over, and rows of out that none names are left as they are. */
 int dcr_experts_gather(const void* x, uint32_t x_dtype, uint64_t tokens, uint64_t cols, uint64_t x_stride,
                        const int32_t* positions, uint32_t k, const float* weights, void* out, uint32_t dtype,
                        uint64_t rows, uint64_t out_stride, void* stream);
 
-/* The rows back: out[t] = sum_j weights[t, j] y[positions[t, j]] (weights NULL:
- * 1), summed in 32 bits in the order of j and rounded once; a token without a row
- * gets 0, whatever the other rows hold.  y: `rows` rows.  With weights NULL
- * it is the gradient of dcr_experts_gather by x. */
+/* The rows back: out[t] = sum_j weights[t, j] y[positions[t, j]] (weights
+ * NULL: 1), summed in 32 bits in the order of j and rounded once; a token
+ * without a row gets 0, whatever the other rows hold.  y: `rows` rows.  With
+ * weights NULL it is the gradient of dcr_experts_gather by x. */
 int dcr_experts_combine(const void* y, uint32_t y_dtype, uint64_t rows, uint64_t cols, uint64_t y_stride,
                         const int32_t* positions, const float* weights, uint64_t tokens, uint32_t k, void* out,
                         uint32_t dtype, uint64_t out_stride, void* stream);
 
-/* Gradients of dcr_experts_combine from that of its output, grad [tokens, cols]
- * (dtype): grad_y[positions[t, j]] = weights[t, j] grad[t] (y_dtype, nullable; rows that no
- * slot has are left as they are) and grad_weights[t, j] = y[positions[t, j]] .
- * grad[t] (nullable; 0 for a slot without a row).  weights NULL: 1. */
+/* Gradients of dcr_experts_combine from that of its output, grad [tokens,
+ * cols] (dtype): grad_y[positions[t, j]] = weights[t, j] grad[t] (y_dtype,
+ * nullable; rows that no slot has are left as they are), and grad_weights[t,
+ * j] (nullable) is the dot product of y[positions[t, j]] and grad[t], 0 for a
+ * slot without a row.  weights NULL: 1. */
 int dcr_experts_combine_grad(const void* y, uint32_t y_dtype, uint64_t rows, uint64_t cols, uint64_t y_stride,
                              const int32_t* positions, const float* weights, uint64_t tokens, uint32_t k,
                              const void* grad, uint32_t dtype, uint64_t grad_stride, void* grad_y,
                              uint64_t grad_y_stride, float* grad_weights, void* stream);
 
 /* ---- the trainer's step ------------------------------------------------
- * norm [1] = the square root of the sum of the squares (in 32 bits, added up in 64, in a fixed order)
- * of every gradient: `count` tensors of n contiguous values of dtype.  workspace: device, 8-byte
- * aligned, DCR_NORM_WORKSPACE bytes. */
+ * norm [1] = the square root of the sum of the squares of every gradient:
+ * `count` tensors of n contiguous values of dtype.  Squares are held in 32
+ * bits (a value beyond 1.8e19 makes the norm infinite) and added up in 64 in a
+ * fixed order.  workspace: device, 8-byte aligned, DCR_NORM_WORKSPACE bytes. */
 #define DCR_NORM_WORKSPACE 9728u
 typedef struct {
     const void* values;
@@ -250,24 +251,27 @@ int dcr_grad_norm(const dcr_grad* grads, uint32_t count, uint32_t dtype, void* w
  *   g = grad * grad_scale (times max_norm / N if N = |grad_scale| norm[0] > max_norm > 0),
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
  *   w = w (1 - lr weight_decay) - lr / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps).
- * Every operation is rounded to 32 bits by itself, in that order, w to its
- * type at the end and the copy (copy_dtype, DCR_NONE without), from the same 32 bits, to
- * its own: a master in 32 bits and 16-bit weights in a refit's arena are
- * written together.  16-bit weights without a master are rounded to nearest, and so lose
- * updates below half of their last bit.
- *   state_bits 32: m and v are floats.  state_bits 8: m and sqrt(v) are held as e4m3
- * values (m, v: n bytes) times a 32-bit scale per 256 consecutive values
+ * The factors of lr, betas and step are formed in 64 bits; every operation on
+ * the values is rounded to 32 bits by itself, in that order, w to its type at
+ * the end and the copy (copy_dtype, DCR_NONE without), from the same 32 bits,
+ * to its own: a master in 32 bits and 16-bit weights in a refit's arena are
+ * written together.  16-bit weights without a master are rounded to nearest,
+ * and so lose updates below half of their last bit.
+ * state_bits 32: m and v are floats.  state_bits 8: m and sqrt(v) are held as
+ * e4m3 values (m, v: n bytes) times a 32-bit scale per 256 consecutive values
  * of a tensor (m_scale, v_scale: ceil(n / 256) floats), the scale being the
  * block's largest magnitude times 1 / 448.  A value between two of e4m3 is
  * rounded up with the probability of its distance from the lower one, so that
- * moments keep moving on average although a step changes them by less than half an e4m3
- * step; sqrt(v) above 0 is never rounded to 0.  The random bits are a hash of
- * seed, step and the value's number in the call: the same call gives the same
- * bits.  A block with an infinite or NaN moment reads back as NaN.
- * norm (device, nullable): if it is not finite the step is left out whole: nothing is written.
- * device_step, device_lr (device, nullable) stand in step's and lr's place, for captured graphs;
- * the step is the number of this update, from 1, and is not changed.
- * Tensors that are written may not overlap any other. */
+ * moments keep moving on average although a step changes them by less than
+ * half an e4m3 step; sqrt(v) above 0 is never rounded to 0.  The random bits
+ * are a hash of seed, step and the value's number in the call: the same call
+ * gives the same bits.  A block with an infinite or NaN moment reads back as
+ * NaN.  norm (device, nullable): if N is not finite the step is left out
+ * whole: nothing is written.  device_step, device_lr (device, nullable) stand
+ * in step's and lr's place, for captured graphs (their factors are formed in
+ * 32 bits); the step is the number of
+ * this update, from 1, and is not changed.  Tensors that are written may not
+ * overlap any other. */
 typedef struct {
     void* w;
     const void* grad;
