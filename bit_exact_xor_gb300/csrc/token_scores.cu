@@ -15,8 +15,8 @@
 // chunks that reach it are read again, and their values of that size sorted.
 // Where those are too many (equal ones above all: masked rows), the values
 // above the bound are taken, and the first of the equal ones in the order of
-// their indexes; where that does not fit either, the largest is searched
-// `top` times.
+// their indexes, then of NaN; where that does not fit either, the largest is
+// searched `top` times.
 //
 // Long batches are bound by instruction issue, 8 to 9 a value, and by the steps
 // at a row's end: 4096 rows of 128256 bf16 values in 173 us (6.1 TB/s), with
@@ -399,7 +399,7 @@ __device__ __noinline__ void search_top(TopMemory<TH>& M, const T* x, uint32_t v
     const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32, bound = bound_of(M);
     __syncthreads();
     if (count > kList) {
-        // more than the list holds: those above the bound, then the first that are equal to it
+        // more than the list holds: those above the bound, then the first that are equal to it, then the first NaN
         if (threadIdx.x == 0) M.count = M.buckets = 0;
         __syncthreads();
         list_buckets(M, S, bound + 1);
@@ -410,31 +410,34 @@ __device__ __noinline__ void search_top(TopMemory<TH>& M, const T* x, uint32_t v
         count = M.count;
         if (fits && count <= kList - DCR_MAX_TOP) {
             uint32_t need = count < n ? n - count : 0, at = count;
-            for (uint32_t k = S.first; need && k - threadIdx.x < S.in.words; k += S.step) {
-                // all threads go through words of one stride at a time, in the order of the indexes
-                const uint4 q = S.in.load(k);
-                uint32_t equal = 0;
-                S.each(q, k, [&](float v, uint32_t) { equal += order_of(v) == bound; });
-                uint32_t before = equal;
+            // a bound of -inf is also that of threads that met no number: what is missing then is NaN, of order 0
+            for (uint32_t pass = 0, order = bound; pass < 2; ++pass, order = 0) {
+                for (uint32_t k = S.first; need && k - threadIdx.x < S.in.words; k += S.step) {
+                    // all threads go through words of one stride at a time, in the order of the indexes
+                    const uint4 q = S.in.load(k);
+                    uint32_t equal = 0;
+                    S.each(q, k, [&](float v, uint32_t) { equal += order_of(v) == order; });
+                    uint32_t before = equal;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t u = __shfl_up_sync(~0u, before, o);
-                    if (lane >= uint32_t(o)) before += u;
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const uint32_t u = __shfl_up_sync(~0u, before, o);
+                        if (lane >= uint32_t(o)) before += u;
+                    }
+                    __syncthreads();
+                    if (lane == 31) M.scan[warp] = before;
+                    __syncthreads();
+                    before -= equal;
+                    uint32_t all = 0;
+                    for (uint32_t i = 0; i < W; ++i) {
+                        if (i < warp) before += M.scan[i];
+                        all += M.scan[i];
+                    }
+                    S.each(q, k, [&](float v, uint32_t i) {
+                        if (order_of(v) == order && before++ < need) M.list[at + before - 1] = key_of(v, i);
+                    });
+                    const uint32_t taken = min(all, need);
+                    at += taken, need -= taken;
                 }
-                __syncthreads();
-                if (lane == 31) M.scan[warp] = before;
-                __syncthreads();
-                before -= equal;
-                uint32_t all = 0;
-                for (uint32_t i = 0; i < W; ++i) {
-                    if (i < warp) before += M.scan[i];
-                    all += M.scan[i];
-                }
-                S.each(q, k, [&](float v, uint32_t i) {
-                    if (order_of(v) == bound && before++ < need) M.list[at + before - 1] = key_of(v, i);
-                });
-                const uint32_t taken = min(all, need);
-                at += taken, need -= taken;
             }
             __syncthreads();
             sort_list(M, at, n);

@@ -1,0 +1,36 @@
+"""Rare inputs of a step's operators."""
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import bit_exact_xor_gb300 as dcr  # noqa: E402
+import step_ref as R  # noqa: E402
+from step_ref import DT  # noqa: E402
+
+
+def _rows_of_few_numbers(vocab):
+    g = torch.Generator().manual_seed(3)
+    z = torch.full((8, vocab), float("nan"))                            # the first: no number at all
+    z[1, [5, vocab // 2, vocab - 1]] = torch.tensor([1.0, -2.0, 3.0])
+    z[2, ::vocab // 30] = float("-inf")
+    z[3] = z[2]
+    z[3, 7:12] = torch.randn(5, generator=g)
+    z[4, :600] = torch.randn(vocab, generator=g)[:600]
+    z[5, 100:] = float("-inf")
+    z[6, torch.randperm(vocab, generator=g)[:63]] = float("inf")
+    z[7] = torch.randn(vocab, generator=g)                              # an ordinary one beside them
+    return z
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(6, 40000, "f32"), (400, 40000, "f32"), (400, 40000, "bf16"), (1216, 20011, "f32"), (800, 9000, "f16"), (700, 200, "bf16")])
+@pytest.mark.parametrize("top", [1, 8, 64])
+def test_alternatives_of_rows_of_few_numbers(rows, vocab, dtype, top):
+    z = _rows_of_few_numbers(vocab).to(DT[dtype])
+    exp = R.top(z, top)
+    at = torch.arange(rows) % len(z)
+    got = dcr.token_scores(z[at].cuda(), torch.zeros(rows, dtype=torch.int64, device="cuda"), top=top)
+    tokens = got.top_tokens.cpu()
+    assert int(tokens.min()) >= 0 and int(tokens.max()) < vocab
+    assert torch.equal(tokens, exp[at]), (tokens != exp[at]).any(1).nonzero()[:8, 0]
