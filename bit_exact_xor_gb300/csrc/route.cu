@@ -125,11 +125,11 @@ __device__ __forceinline__ float bias_of(const RouteArgs& A, int32_t e) { return
 struct Slack {
     float score;
     __device__ __forceinline__ Slack(bool sigmoid, float most) : score(0x1p-24f * (sigmoid ? 20.0f : 256.0f) * most) {}
-    // a is the larger one; parts: scores that each is the sum of
-    __device__ __forceinline__ bool near(float a, float b, float parts) const
-    {
-        return a - b <= score * parts + 0x1p-23f * parts * (fabsf(a) + fabsf(b));
-    }
+    // a is the larger one
+    __device__ __forceinline__ bool near(float a, float b) const { return a - b <= score + 0x1p-23f * (fabsf(a) + fabsf(b)); }
+    // How far a group's sum of two keys may be off, where `size` is the sum of their magnitudes, which may be far larger than
+    // their sum's: two scores' errors, half a unit of each key and of the sum, and as much again for what is computed with it.
+    __device__ __forceinline__ float of_group(float size) const { return score + 0x1p-22f * size; }
 };
 
 // A lane's consecutive values of a row, -inf behind its end; 16 bytes at a
@@ -269,10 +269,14 @@ __device__ __forceinline__ void keys_of(const T* row, const float (&x)[PER], con
         }
     }
     if (A.groups > 1) {
-        // lane g: the order of group g's score
+        // lane g: the order of group g's score, and the magnitudes that it is the sum of
         O score = 0;
+        float size = 0.0f;
         const uint32_t lanes = A.group_size / PER;
         auto join = [&](O a, O b) { return a == 0 ? O(0) : b == 0 || A.group_by == 1 ? a : order_of(value_of(a, V()) + value_of(b, V())); };
+        auto size_of = [&](O a, O b) {      // of numbers of 32 bits: those of 64 need no bound
+            return k32 ? (a == 0 ? 0.0f : fabsf(float(value_of(a, V())))) + (b == 0 ? 0.0f : fabsf(float(value_of(b, V())))) : 0.0f;
+        };
         if (lanes * PER == A.group_size && (lanes & (lanes - 1)) == 0) {
             // groups of whole lanes, a power of two of them
             O a = 0, b = 0;
@@ -287,6 +291,7 @@ __device__ __forceinline__ void keys_of(const T* row, const float (&x)[PER], con
                 a = max(a, c);
             }
             score = __shfl_sync(~0u, join(a, b), (lane * lanes) & 31);
+            size = __shfl_sync(~0u, size_of(a, b), (lane * lanes) & 31);
             if (lane >= A.groups) score = 0;
         } else {
             for (uint32_t g = 0; g < A.groups; ++g) {
@@ -301,25 +306,27 @@ __device__ __forceinline__ void keys_of(const T* row, const float (&x)[PER], con
                 const O top = warp_max(a);
                 const uint32_t who = __ffs(__ballot_sync(~0u, a == top)) - 1;
                 const O next = warp_max(lane == who ? b : a);
-                if (lane == g) score = join(top, next);
+                if (lane == g) score = join(top, next), size = size_of(top, next);
             }
         }
         const O group = score;
         uint32_t taken = 0;
-        O last = 0;
         for (uint32_t r = 0; r <= A.group_top; ++r) {
             const O top = warp_max(score);
             if (top == 0) break;
             if (r == A.group_top) {
                 if constexpr (k32) {
-                    const Slack slack(A.sigmoid, most);
-                    const float in = value_of(last, 0.0f), out = value_of(top, 0.0f), mine = value_of(group, 0.0f);
-                    if (!A.by_logit && slack.near(in, out, 2.0f)) {
-                        // groups that may change places
-                        const bool taken_one = taken >> lane & 1;
-                        const bool close = group != 0 && (taken_one ? slack.near(mine, out, 2.0f) : slack.near(in, mine, 2.0f));
-                        const uint32_t all = __ballot_sync(~0u, close);
-                        taken = settle_groups<PER>(row, A, taken & ~all, all);
+                    if (!A.by_logit) {
+                        // a group may change places if it may be lower than one that is not taken, or higher than one that is
+                        // (low is 0 where an infinite error is taken from an infinite score)
+                        const float v = value_of(group, 0.0f), err = Slack(A.sigmoid, most).of_group(size);
+                        const bool in = taken >> lane & 1, out = group != 0 && !in;
+                        const uint32_t low = order_of(v - err), high = order_of(v + err);
+                        const uint32_t highest = warp_max(out ? high : 0u), lowest = ~warp_max(in ? ~low : 0u);
+                        if (lowest <= highest) {
+                            const uint32_t all = __ballot_sync(~0u, in ? low <= highest : out && high >= lowest);
+                            taken = settle_groups<PER>(row, A, taken & ~all, all);
+                        }
                     }
                 }
                 break;
@@ -327,7 +334,6 @@ __device__ __forceinline__ void keys_of(const T* row, const float (&x)[PER], con
             const uint32_t who = __ffs(__ballot_sync(~0u, score == top)) - 1;
             taken |= 1u << who;
             if (lane == who) score = 0;
-            last = top;
         }
         uint32_t g = first / A.group_size, within = first - g * A.group_size;
 #pragma unroll
@@ -450,7 +456,7 @@ __device__ __forceinline__ int32_t choose(const float (&x)[PER], const T* row, c
         const uint32_t other = lane < count ? lane + 1 : count - 1;
         const float v = value_of(uint32_t(mine >> 32), 0.0f), u = __shfl_sync(~0u, v, other & 31);
         const int32_t e = __shfl_sync(~0u, expert, other & 31);
-        const bool close = lane < n && other < n && slack.near(fmaxf(u, v), fminf(u, v), 1.0f);
+        const bool close = lane < n && other < n && slack.near(fmaxf(u, v), fminf(u, v));
         const bool tie = close && !(to_f32(row[e]) == to_f32(row[expert]) && bias_of(A, e) == bias_of(A, expert));
         if (__any_sync(~0u, tie)) return settle<PER, T>(row, A, expert, count, count + __popc(__ballot_sync(~0u, close && lane >= count)));
     }

@@ -34,3 +34,20 @@ def test_alternatives_of_rows_of_few_numbers(rows, vocab, dtype, top):
     tokens = got.top_tokens.cpu()
     assert int(tokens.min()) >= 0 and int(tokens.max()) < vocab
     assert torch.equal(tokens, exp[at]), (tokens != exp[at]).any(1).nonzero()[:8, 0]
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("large", [100.0, 1000.0, 65536.0])
+@pytest.mark.parametrize("size", [2, 4, 6])
+def test_groups_whose_biases_cancel(size, large, scoring):
+    # the two best of a group have biases of opposite sign: their sum is far smaller than what it is the sum of
+    tokens, groups = 2000, 4
+    g = torch.Generator().manual_seed(size)
+    bias = torch.tensor([large, -large] + [-4 * large] * (size - 2)).repeat(groups)
+    z = torch.randn(tokens, 1, size, generator=g) + torch.randn(tokens, groups, size, generator=g) * 2e-5
+    z = z.reshape(tokens, groups * size).contiguous()
+    for group_top in (1, 2):
+        kw = dict(scoring=scoring, groups=groups, group_top=group_top, group_by=2)
+        got = dcr.route_experts(z.cuda(), 2, bias=bias.cuda(), **kw)
+        exp = R.choose(z, 2, scoring, bias, groups, group_top, 2, None)
+        assert torch.equal(got.experts.cpu().long(), exp), int((got.experts.cpu().long() != exp).any(1).sum())
