@@ -1,4 +1,5 @@
 """Rare inputs of a step's operators."""
+import math
 
 import pytest
 
@@ -51,3 +52,15 @@ def test_groups_whose_biases_cancel(size, large, scoring):
         got = dcr.route_experts(z.cuda(), 2, bias=bias.cuda(), **kw)
         exp = R.choose(z, 2, scoring, bias, groups, group_top, 2, None)
         assert torch.equal(got.experts.cpu().long(), exp), int((got.experts.cpu().long() != exp).any(1).sum())
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_groups_whose_sums_pass_32_bits(scoring):
+    # each score and bias is a finite number, and the sum of two is not one of 32 bits
+    far = torch.tensor([-3.4e38, -3.4e38, -3e38, -3e38, -3.2e38, -3.2e38, 1.0, -math.inf])
+    z = torch.randn(50, 8, generator=torch.Generator().manual_seed(4))
+    for bias, group_top, k in ((far, 1, 1), (far, 2, 3), (far, 3, 5), (-far, 1, 2), (-far, 2, 4), (far.abs().clamp(max=3.4e38), 2, 3)):
+        kw = dict(scoring=scoring, groups=4, group_top=group_top, group_by=2)
+        got = dcr.route_experts(z.cuda(), k, bias=bias.cuda(), **kw)
+        exp = R.choose(z, k, scoring, bias, 4, group_top, 2, None)
+        assert torch.equal(got.experts.cpu().long(), exp), (got.experts[0].tolist(), exp[0].tolist())
