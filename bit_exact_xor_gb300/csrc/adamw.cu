@@ -428,32 +428,76 @@ struct NormTable {
     uint32_t count;
 };
 
-// Partial sums of squares: each block takes every gridDim-th chunk, whose
-// squares a thread adds up in 32 bits and over chunks in 64.
-template <typename T, int N>
-__global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ NormTable<N> A, double* part, bool more)
+// The values of a chunk that a thread takes: 16-byte words from lo on, and at
+// most one value (of index `single`) before or behind them.
+template <typename T>
+struct Share {
+    static constexpr int V = 16 / sizeof(T);
+    const T* p;
+    uint64_t lo, single;
+    uint32_t words;
+    bool one;
+    __device__ __forceinline__ Share(const T* p_, uint64_t begin, uint64_t end) : p(p_)
+    {
+        lo = min(begin + (16 - (uintptr_t(p + begin) & 15)) % 16 / sizeof(T), end);
+        words = uint32_t((end - lo) / V);
+        single = threadIdx.x < V ? begin + threadIdx.x : lo + words * V + (threadIdx.x - V);
+        one = threadIdx.x < V ? single < lo : threadIdx.x < 2 * V && single < end;
+    }
+    __device__ __forceinline__ const uint4* word(uint32_t i) const { return reinterpret_cast<const uint4*>(p + lo) + i; }
+};
+
+// A thread's squares of its values times `scale`.
+template <typename T>
+__device__ __noinline__ float scaled_squares(const T* p, uint64_t begin, uint64_t end, float scale)
 {
-    constexpr int V = 16 / sizeof(T);
+    const Share<T> S(p, begin, end);
+    float q = 0.0f;
+    for (uint32_t i = threadIdx.x; i < S.words; i += kThreads) {
+        const uint4 x = *S.word(i);
+        const T* t = reinterpret_cast<const T*>(&x);
+#pragma unroll
+        for (int j = 0; j < S.V; ++j) q = fmaf(to_f32(t[j]) * scale, to_f32(t[j]) * scale, q);
+    }
+    const float v = S.one ? to_f32(p[S.single]) * scale : 0.0f;
+    return fmaf(v, v, q);
+}
+
+// Partial sums of squares: each block takes every gridDim-th chunk, whose
+// squares a thread adds up in 32 bits (65 at most) and over chunks in 64.  A
+// thread whose sum overflows takes its values again times 2^-70 (squares up to
+// 2^116), and one whose sum is so small, although values are not 0, that it may
+// lack squares below the smallest normal number, times 2^100 (of values below
+// 2^-50; the smallest number's square is 2^-98).
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads, 8) squares_kernel(const __grid_constant__ NormTable<N> A, double* part, bool more)
+{
     __shared__ double sums[kThreads / 32];
     double s = 0.0;
     for (uint32_t c = blockIdx.x; c < A.chunk[A.count]; c += gridDim.x) {
         const uint32_t k = tensor_of(A, c);
         const uint64_t begin = uint64_t(c - A.chunk[k]) * kNormPer, end = min(begin + kNormPer, A.e[k].n);
         const T* p = static_cast<const T*>(A.e[k].values);
-        // the 16-byte words inside, and the values before and behind them
-        const uint64_t lo = min(begin + (16 - (uintptr_t(p + begin) & 15)) % 16 / sizeof(T), end), words = (end - lo) / V;
+        const Share<T> S(p, begin, end);
         float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        const uint4* w = reinterpret_cast<const uint4*>(p + lo);
+        uint32_t any = 0;
 #pragma unroll 4
-        for (uint32_t i = threadIdx.x; i < words; i += kThreads) {
-            const uint4 x = w[i];
+        for (uint32_t i = threadIdx.x; i < S.words; i += kThreads) {
+            const uint4 x = *S.word(i);
             const T* t = reinterpret_cast<const T*>(&x);
 #pragma unroll
-            for (int j = 0; j < V; ++j) q[j % 4] = fmaf(to_f32(t[j]), to_f32(t[j]), q[j % 4]);
+            for (int j = 0; j < S.V; ++j) q[j % 4] = fmaf(to_f32(t[j]), to_f32(t[j]), q[j % 4]);
+            any |= x.x | x.y | x.z | x.w;
         }
-        const uint64_t i = threadIdx.x < V ? begin + threadIdx.x : lo + words * V + (threadIdx.x - V);
-        if (threadIdx.x < V ? i < lo : threadIdx.x < 2 * V && i < end) q[0] = fmaf(to_f32(p[i]), to_f32(p[i]), q[0]);
-        s += double(q[0] + q[1]) + double(q[2] + q[3]);
+        if (S.one) {
+            const float v = to_f32(p[S.single]);
+            q[0] = fmaf(v, v, q[0]);
+            any |= __float_as_uint(v);
+        }
+        double sum = double(q[0] + q[1]) + double(q[2] + q[3]);
+        if (!(sum <= FLT_MAX)) sum = double(scaled_squares(p, begin, end, 0x1p-70f)) * 0x1p140;
+        else if (any != 0 && sum < 0x1p-100) sum = double(scaled_squares(p, begin, end, 0x1p100f)) * 0x1p-200;
+        s += sum;
     }
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
     if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = s;

@@ -237,9 +237,11 @@ int dcr_experts_combine_grad(const void* y, uint32_t y_dtype, uint64_t rows, uin
 
 /* ---- the trainer's step ------------------------------------------------
  * norm [1] = the square root of the sum of the squares of every gradient:
- * `count` tensors of n contiguous values of dtype.  Squares are held in 32
- * bits (a value beyond 1.8e19 makes the norm infinite) and added up in 64 in a
- * fixed order.  workspace: device, 8-byte aligned, DCR_NORM_WORKSPACE bytes. */
+ * `count` tensors of n contiguous values of dtype.  Up to 65 squares are
+ * added up in 32 bits (scaled by a power of two where these would not hold
+ * them) and the sums of these in 64, all in a fixed order; a norm beyond the
+ * largest float is infinite.  workspace: device, 8-byte aligned,
+ * DCR_NORM_WORKSPACE bytes. */
 #define DCR_NORM_WORKSPACE 9728u
 typedef struct {
     const void* values;

@@ -64,3 +64,28 @@ def test_groups_whose_sums_pass_32_bits(scoring):
         got = dcr.route_experts(z.cuda(), k, bias=bias.cuda(), **kw)
         exp = R.choose(z, k, scoring, bias, 4, group_top, 2, None)
         assert torch.equal(got.experts.cpu().long(), exp), (got.experts[0].tolist(), exp[0].tolist())
+
+
+@pytest.mark.parametrize("dtype,value", [("f32", 5e18), ("f32", 1e19), ("f32", 3e38), ("f32", 1e-22), ("f32", 1e-38), ("f32", 1e-44), ("bf16", 5e18),
+                                         ("bf16", 1e38), ("bf16", 1e-22), ("bf16", 1e-39), ("f16", 6e-8)])
+@pytest.mark.parametrize("n,gap", [(1, 0), (300, 1), (16384, 0), (100003, 3)])
+def test_norm_of_squares_that_32_bits_do_not_hold(n, gap, dtype, value):
+    g = (torch.randn(n + gap, generator=torch.Generator().manual_seed(1)).clamp(-1, 1) * value).to(DT[dtype])
+    for x in (g, torch.full_like(g, value)):
+        exp = math.sqrt(float((x[gap:].double() / value).square().sum())) * value
+        got = float(dcr.grad_norm([x.cuda()[gap:]]))
+        # at most 65 squares of 32 bits one after another, of which the root halves the error, and the result's own rounding
+        assert abs(got - exp) <= exp * 70 * 2.0 ** -25 + 2.0 ** -150 or (exp > 3.4028235e38 and got == math.inf), (got, exp)
+
+
+def test_norm_of_large_among_small():
+    # one thread's squares do not fit 32 bits, the others' do not; what is not a number stays that
+    x = torch.ones(100000)
+    x[777], x[50001] = 1e30, 1e-30
+    exp = math.sqrt(float(x.double().square().sum()))
+    assert abs(float(dcr.grad_norm([torch.zeros(5000, device="cuda"), x.cuda()])) - exp) <= exp * 70 * 2.0 ** -25
+    for bad in (math.inf, math.nan):
+        x[99999] = bad
+        norm = float(dcr.grad_norm([x.cuda()]))
+        assert not math.isfinite(norm) and math.isnan(norm) == math.isnan(bad)
+    assert float(dcr.grad_norm([torch.zeros(70001, dtype=torch.bfloat16, device="cuda"), -torch.zeros(3, dtype=torch.bfloat16, device="cuda")])) == 0.0
