@@ -88,8 +88,6 @@ __device__ __forceinline__ float warp_max(float v)
     return v;
 }
 
-__device__ __forceinline__ float max_of(float a, float b) { return fmaxf(a, b); }
-__device__ __forceinline__ double max_of(double a, double b) { return fmax(a, b); }
 __device__ __forceinline__ float exp_of(float v) { return expf(v); }
 __device__ __forceinline__ double exp_of(double v) { return exp(v); }
 
@@ -276,9 +274,11 @@ __device__ __forceinline__ void keys_of(const T* row, const float (&x)[PER], con
         O score = 0;
         float size = 0.0f;
         const uint32_t lanes = A.group_size / PER;
-        // the sum of two keys that can be chosen is one that can, also where 32 bits do not hold it
+        // the sum of two keys that can be chosen is one that can, also where 32 bits do not hold it (64 always do)
         auto join = [&](O a, O b) {
-            return a == 0 ? O(0) : b == 0 || A.group_by == 1 ? a : order_of(max_of(value_of(a, V()) + value_of(b, V()), V(-FLT_MAX)));
+            V sum = value_of(a, V()) + value_of(b, V());
+            if constexpr (k32) sum = fmaxf(sum, -FLT_MAX);
+            return a == 0 ? O(0) : b == 0 || A.group_by == 1 ? a : order_of(sum);
         };
         auto size_of = [&](O a, O b) {      // of numbers of 32 bits: those of 64 need no bound
             return k32 ? (a == 0 ? 0.0f : fabsf(float(value_of(a, V())))) + (b == 0 ? 0.0f : fabsf(float(value_of(b, V())))) : 0.0f;

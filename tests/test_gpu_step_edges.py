@@ -66,6 +66,18 @@ def test_groups_whose_sums_pass_32_bits(scoring):
         assert torch.equal(got.experts.cpu().long(), exp), (got.experts[0].tolist(), exp[0].tolist())
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_groups_whose_sums_pass_32_bits_and_that_are_chosen_from_again(scoring):
+    # more experts of equal scores than a warp has lanes, which are decided one after another
+    bias = torch.tensor([-3.4e38, -3e38, -3.2e38, -3.1e38]).repeat_interleave(40)
+    z = torch.randn(50, 160, generator=torch.Generator().manual_seed(4))
+    for group_top in (1, 2, 4):
+        kw = dict(scoring=scoring, groups=4, group_top=group_top, group_by=2)
+        got = dcr.route_experts(z.cuda(), 8, bias=bias.cuda(), **kw)
+        exp = R.choose(z, 8, scoring, bias, 4, group_top, 2, None)
+        assert torch.equal(got.experts.cpu().long(), exp), (got.experts[0].tolist(), exp[0].tolist())
+
+
 @pytest.mark.parametrize("dtype,value", [("f32", 5e18), ("f32", 1e19), ("f32", 3e38), ("f32", 1e-22), ("f32", 1e-38), ("f32", 1e-44), ("bf16", 5e18),
                                          ("bf16", 1e38), ("bf16", 1e-22), ("bf16", 1e-39), ("f16", 6e-8)])
 @pytest.mark.parametrize("n,gap", [(1, 0), (300, 1), (16384, 0), (100003, 3)])
