@@ -223,10 +223,13 @@ struct Scale {
 
 // |x| inv as e4m3 codes, in the last byte: a value of e4m3 is one of 32 bits
 // whose exponent is 120 larger, cut to 3 bits of mantissa; 16 random bits, a
-// half below their last one, are added to what is cut off.  The largest value
-// is 448 within three units of its last place, which leaves the code at 448's
-// whatever is added (at most 2^20 - 8).  (A block that is not finite has a NaN
-// for its scale, and any codes.)
+// half below their last one, are added to what is cut off.  That is at most
+// 2^20 - 8 units of the last place of 448, so that a largest value less than 8
+// above 448 keeps 448's code and does not become a NaN's.  It is within three
+// where the scale is a normal number.  A subnormal one (largest values of 1.3e-36
+// to 5.3e-36) is itself off by up to 2^-22 of it, 3.5 units instead of 0.9, which
+// makes six; below, 1 / scale is cut to the largest number, and values are
+// smaller.  (A block that is not finite has a NaN for its scale, and any codes.)
 __device__ __forceinline__ uint2 encode2(float2 x, float inv, uint32_t random0, uint32_t random1)
 {
     const float2 y = mul2(mul2(make_float2(fabsf(x.x), fabsf(x.y)), both(inv)), both(0x1p-120f));

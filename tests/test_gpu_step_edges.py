@@ -101,3 +101,25 @@ def test_norm_of_large_among_small():
         norm = float(dcr.grad_norm([x.cuda()]))
         assert not math.isfinite(norm) and math.isnan(norm) == math.isnan(bad)
     assert float(dcr.grad_norm([torch.zeros(70001, dtype=torch.bfloat16, device="cuda"), -torch.zeros(3, dtype=torch.bfloat16, device="cuda")])) == 0.0
+
+
+def test_moments_in_8_bits_near_the_smallest_number():
+    # scales below the smallest normal number: they, and what the moments are divided by, have fewer digits
+    n, blocks = 2 ** 20, 2 ** 12
+    g = torch.Generator().manual_seed(6)
+    size = torch.exp(torch.linspace(math.log(1e-36), math.log(1e-34), blocks))
+    grad = (torch.rand(blocks, 256, generator=g) * 2 - 1) * size[:, None]
+    grad[:, 0] = size                       # the block's largest
+    grad[::2, ::3] = -size[::2, None]       # and many equal to it
+    grad = grad.reshape(-1)
+    w = torch.randn(n, generator=g)
+    state = dcr.adamw_states([w.cuda()], 8)
+    dev = w.cuda()
+    dcr.adamw_step([dev], [grad.cuda()], state, 1, 1e-3, seed=11)
+    zero = (torch.zeros(n, dtype=torch.uint8), torch.zeros(blocks))
+    new, _, st = R.adamw(w, grad, zero + zero, None, 1, 1e-3, (0.9, 0.999), 1e-8, 0.0, bits=R.random_bits(11, 1, 0, n))
+    assert float(st[1].min()) < 2.0 ** -126 < float(st[1].max())
+    assert torch.equal(dev.cpu(), new)
+    for a, b in zip(state[0], st):
+        assert torch.equal(a.cpu(), b)
+    assert not bool(((state[0].m & 127) == 127).any())
