@@ -123,3 +123,17 @@ def test_moments_in_8_bits_near_the_smallest_number():
     for a, b in zip(state[0], st):
         assert torch.equal(a.cpu(), b)
     assert not bool(((state[0].m & 127) == 127).any())
+
+
+@pytest.mark.parametrize("tokens,experts,k", [(20000, 16, 8), (6000, 64, 32), (9800, 600, 32), (40000, 33, 8)])
+def test_parts_of_several_rounds(tokens, experts, k):
+    # a part of the batch holds more slots than the block that places them has threads
+    z = torch.randn(tokens, experts, generator=torch.Generator().manual_seed(tokens))
+    mask = torch.arange(tokens) % 7 != 3
+    got = dcr.route_experts(z.cuda(), k, mask=mask.cuda())
+    chosen = torch.where(mask[:, None], torch.sort(z, dim=1, descending=True, stable=True)[1][:, :k], -1)
+    assert torch.equal(got.experts.cpu().long(), chosen)
+    offsets, order, positions = R.expert_order(chosen, experts)
+    assert torch.equal(got.offsets.cpu().long(), offsets)
+    assert torch.equal(got.order.cpu().long(), order)
+    assert torch.equal(got.positions.cpu().long(), positions)
