@@ -272,6 +272,9 @@ extern "C" int dcr_experts_gather(const void* x, uint32_t x_dtype, uint64_t toke
     if (int rc = check_matrix(what, "x", x, x_dtype, tokens, cols, x_stride)) return rc;
     if (int rc = check_matrix(what, "out", out, dtype, rows, cols, out_stride)) return rc;
     if (tokens == 0 || cols == 0 || rows == 0) return DCR_OK;
+    if (int rc = check_overlap(what, {{"out", out, dtype_size(dtype), rows, cols, out_stride}},
+                               {{"x", x, dtype_size(x_dtype), tokens, cols, x_stride}, {"positions", positions, tokens * k * 4}, {"weights", weights, tokens * k * 4}}))
+        return rc;
     ExchangeArgs A{};
     A.tokens_side = x, A.out = out, A.positions = positions, A.weights = weights;
     A.tokens = tokens, A.cols = cols, A.rows = rows, A.token_stride = x_stride, A.out_stride = out_stride, A.k = k;
@@ -290,6 +293,9 @@ extern "C" int dcr_experts_combine(const void* y, uint32_t y_dtype, uint64_t row
     if (int rc = check_matrix(what, "y", y, y_dtype, rows, cols, y_stride)) return rc;
     if (int rc = check_matrix(what, "out", out, dtype, tokens, cols, out_stride)) return rc;
     if (tokens == 0 || cols == 0) return DCR_OK;
+    if (int rc = check_overlap(what, {{"out", out, dtype_size(dtype), tokens, cols, out_stride}},
+                               {{"y", y, dtype_size(y_dtype), rows, cols, y_stride}, {"positions", positions, tokens * k * 4}, {"weights", weights, tokens * k * 4}}))
+        return rc;
     ExchangeArgs A{};
     A.rows_side = y, A.out = out, A.positions = positions, A.weights = weights;
     A.tokens = tokens, A.cols = cols, A.rows = rows, A.row_stride = y_stride, A.out_stride = out_stride, A.k = k;
@@ -311,6 +317,13 @@ extern "C" int dcr_experts_combine_grad(const void* y, uint32_t y_dtype, uint64_
     if (int rc = check_matrix(what, "grad_y", grad_y, y_dtype, 0, cols, grad_y ? grad_y_stride : cols)) return rc;
     if (uintptr_t(grad_weights) % 4) return set_error(DCR_ERR_INVALID, "%s: misaligned buffer", what);
     if (tokens == 0 || (!grad_y && !grad_weights)) return DCR_OK;
+    // each value of y, and each weight, is read by the threads that write its gradient, and before that
+    const Memory in_y = {"y", grad_weights ? y : nullptr, dtype_size(y_dtype), rows, cols, y_stride}, in_w = {"weights", weights, tokens * k * 4},
+                 none, out_y = {"grad_y", grad_y, dtype_size(y_dtype), rows, cols, grad_y_stride}, out_w = {"grad_weights", grad_weights, tokens * k * 4};
+    const Memory in_grad = {"grad", grad, dtype_size(dtype), tokens, cols, grad_stride}, in_pos = {"positions", positions, tokens * k * 4};
+    if (int rc = check_overlap(what, {out_y, out_w}, {in_grad, in_pos})) return rc;
+    if (int rc = check_overlap(what, {out_y}, {grad_y == y && grad_y_stride == y_stride ? none : in_y, in_w})) return rc;
+    if (int rc = check_overlap(what, {out_w}, {grad_weights == weights ? none : in_w, in_y})) return rc;
     ExchangeArgs A{};
     A.tokens_side = grad, A.rows_side = y, A.out = grad_y, A.positions = positions, A.weights = weights, A.grad_weights = grad_weights;
     A.tokens = tokens, A.cols = cols, A.rows = rows, A.token_stride = grad_stride, A.row_stride = y_stride, A.out_stride = grad_y_stride, A.k = k;

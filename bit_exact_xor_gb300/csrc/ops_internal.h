@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "../../include/dcr_ops.h"
+#include "overlap.h"
 
 namespace dcr {
 

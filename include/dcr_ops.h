@@ -212,7 +212,9 @@ int dcr_route_grad(const void* logits, uint32_t dtype, uint64_t tokens, uint32_t
  * j] if weights is not NULL, rounded once.  x [tokens, cols] (x_dtype, rows
  * x_stride elements apart), out (dtype, rows out_stride apart) of `rows` rows;
  * positions [tokens, k] as from dcr_route; one that lies outside [0, rows) is
- * passed over, and rows of out that none names are left as they are. */
+ * passed over, and rows of out that none names are left as they are.  out may
+ * overlap no input: such calls are refused, as they are of every operator from
+ * here to the end of this file. */
 int dcr_experts_gather(const void* x, uint32_t x_dtype, uint64_t tokens, uint64_t cols, uint64_t x_stride,
                        const int32_t* positions, uint32_t k, const float* weights, void* out, uint32_t dtype,
                        uint64_t rows, uint64_t out_stride, void* stream);
@@ -229,7 +231,8 @@ int dcr_experts_combine(const void* y, uint32_t y_dtype, uint64_t rows, uint64_t
  * cols] (dtype): grad_y[positions[t, j]] = weights[t, j] grad[t] (y_dtype,
  * nullable; rows that no slot has are left as they are), and grad_weights[t,
  * j] (nullable) is the dot product of y[positions[t, j]] and grad[t], 0 for a
- * slot without a row.  weights NULL: 1. */
+ * slot without a row.  weights NULL: 1.  grad_y may be y itself, in the same
+ * place, and grad_weights weights. */
 int dcr_experts_combine_grad(const void* y, uint32_t y_dtype, uint64_t rows, uint64_t cols, uint64_t y_stride,
                              const int32_t* positions, const float* weights, uint64_t tokens, uint32_t k,
                              const void* grad, uint32_t dtype, uint64_t grad_stride, void* grad_y,

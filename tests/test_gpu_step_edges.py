@@ -7,6 +7,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import bit_exact_xor_gb300 as dcr  # noqa: E402
+from bit_exact_xor_gb300 import experts  # noqa: E402
 import step_ref as R  # noqa: E402
 from step_ref import DT  # noqa: E402
 
@@ -137,3 +138,32 @@ def test_parts_of_several_rounds(tokens, experts, k):
     assert torch.equal(got.offsets.cpu().long(), offsets)
     assert torch.equal(got.order.cpu().long(), order)
     assert torch.equal(got.positions.cpu().long(), positions)
+
+
+@pytest.mark.parametrize("cols", [24, 515, 4096])
+def test_exchange_within_one_buffer(cols):
+    # inputs and outputs side by side in the columns of one buffer, and gradients in the place of what they are of
+    tokens, k = 40, 2
+    g = torch.Generator().manual_seed(2)
+    chosen = torch.stack([torch.randperm(6, generator=g)[:k] for _ in range(tokens)])
+    offsets, order, positions = R.expert_order(chosen, 6)
+    r = dcr.Route(*(x.cuda() for x in (chosen.int(), torch.rand(tokens, k, generator=g), offsets.int(), order.int(), positions.int())))
+    buf = torch.randn(tokens * k, 3 * cols + 8, generator=g).cuda()
+    x, y, out, left = buf[:tokens, :cols], buf[:, cols:2 * cols], buf[:, 2 * cols:3 * cols], buf[:, 3 * cols:].clone()
+    rows, sums = dcr.experts_gather(x.clone(), r), dcr.experts_combine(y.clone(), r)
+    grads = dcr.experts_combine_grad(y.clone(), r, x.clone())
+    assert torch.equal(dcr.experts_gather(x, r, out=out), rows)
+    assert torch.equal(dcr.experts_combine(y, r, out=out[:tokens]), sums)
+    with pytest.raises(dcr.DcrError, match="out overlaps y"):
+        dcr.experts_combine(y, r, out=buf[:tokens, cols + 1:2 * cols + 1])
+    with pytest.raises(dcr.DcrError, match="out overlaps x"):
+        dcr.experts_gather(buf[:, :cols], dcr.Route(*(t[:, :1].contiguous() if t.dim() == 2 else t for t in r))._replace(
+            positions=torch.arange(tokens * k, dtype=torch.int32, device="cuda").view(-1, 1)), out=buf[:, :cols])
+    by_y, by_w = dcr.experts_combine_grad(y, r, x, out=y)
+    assert torch.equal(y, grads[0]) and torch.equal(by_w, grads[1]) and torch.equal(buf[:, 3 * cols:], left)
+    # the weights' gradient in the weights' place
+    w, yy = r.weights.clone(), rows.clone()
+    exp = dcr.experts_combine_grad(yy, r, sums)
+    dcr.check(experts._library().dcr_experts_combine_grad(yy.data_ptr(), 0, tokens * k, cols, cols, r.positions.data_ptr(), w.data_ptr(), tokens, k,
+                                                          sums.data_ptr(), 0, cols, None, cols, w.data_ptr(), torch.cuda.current_stream().cuda_stream))
+    assert torch.equal(w, exp[1])

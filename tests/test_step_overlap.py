@@ -1,0 +1,92 @@
+"""Operands that overlap: which do, against every byte of them, and which calls
+of a step's operators are refused for it (before anything is launched)."""
+import ctypes
+import os
+import random
+import shutil
+import subprocess
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import bit_exact_xor_gb300 as dcr  # noqa: E402
+from bit_exact_xor_gb300 import adamw, experts, scores  # noqa: E402
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_exact_xor_gb300", "csrc")
+SOURCE = """
+#include "overlap.h"
+int dcr::set_error(int code, const char*, ...) { return code; }
+extern "C" int meet(const uint64_t* a, const uint64_t* b)
+{
+    using dcr::Memory;
+    return dcr::overlap(Memory("a", (const void*)a[0], uint32_t(a[1]), a[2], a[3], a[4]), Memory("b", (const void*)b[0], uint32_t(b[1]), b[2], b[3], b[4]));
+}
+"""
+
+
+def _bytes(at, size, rows, cols, stride):
+    return {at + (r * stride + c) * size + b for r in range(rows) for c in range(cols) for b in range(size)} if at else set()
+
+
+def test_overlap_of_matrices(tmp_path):
+    if shutil.which("g++") is None:
+        pytest.skip("needs g++")
+    src, lib = tmp_path / "o.cpp", tmp_path / "o.so"
+    src.write_text(SOURCE)
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-shared", "-fPIC", "-I", CSRC, str(src), "-o", str(lib)], check=True)
+    meet = ctypes.CDLL(str(lib)).meet
+    rng = random.Random(1)
+    seen = [0, 0]
+
+    def one(steps):
+        cols = rng.randint(0, 6)
+        return (rng.choice([0, 1, 1, 1]) * 2 * rng.randint(20, 60), rng.choice([1, 2, 4]), rng.randint(0, 7), cols, max(1, cols, rng.choice(steps)))
+
+    for i in range(20000):
+        steps = [rng.randint(1, 16)] if i % 2 else range(1, 17)
+        a, b = one(steps), one(steps)
+        exp = bool(_bytes(*a) & _bytes(*b))
+        assert bool(meet((ctypes.c_uint64 * 5)(*a), (ctypes.c_uint64 * 5)(*b))) == exp, (a, b)
+        seen[exp] += 1
+    assert min(seen) > 2000, seen
+    far = (4096, 4, 2 ** 31 - 1, 5, 2 ** 40 - 1)        # whose end no address reaches
+    assert meet((ctypes.c_uint64 * 5)(*far), (ctypes.c_uint64 * 5)(4100, 4, 1, 1, 1)) and not meet((ctypes.c_uint64 * 5)(*far), (ctypes.c_uint64 * 5)(4116, 4, 1, 1, 1))
+
+
+M = 1 << 20     # addresses that no refused call reads, far apart
+A = [i * M for i in range(1, 16)]
+
+
+def _refused(rc, why):
+    assert rc == dcr.ERR_INVALID
+    assert why in dcr.last_error(), dcr.last_error()
+
+
+def _gather(x=A[0], cols=8, xs=8, pos=A[1], w=A[2], out=A[3], rows=8, stride=8):
+    return experts._library().dcr_experts_gather(x, 1, 4, cols, xs, pos, 2, w, out, 1, rows, stride, None)
+
+
+def _combine(y=A[0], cols=8, ys=8, pos=A[1], w=A[2], out=A[3], stride=8):
+    return experts._library().dcr_experts_combine(y, 1, 8, cols, ys, pos, w, 4, 2, out, 1, stride, None)
+
+
+def _combine_grad(y=A[0], ys=8, pos=A[1], w=A[2], g=A[3], gs=8, gy=A[4], gys=8, gw=A[5]):
+    return experts._library().dcr_experts_combine_grad(y, 1, 8, 8, ys, pos, w, 4, 2, g, 1, gs, gy, gys, gw, None)
+
+
+@pytest.mark.parametrize("call,kw,why", [
+    (_gather, dict(out=A[0]), "out overlaps x"), (_gather, dict(out=A[0] - 2 * 8 * 8 + 2), "out overlaps x"), (_gather, dict(out=A[0] + 2 * 8 * 4 - 2), "out overlaps x"),
+    # columns of one buffer, the last of the one the first of the other
+    (_gather, dict(xs=15, stride=15, out=A[0] + 14), "out overlaps x"), (_gather, dict(xs=15, stride=15, out=A[0] - 14), "out overlaps x"),
+    (_gather, dict(xs=24, stride=31, out=A[0] + 32), "out overlaps x"),
+    (_gather, dict(out=A[1] + 16), "out overlaps positions"), (_gather, dict(out=A[2] + 16), "out overlaps weights"), (_gather, dict(pos=A[3] + 124), "out overlaps positions"),
+    (_combine, dict(out=A[0]), "out overlaps y"), (_combine, dict(out=A[0] + 126), "out overlaps y"), (_combine, dict(out=A[1] + 28), "out overlaps positions"),
+    (_combine, dict(out=A[2] - 62), "out overlaps weights"),
+    (_combine_grad, dict(gy=A[3]), "grad_y overlaps grad"), (_combine_grad, dict(gy=A[1]), "grad_y overlaps positions"), (_combine_grad, dict(gy=A[2] - 4), "grad_y overlaps weights"),
+    (_combine_grad, dict(gw=A[4] + 124), "grad_y overlaps grad_weights"), (_combine_grad, dict(gw=A[3] - 28), "grad_weights overlaps grad"),
+    (_combine_grad, dict(gw=A[1]), "grad_weights overlaps positions"), (_combine_grad, dict(gw=A[0]), "grad_weights overlaps y"),
+    # in the same place, but not the same rows; and beside it
+    (_combine_grad, dict(gy=A[0], gys=9), "grad_y overlaps y"), (_combine_grad, dict(gy=A[0] + 16), "grad_y overlaps y"), (_combine_grad, dict(gw=A[2] + 4), "grad_weights overlaps weights")])
+def test_exchange(call, kw, why):
+    _refused(call(**kw), why)
