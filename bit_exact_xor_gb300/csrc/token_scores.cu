@@ -795,6 +795,11 @@ extern "C" int dcr_token_scores(const void* logits, uint32_t dtype, uint64_t row
     if (uintptr_t(logp) % 4 || uintptr_t(entropy) % 4 || uintptr_t(top_logp) % 4 || uintptr_t(top_tokens) % 8 || uintptr_t(stats) % 4)
         return set_error(DCR_ERR_INVALID, "dcr_token_scores: misaligned buffer");
     if (rows == 0 || (!logp && !entropy && !stats && !top)) return DCR_OK;
+    if (int rc = check_overlap("dcr_token_scores",
+                               {{"logp", logp, rows * 4}, {"entropy", entropy, rows * 4}, {"stats", stats, rows * 12}, {"top_logp", top_logp, rows * top * 4},
+                                {"top_tokens", top_tokens, rows * top * 8}},
+                               {{"logits", logits, dtype_size(dtype), rows, vocab, row_stride}, {"tokens", tokens, rows * 8}}))
+        return rc;
     ScoreArgs A{logits, rows, vocab, row_stride, tokens, logp, entropy, top_logp, top_tokens, stats, top};
     scales_of(temperature, A.inv_temp, A.sc, &A.sc_dn, &A.sc_lo);
     return with_dtype(dtype, [&](auto t) { return scores_launch<decltype(t)>(A, static_cast<cudaStream_t>(stream)); });
@@ -812,6 +817,10 @@ extern "C" int dcr_token_scores_grad(const void* logits, uint32_t dtype, uint64_
     if (uintptr_t(grad) % dtype_size(dtype) || uintptr_t(stats) % 4 || uintptr_t(grad_logp) % 4 || uintptr_t(grad_entropy) % 4)
         return set_error(DCR_ERR_INVALID, "dcr_token_scores_grad: misaligned buffer");
     if (rows == 0) return DCR_OK;
+    if (int rc = check_overlap("dcr_token_scores_grad", {{"grad", grad, dtype_size(dtype), rows, vocab, grad_stride}},
+                               {{"logits", grad == logits ? nullptr : logits, dtype_size(dtype), rows, vocab, row_stride}, {"tokens", tokens, rows * 8},
+                                {"stats", stats, rows * 12}, {"grad_logp", grad_logp, rows * 4}, {"grad_entropy", grad_entropy, rows * 4}}))
+        return rc;
     GradArgs A{logits, grad, rows, vocab, row_stride, grad_stride, tokens, stats, grad_logp, grad_entropy};
     scales_of(temperature, A.inv_temp, A.sc, nullptr, nullptr);
     const uint64_t words = (vocab * dtype_size(dtype) + 15) / 16 + 1;

@@ -11,6 +11,10 @@
  * valid and launch nothing (no scale is written, but dcr_policy_loss of no rows
  * still writes a loss of 0).  Device buffers belong to the caller; no call
  * keeps an address after it returns, so calls on several streams may overlap.
+ * What a call writes may overlap nothing else that it is given, except where it
+ * says that an output may be one of its inputs, which is then the same memory,
+ * laid out alike.  From dcr_token_scores on other overlaps are refused, matrices
+ * by their rows: columns of one buffer side by side are no overlap.
  *
  * NVFP4.  A matrix [rows, cols] is held as codes [rows, cols / 2] (e2m1, two
  * per byte, the even column in the low nibble), scales [rows, cols / 16]
@@ -202,8 +206,8 @@ int dcr_route(const void* logits, uint32_t dtype, uint64_t tokens, uint32_t expe
 
 /* The gradient by the logits of a loss whose derivative by the weights is
  * grad_weights [tokens, k]; the choice itself and the bias carry none.  grad
- * [tokens, experts] (dtype, rows grad_stride elements apart); opts: scoring,
- * k, renormalise and scale are used. */
+ * [tokens, experts] (dtype, rows grad_stride elements apart) may be logits
+ * itself; opts: scoring, k, renormalise and scale are used. */
 int dcr_route_grad(const void* logits, uint32_t dtype, uint64_t tokens, uint32_t experts, uint64_t row_stride,
                    const int32_t* chosen, const float* grad_weights, const dcr_route_opts* opts, void* grad,
                    uint64_t grad_stride, void* stream);
@@ -212,9 +216,7 @@ int dcr_route_grad(const void* logits, uint32_t dtype, uint64_t tokens, uint32_t
  * j] if weights is not NULL, rounded once.  x [tokens, cols] (x_dtype, rows
  * x_stride elements apart), out (dtype, rows out_stride apart) of `rows` rows;
  * positions [tokens, k] as from dcr_route; one that lies outside [0, rows) is
- * passed over, and rows of out that none names are left as they are.  out may
- * overlap no input: such calls are refused, as they are of every operator from
- * here to the end of this file. */
+ * passed over, and rows of out that none names are left as they are. */
 int dcr_experts_gather(const void* x, uint32_t x_dtype, uint64_t tokens, uint64_t cols, uint64_t x_stride,
                        const int32_t* positions, uint32_t k, const float* weights, void* out, uint32_t dtype,
                        uint64_t rows, uint64_t out_stride, void* stream);

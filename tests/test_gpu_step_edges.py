@@ -167,3 +167,19 @@ def test_exchange_within_one_buffer(cols):
     dcr.check(experts._library().dcr_experts_combine_grad(yy.data_ptr(), 0, tokens * k, cols, cols, r.positions.data_ptr(), w.data_ptr(), tokens, k,
                                                           sums.data_ptr(), 0, cols, None, cols, w.data_ptr(), torch.cuda.current_stream().cuda_stream))
     assert torch.equal(w, exp[1])
+
+
+@pytest.mark.parametrize("vocab", [40, 9001])
+def test_scores_within_one_buffer(vocab):
+    # the gradient, and the outputs, in the columns beside the logits
+    rows = 12
+    z = torch.randn(rows, vocab, generator=torch.Generator().manual_seed(2))
+    tokens, one = torch.arange(rows).cuda(), torch.ones(rows, device="cuda")
+    buf = torch.zeros(rows, 2 * vocab, device="cuda")
+    left, right = buf[:, :vocab], buf[:, vocab:]
+    left.copy_(z)
+    s = dcr.token_scores(left, tokens)
+    exp = dcr.token_scores_grad(left.contiguous(), tokens, s.stats, one, one)
+    assert torch.equal(dcr.token_scores_grad(left, tokens, s.stats, one, one, out=right), exp)
+    with pytest.raises(dcr.DcrError, match="grad overlaps logits"):
+        dcr.token_scores_grad(left, tokens, s.stats, one, one, out=buf[:, 1:vocab + 1])

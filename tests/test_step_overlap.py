@@ -11,7 +11,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import bit_exact_xor_gb300 as dcr  # noqa: E402
-from bit_exact_xor_gb300 import adamw, experts, scores  # noqa: E402
+from bit_exact_xor_gb300 import experts, scores  # noqa: E402
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_exact_xor_gb300", "csrc")
 SOURCE = """
@@ -89,4 +89,25 @@ def _combine_grad(y=A[0], ys=8, pos=A[1], w=A[2], g=A[3], gs=8, gy=A[4], gys=8, 
     # in the same place, but not the same rows; and beside it
     (_combine_grad, dict(gy=A[0], gys=9), "grad_y overlaps y"), (_combine_grad, dict(gy=A[0] + 16), "grad_y overlaps y"), (_combine_grad, dict(gw=A[2] + 4), "grad_weights overlaps weights")])
 def test_exchange(call, kw, why):
+    _refused(call(**kw), why)
+
+
+def _scores(x=A[0], tokens=A[1], logp=A[2], entropy=A[3], tl=A[4], tt=A[5], stats=A[6], vocab=10, stride=10):
+    return scores._library().dcr_token_scores(x, 1, 4, vocab, stride, tokens, 1.0, 2, logp, entropy, tl, tt, stats, None)
+
+
+def _scores_grad(x=A[0], stride=10, tokens=A[1], stats=A[2], gl=A[3], ge=A[4], grad=A[5], gs=10):
+    return scores._library().dcr_token_scores_grad(x, 1, 4, 10, stride, tokens, stats, gl, ge, 1.0, grad, gs, None)
+
+
+@pytest.mark.parametrize("call,kw,why", [
+    (_scores, dict(logp=A[0] + 76), "logp overlaps logits"), (_scores, dict(entropy=A[1] + 28), "entropy overlaps tokens"), (_scores, dict(tl=A[0]), "top_logp overlaps logits"),
+    (_scores, dict(tt=A[1]), "top_tokens overlaps tokens"), (_scores, dict(stats=A[0] - 44), "stats overlaps logits"), (_scores, dict(entropy=A[2]), "logp overlaps entropy"),
+    (_scores, dict(tt=A[4] + 24), "top_logp overlaps top_tokens"), (_scores, dict(stride=12, logp=A[0] + 16), "logp overlaps logits"),
+    # one value or one row further on, and other strides
+    (_scores_grad, dict(grad=A[0] + 2), "grad overlaps logits"), (_scores_grad, dict(grad=A[0] + 20), "grad overlaps logits"),
+    (_scores_grad, dict(grad=A[0] - 2), "grad overlaps logits"), (_scores_grad, dict(stride=20, grad=A[0] + 18, gs=20), "grad overlaps logits"),
+    (_scores_grad, dict(stride=12, grad=A[0] + 4, gs=10), "grad overlaps logits"), (_scores_grad, dict(grad=A[1] + 24), "grad overlaps tokens"),
+    (_scores_grad, dict(grad=A[2] + 44), "grad overlaps stats"), (_scores_grad, dict(grad=A[3]), "grad overlaps grad_logp"), (_scores_grad, dict(grad=A[4]), "grad overlaps grad_entropy")])
+def test_scores(call, kw, why):
     _refused(call(**kw), why)
