@@ -853,6 +853,12 @@ extern "C" int dcr_route(const void* logits, uint32_t dtype, uint64_t tokens, ui
     if (uintptr_t(logits) % dtype_size(dtype) || uintptr_t(bias) % 4 || uintptr_t(chosen) % 4 || uintptr_t(weights) % 4 ||
         uintptr_t(offsets) % 4 || uintptr_t(order) % 4 || uintptr_t(positions) % 4 || uintptr_t(workspace) % 16)
         return set_error(DCR_ERR_INVALID, "dcr_route: misaligned buffer");
+    const uint64_t slots = tokens * o.k;
+    if (int rc = check_overlap("dcr_route",
+                               {{"experts", chosen, slots * 4}, {"weights", weights, slots * 4}, {"offsets", offsets, (experts + 1ull) * 4}, {"order", order, slots * 4},
+                                {"positions", positions, slots * 4}, {"workspace", workspace, DCR_ROUTE_WORKSPACE(experts)}},
+                               {{"logits", logits, dtype_size(dtype), tokens, experts, row_stride}, {"bias", bias, experts * 4ull}, {"mask", mask, tokens}}))
+        return rc;
     RouteArgs A{};
     A.logits = logits, A.bias = bias, A.mask = mask, A.chosen = chosen, A.weights = weights, A.offsets = offsets, A.order = order;
     A.positions = positions, A.counts = static_cast<uint32_t*>(workspace), A.tokens = tokens, A.row_stride = row_stride, A.experts = experts;
@@ -876,6 +882,10 @@ extern "C" int dcr_route_grad(const void* logits, uint32_t dtype, uint64_t token
     if (uintptr_t(logits) % dtype_size(dtype) || uintptr_t(chosen) % 4 || uintptr_t(grad_weights) % 4 || uintptr_t(grad) % dtype_size(dtype))
         return set_error(DCR_ERR_INVALID, "dcr_route_grad: misaligned buffer");
     if (tokens == 0) return DCR_OK;
+    if (int rc = check_overlap("dcr_route_grad", {{"grad", grad, dtype_size(dtype), tokens, experts, grad_stride}},
+                               {{"logits", grad == logits ? nullptr : logits, dtype_size(dtype), tokens, experts, row_stride},
+                                {"experts", chosen, tokens * opts->k * 4}, {"grad_weights", grad_weights, tokens * opts->k * 4}}))
+        return rc;
     const RouteGradArgs A{logits, chosen, grad_weights, grad, tokens, row_stride, grad_stride, experts, opts->k,
                           opts->scoring == DCR_SIGMOID, opts->renormalise != 0, opts->scale};
     const LaunchAttrs at(std::min<uint64_t>((tokens + kThreads / 32 - 1) / (kThreads / 32), 1u << 20), kThreads, 0, 1, false, static_cast<cudaStream_t>(stream));

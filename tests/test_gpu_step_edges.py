@@ -183,3 +183,16 @@ def test_scores_within_one_buffer(vocab):
     assert torch.equal(dcr.token_scores_grad(left, tokens, s.stats, one, one, out=right), exp)
     with pytest.raises(dcr.DcrError, match="grad overlaps logits"):
         dcr.token_scores_grad(left, tokens, s.stats, one, one, out=buf[:, 1:vocab + 1])
+
+
+def test_routing_within_one_buffer():
+    # the router's logits, and their gradient, beside what they are computed from
+    tokens, n = 70, 24
+    buf = torch.randn(tokens, 100 + n, generator=torch.Generator().manual_seed(2)).cuda()
+    z, d = buf[:, 100:], torch.ones(tokens, 4, device="cuda")
+    r, exp = dcr.route_experts(z, 4), dcr.route_experts(z.contiguous(), 4)
+    assert all(torch.equal(a, b) for a, b in zip(r, exp))
+    grad = dcr.route_experts_grad(z, r, d, renormalise=False)
+    assert torch.equal(dcr.route_experts_grad(z, r, d, renormalise=False, out=buf[:, 100 - n:100]), grad)
+    with pytest.raises(dcr.DcrError, match="grad overlaps logits"):
+        dcr.route_experts_grad(z, r, d, out=buf[:, 99:99 + n])

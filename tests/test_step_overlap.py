@@ -111,3 +111,22 @@ def _scores_grad(x=A[0], stride=10, tokens=A[1], stats=A[2], gl=A[3], ge=A[4], g
     (_scores_grad, dict(grad=A[2] + 44), "grad overlaps stats"), (_scores_grad, dict(grad=A[3]), "grad overlaps grad_logp"), (_scores_grad, dict(grad=A[4]), "grad overlaps grad_entropy")])
 def test_scores(call, kw, why):
     _refused(call(**kw), why)
+
+
+def _route(x=A[0], stride=8, bias=A[1], mask=A[2], chosen=A[3], weights=A[4], offsets=A[5], order=A[6], positions=A[7], work=A[8]):
+    o = ctypes.byref(experts._RouteOpts(0, 2, 1, 1, 1, 1, 1.0))
+    return experts._library().dcr_route(x, 1, 4, 8, stride, bias, mask, o, chosen, weights, offsets, order, positions, work, None)
+
+
+def _route_grad(x=A[0], stride=8, chosen=A[1], gw=A[2], grad=A[3], gs=8):
+    return experts._library().dcr_route_grad(x, 1, 4, 8, stride, chosen, gw, ctypes.byref(experts._RouteOpts(0, 2, 1, 1, 1, 1, 1.0)), grad, gs, None)
+
+
+@pytest.mark.parametrize("call,kw,why", [
+    (_route, dict(chosen=A[0] + 60), "experts overlaps logits"), (_route, dict(weights=A[1] + 28), "weights overlaps bias"), (_route, dict(offsets=A[2] - 32), "offsets overlaps mask"),
+    (_route, dict(order=A[0]), "order overlaps logits"), (_route, dict(positions=A[3]), "experts overlaps positions"), (_route, dict(positions=A[6] + 28), "order overlaps positions"),
+    (_route, dict(work=A[5] - 16 * 152 * 2 + 16), "offsets overlaps workspace"), (_route, dict(work=A[0]), "workspace overlaps logits"),
+    (_route_grad, dict(grad=A[0] + 2), "grad overlaps logits"), (_route_grad, dict(grad=A[0] - 16), "grad overlaps logits"),
+    (_route_grad, dict(stride=16, grad=A[0] + 14, gs=16), "grad overlaps logits"), (_route_grad, dict(grad=A[1] + 28), "grad overlaps experts"), (_route_grad, dict(grad=A[2]), "grad overlaps grad_weights")])
+def test_route(call, kw, why):
+    _refused(call(**kw), why)
