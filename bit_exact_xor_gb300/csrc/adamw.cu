@@ -590,12 +590,13 @@ struct Range {
 
 // kinds: the ranges of all weights, of all gradients and so on, each of which
 // a program mostly has in the order of their addresses.
-bool overlapping(std::vector<Range> (&kinds)[7])
+constexpr size_t kKinds = 8;
+bool overlapping(std::vector<Range> (&kinds)[kKinds])
 {
     for (auto& k : kinds)
         if (!std::is_sorted(k.begin(), k.end())) std::sort(k.begin(), k.end());
-    for (size_t step = 1; step < 7; step *= 2)
-        for (size_t i = 0; i + step < 7; i += 2 * step) {
+    for (size_t step = 1; step < kKinds; step *= 2)
+        for (size_t i = 0; i + step < kKinds; i += 2 * step) {
             std::vector<Range> both(kinds[i].size() + kinds[i + step].size());
             std::merge(kinds[i].begin(), kinds[i].end(), kinds[i + step].begin(), kinds[i + step].end(), both.begin());
             kinds[i].swap(both);
@@ -628,6 +629,9 @@ extern "C" int dcr_grad_norm(const dcr_grad* grads, uint32_t count, uint32_t dty
             if (!grads[i].values) return set_error(DCR_ERR_INVALID, "dcr_grad_norm: tensor %u is NULL", i);
             if (uintptr_t(grads[i].values) % dtype_size(dtype)) return set_error(DCR_ERR_INVALID, "dcr_grad_norm: tensor %u is misaligned", i);
             if (grads[i].n >= 1ull << 40) return set_error(DCR_ERR_INVALID, "dcr_grad_norm: tensor %u is too large", i);
+            if (int rc = check_overlap("dcr_grad_norm", {{"norm", norm, 4}, {"workspace", workspace, DCR_NORM_WORKSPACE}},
+                                       {{"a gradient", grads[i].values, grads[i].n * dtype_size(dtype)}}))
+                return rc;
             chunks += (grads[i].n + kNormPer - 1) / kNormPer;
             t.push_back(grads[i]);
         }
@@ -673,9 +677,14 @@ extern "C" int dcr_adamw(const dcr_adamw_tensor* tensors, uint32_t count, uint32
         return set_error(DCR_ERR_INVALID, "dcr_adamw: misaligned buffer");
     try {
         std::vector<dcr_adamw_tensor> t;
-        std::vector<Range> used[7];
+        std::vector<Range> used[kKinds];
         t.reserve(count);
         for (auto& u : used) u.reserve(count);
+        auto use = [&](int kind, const void* p, uint64_t bytes, bool out) { used[kind].push_back(Range{uintptr_t(p), uintptr_t(p) + bytes, out}); };
+        // every block reads these, while others write
+        if (o.norm) use(7, o.norm, 4, false);
+        if (o.device_step) use(7, o.device_step, 8, false);
+        if (o.device_lr) use(7, o.device_lr, 4, false);
         uint64_t chunks = 0;
         for (uint32_t i = 0; i < count; ++i) {
             dcr_adamw_tensor x = tensors[i];
@@ -688,7 +697,6 @@ extern "C" int dcr_adamw(const dcr_adamw_tensor* tensors, uint32_t count, uint32
             if (uintptr_t(x.w) % dtype_size(w_dtype) || uintptr_t(x.grad) % dtype_size(grad_dtype) || uintptr_t(x.copy) % cb ||
                 uintptr_t(x.m) % sb || uintptr_t(x.v) % sb || (sb == 1 && (uintptr_t(x.m_scale) % 4 || uintptr_t(x.v_scale) % 4)))
                 return set_error(DCR_ERR_INVALID, "dcr_adamw: tensor %u is misaligned", i);
-            auto use = [&](int kind, const void* p, uint64_t bytes, bool out) { used[kind].push_back(Range{uintptr_t(p), uintptr_t(p) + bytes, out}); };
             use(0, x.w, x.n * dtype_size(w_dtype), true);
             use(1, x.grad, x.n * dtype_size(grad_dtype), false);
             use(2, x.m, x.n * sb, true);

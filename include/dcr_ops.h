@@ -278,7 +278,7 @@ int dcr_grad_norm(const dcr_grad* grads, uint32_t count, uint32_t dtype, void* w
  * in step's and lr's place, for captured graphs (their factors are formed in
  * 32 bits); the step is the number of
  * this update, from 1, and is not changed.  Tensors that are written may not
- * overlap any other. */
+ * overlap any other, nor norm, device_step or device_lr. */
 typedef struct {
     void* w;
     const void* grad;

@@ -196,3 +196,20 @@ def test_routing_within_one_buffer():
     assert torch.equal(dcr.route_experts_grad(z, r, d, renormalise=False, out=buf[:, 100 - n:100]), grad)
     with pytest.raises(dcr.DcrError, match="grad overlaps logits"):
         dcr.route_experts_grad(z, r, d, out=buf[:, 99:99 + n])
+
+
+def test_update_beside_its_numbers():
+    # the norm, the rate and the step beside the tensors that are written, and the norm of a gradient that is the rate's neighbour
+    n = 64
+    buf = torch.zeros(4 * n + 8, device="cuda")
+    w, m, v, g = (buf[i * n:(i + 1) * n] for i in range(4))
+    norm, lr = buf[4 * n:4 * n + 1], buf[4 * n + 1:4 * n + 2]
+    g.normal_()
+    norm.copy_(dcr.grad_norm([g]))
+    lr.fill_(0.5)
+    dcr.adamw_step([w], [g], [dcr.AdamState32(m, v)], 1, lr, norm=norm, max_norm=1e6)
+    assert bool(((w + 0.5 * torch.sign(g)).abs() < 1e-3).all())
+    before = buf.clone()
+    with pytest.raises(dcr.DcrError, match="overlap"):
+        dcr.adamw_step([w], [g], [dcr.AdamState32(m, v)], 2, lr, norm=v[:1], max_norm=1e6)
+    assert torch.equal(buf, before)

@@ -11,7 +11,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import bit_exact_xor_gb300 as dcr  # noqa: E402
-from bit_exact_xor_gb300 import experts, scores  # noqa: E402
+from bit_exact_xor_gb300 import adamw, experts, scores  # noqa: E402
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_exact_xor_gb300", "csrc")
 SOURCE = """
@@ -129,4 +129,23 @@ def _route_grad(x=A[0], stride=8, chosen=A[1], gw=A[2], grad=A[3], gs=8):
     (_route_grad, dict(grad=A[0] + 2), "grad overlaps logits"), (_route_grad, dict(grad=A[0] - 16), "grad overlaps logits"),
     (_route_grad, dict(stride=16, grad=A[0] + 14, gs=16), "grad overlaps logits"), (_route_grad, dict(grad=A[1] + 28), "grad overlaps experts"), (_route_grad, dict(grad=A[2]), "grad overlaps grad_weights")])
 def test_route(call, kw, why):
+    _refused(call(**kw), why)
+
+
+def _norm(work=A[0], norm=A[1], grads=((A[2], 8), (A[3], 8))):
+    return adamw._library().dcr_grad_norm((adamw._Grad * len(grads))(*grads), len(grads), 1, work, norm, None)
+
+
+def _adamw(**kw):
+    table = (adamw._Tensor * 2)()
+    for i, e in enumerate(table):
+        e.w, e.grad, e.m, e.v, e.n = A[4 * i], A[4 * i + 1], A[4 * i + 2], A[4 * i + 3], 64
+    o = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=1.0, step=1, state_bits=32)
+    return adamw._library().dcr_adamw(table, 2, 0, 1, 3, ctypes.byref(adamw._Opts(**dict(o, **kw))), None)
+
+
+@pytest.mark.parametrize("call,kw,why", [
+    (_norm, dict(norm=A[3] + 12), "norm overlaps a gradient"), (_norm, dict(work=A[2] - 9728 + 8), "workspace overlaps a gradient"), (_norm, dict(norm=A[0] + 9724), "norm overlaps workspace"),
+    (_adamw, dict(norm=A[0] + 252), "overlap"), (_adamw, dict(norm=A[6]), "overlap"), (_adamw, dict(device_lr=A[3] + 4), "overlap"), (_adamw, dict(device_step=A[4] + 248), "overlap")])
+def test_update(call, kw, why):
     _refused(call(**kw), why)
