@@ -629,13 +629,14 @@ extern "C" int dcr_grad_norm(const dcr_grad* grads, uint32_t count, uint32_t dty
             if (!grads[i].values) return set_error(DCR_ERR_INVALID, "dcr_grad_norm: tensor %u is NULL", i);
             if (uintptr_t(grads[i].values) % dtype_size(dtype)) return set_error(DCR_ERR_INVALID, "dcr_grad_norm: tensor %u is misaligned", i);
             if (grads[i].n >= 1ull << 40) return set_error(DCR_ERR_INVALID, "dcr_grad_norm: tensor %u is too large", i);
-            if (int rc = check_overlap("dcr_grad_norm", {{"norm", norm, 4}, {"workspace", workspace, DCR_NORM_WORKSPACE}},
-                                       {{"a gradient", grads[i].values, grads[i].n * dtype_size(dtype)}}))
-                return rc;
             chunks += (grads[i].n + kNormPer - 1) / kNormPer;
             t.push_back(grads[i]);
         }
         if (chunks >= 1ull << 31) return set_error(DCR_ERR_INVALID, "dcr_grad_norm: too large");
+        const Memory out = {"norm", norm, 4}, work = {"workspace", workspace, DCR_NORM_WORKSPACE};
+        if (int rc = check_overlap("dcr_grad_norm", {out, work}, {})) return rc;
+        for (const dcr_grad& g : t)
+            if (int rc = check_overlap("dcr_grad_norm", {out, work}, {{"a gradient", g.values, g.n * dtype_size(dtype)}})) return rc;
         const cudaStream_t s = static_cast<cudaStream_t>(stream);
         double* part = static_cast<double*>(workspace);
         const uint32_t grid = uint32_t(std::min<uint64_t>(std::max<uint64_t>(chunks, 1), kNormBlocks));
