@@ -7,11 +7,12 @@
 // time: the block of values that shares a scale of an 8-bit moment, 8 a lane.
 // The loads of a warp's next values come before the arithmetic on these.
 //
-// Moments in 32 bits are bound by DRAM: 185 million values in 196 tensors (16-bit
-// gradients and copies) in 968 us, 6.7 TB/s of what it moves, and their norm in
-// 78 (4.8 TB/s).  Moments in 8 bits are bound by instruction issue, 80
-// instructions a value, of which a correctly rounded root and quotient are a
-// third: 218 million values in 574 us, 5.1 TB/s (685 without the loads ahead).
+// Moments in 32 bits are bound by DRAM: 235 million values in 195 tensors (16-bit
+// gradients and copies) in 958 us, 6.9 TB/s of what it moves.  Their norm takes
+// 79 (6.0 TB/s): a block has no loads under way between two chunks.  Moments in 8
+// bits are bound by instruction issue, 82 instructions a value, of which a
+// correctly rounded root and quotient are a third: 185 million values in 574 us,
+// 5.1 TB/s (685 without the loads ahead).
 #include <cuda_fp8.h>
 
 #include <algorithm>

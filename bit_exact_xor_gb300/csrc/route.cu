@@ -16,10 +16,11 @@
 // each block adds up the counts of the parts before its own and places its
 // slots (place_kernel).  A small batch takes one block and one launch.
 //
-// Bound by instruction issue, about 1120 instructions a token of 256 experts in
-// groups with a bias (680 without either): 16381 tokens in 29 us, 20 without
-// either, of which placing takes 6; their gradient in 6.4 (its 34 MB
-// are 5).  64 tokens over 64 experts take 8.6 us, most of it one token's chain.
+// Bound by dependent steps: about 1160 instructions a token of 256 experts in
+// groups with a bias (680 without either), issued on two cycles of three by half
+// of the warps that an SM holds: 16381 tokens in 31 us, 21 without either, of
+// which placing takes 6; their gradient in 6.4 (its 34 MB are 5).  64 tokens over
+// 64 experts take 9.2 us, most of it one token's chain.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -682,7 +683,13 @@ __global__ void __launch_bounds__(TH) place_kernel(const RouteArgs A)
     place<TH>(A, A.chosen + begin, begin, end, next, before);
 }
 
-// All of it for a batch of few slots.
+// All of it for a batch of few slots, whose choices fit in shared memory.  The
+// work goes by tokens, though, and one SM has it all: of 8 experts a token out of
+// 64 to 256, one launch takes 6.5 to 7.6 us for 32 tokens, 9.3 to 10.9 for 64 and
+// 15 to 18 for 128, two take 7.7 to 8.6 for 129 and about 9 for 1024.  Two are
+// faster from about 50 tokens on, and a batch of one expert a token, which this
+// bound keeps on one SM up to 1024 tokens, takes 10 to 13 us for 128 and 58 to 76
+// for 1024 (8 for 1025).
 constexpr uint32_t kOneSlots = 1024;
 
 // What routing and then placing take of the shared memory, one after the other.

@@ -738,8 +738,9 @@ int scores_launch(const ScoreArgs& A, uint32_t cluster, cudaStream_t s)
 // SM) or a load's latency, for as many blocks as come one after another on a
 // slot; and in each round the steps at a row's end, which take longer where
 // blocks have to meet.  (4096 rows of 128256 bf16 values, 20 alternatives: 208 us
-// with 128 threads, 214 with 256, before -inf was kept out of the slow sums; 1021 of 32771 f32 values: 35 and 41; 8 rows
-// of 128256 in clusters of eight: 15.4 and 12.0.)  A row of one chunk takes a
+// with 128 threads and 214 with 256, before rows with -inf were kept out of the
+// slow sums, which took the first to 213; 1021 of 32771 f32 values: 35 and 41; 8
+// rows of 128256 in clusters of eight: 15.4 and 12.0.)  A row of one chunk takes a
 // warp, as long as its 32 maxima give a bound (2154 rows of 60, 5
 // alternatives: 27 -> 15 us).
 template <typename T>

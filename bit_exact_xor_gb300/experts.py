@@ -112,7 +112,7 @@ def route_experts_grad(logits, route, grad_weights, scoring="softmax", renormali
     """dcr_route_grad: the gradient by the logits, in their type, of a loss
     whose derivative by route.weights is grad_weights (float32 [tokens, k]).
     scoring, renormalise and scale are those of route_experts; out: a matrix to
-    write to."""
+    write to (logits itself, to save the memory)."""
     if stream is None and out is None:
         r = _fast.route_grad(logits, route.experts, grad_weights, SCORINGS.get(scoring), renormalise, scale)
         if r is not None:
@@ -147,9 +147,9 @@ def _output(out, rows, cols, dtype, dev, same=False):
 
 def experts_gather(x, route, weighted=False, dtype=None, out=None, stream=None):
     """dcr_experts_gather: the rows of x [tokens, cols] in the experts' order,
-    [tokens * k, cols] in `dtype` (default: x's) or into `out`, times
-    route.weights if weighted.  Rows behind the last expert's are left as they
-    are."""
+    [tokens * k, cols] in `dtype` (default: x's) or into `out` (which may
+    overlap nothing that is read), times route.weights if weighted.  Rows behind
+    the last expert's are left as they are."""
     if stream is None:
         r = _fast.gather(x, route.positions, route.weights if weighted else None, DTYPES.get(x.dtype if dtype is None else dtype), out)
         if r is not None:
@@ -172,7 +172,8 @@ def experts_gather(x, route, weighted=False, dtype=None, out=None, stream=None):
 def experts_combine(y, route, weighted=True, dtype=None, out=None, stream=None):
     """dcr_experts_combine: for each token the sum of its rows of y [tokens * k,
     cols], times route.weights if weighted, [tokens, cols] in `dtype` (default:
-    y's) or into `out`.  With weighted=False it is experts_gather's gradient."""
+    y's) or into `out` (which may overlap nothing that is read).  With
+    weighted=False it is experts_gather's gradient."""
     if stream is None:
         r = _fast.combine(y, route.positions, route.weights if weighted else None, DTYPES.get(y.dtype if dtype is None else dtype), out)
         if r is not None:
@@ -196,8 +197,8 @@ def experts_combine(y, route, weighted=True, dtype=None, out=None, stream=None):
 
 def experts_combine_grad(y, route, grad, out=None, stream=None):
     """dcr_experts_combine_grad of experts_combine(y, route): from the gradient
-    of its output, grad [tokens, cols], those by y (in y's type; into `out`;
-    rows behind the last expert's are left as they are) and by route.weights
+    of its output, grad [tokens, cols], those by y (in y's type; into `out`,
+    which may be y itself; rows behind the last expert's are left as they are) and by route.weights
     (float32 [tokens, k])."""
     if stream is None:
         r = _fast.combine_grad(y, route.positions, route.weights, grad, out)
